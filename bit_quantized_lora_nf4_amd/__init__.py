@@ -10,8 +10,16 @@ a gfx950.
     Y, U = linear_fwd(qw, X, A, B, alpha)              # Y = X W'^T + (alpha/r) X A^T B^T
     dX, dA, dB = linear_bwd(qw, dY, X, A, B, alpha, U)
     Wm = lora_merge(qw, A, B, alpha)                   # bf16(W' + (alpha/r) B A)
+
+Training with dropout on the adapter's input (``lora_dropout``): the same calls with a
+``Dropout``; the mask is a function of its seed and offset and is never stored.
+
+    d = Dropout(0.1, seed, offset=step)                # the same d in forward and backward
+    Y, U = linear_fwd(qw, X, A, B, alpha, dropout=d)
+    dX, dA, dB = linear_bwd(qw, dY, X, A, B, alpha, U, dropout=d)
 """
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 from . import _lib
@@ -21,7 +29,9 @@ from ._lib import (QLORA_BF16, QLORA_CONST_DQ_FP8, QLORA_CONST_DQ_INT8, QLORA_CO
                    qlora_linear_fwd, qlora_linear_fwd_fused, qlora_linear_fwd_noalloc, qlora_lora_merge,
                    qlora_lora_unmerge,
                    qlora_nf4_codebook, qlora_nf4_concat_rows, qlora_nf4_sizes, qlora_quantize,
-                   qlora_quantize_nf4, qlora_workspace_bytes, qlora_workspace_bytes_fused)
+                   qlora_quantize_nf4, qlora_workspace_bytes, qlora_workspace_bytes_fused,
+                   qlora_dropout, qlora_linear_bwd_dropout, qlora_linear_fwd_dropout,
+                   qlora_workspace_bytes_dropout)
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "workspace",
            "adamw_step", "lora_merge", "lora_unmerge", "concat_rows", "linear_fwd_fused",
@@ -30,7 +40,8 @@ __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "w
            "qlora_adamw_step", "qlora_lora_merge", "qlora_lora_unmerge", "qlora_linear_fwd_fused",
            "qlora_linear_bwd_fused", "qlora_workspace_bytes_fused", "qlora_nf4_concat_rows",
            "qlora_quantize", "qlora_codebook", "qlora_linear_fwd_noalloc", "linear_fwd_noalloc", "QLORA_QUANT_NF4", "QLORA_QUANT_FP4", "QLORA_CONST_DQ_INT8",
-           "QLORA_CONST_DQ_FP8", "QLORA_CONST_FP32"]
+           "QLORA_CONST_DQ_FP8", "QLORA_CONST_FP32", "Dropout", "dropout", "qlora_dropout",
+           "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_workspace_bytes_dropout"]
 
 
 def _torch():
@@ -63,8 +74,44 @@ class NF4Weight:
         return (self.n_rows, self.n_cols)
 
 
+@dataclass(frozen=True)
+class Dropout:
+    """Dropout of probability ``p`` from a counter-based generator: element e of a
+    row-major tensor is kept or dropped as a function of (seed, offset, e) alone, the kept
+    ones are scaled by 1 / (1 - p) (p to the nearest multiple of 2^-16; see ``qlora_drop``
+    in the C header).  Use another offset for every layer and step, and the same one in
+    forward and backward.  ``counter``: an int64 tensor of one element on the GPU, added to
+    the offset when the kernels run, so that a captured graph whose counter the program
+    advances draws new masks on each replay."""
+    p: float
+    seed: int = 0
+    offset: int = 0
+    counter: "object" = None
+
+    def descriptor(self, device):
+        torch = _torch()
+        if not 0.0 <= self.p < 1.0:
+            raise ValueError(f"dropout probability {self.p} outside [0, 1)")
+        for v, name in ((self.seed, "seed"), (self.offset, "offset")):
+            if not 0 <= v < 1 << 64:
+                raise ValueError(f"dropout {name} {v} is not an unsigned 64-bit integer")
+        if self.counter is not None:
+            _need(self.counter, torch.int64, "counter", device=device)
+            if self.counter.numel() != 1:
+                raise ValueError(f"counter has {self.counter.numel()} elements, expected 1")
+        return _lib.qlora_drop(self.p, self.seed, self.offset, _ptr(self.counter))
+
+
 def _stream(t):
     return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _guard(device):
+    """Make ``device`` the current one for a call (kernels go to the current device)."""
+    torch = _torch()
+    if device.index is None or torch.cuda.current_device() == device.index:
+        return nullcontext()
+    return torch.cuda.device(device)
 
 
 def _ptr(t):
@@ -196,8 +243,11 @@ def workspace(op, M, K, N, r, device):
     return torch.zeros(max(n, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=device)
 
 
-def linear_fwd(qw, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None):
-    """Y = bf16(X W'^T + U_s B^T) with U_s = bf16((alpha/r) X A^T).  Returns (Y, U_s or None)."""
+def linear_fwd(qw, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None, dropout=None):
+    """Y = bf16(X W'^T + U_s B^T) with U_s = bf16((alpha/r) X A^T).  Returns (Y, U_s or None).
+    With ``dropout`` the adapter reads the dropped X (see Dropout)."""
+    if dropout is not None and A is not None:
+        return linear_fwd_fused(qw, 1, X, A, B, alpha, save_u, Y, U, ws, dropout)
     torch = _torch()
     chk = _Args(qw.codes.device)
     K, N = qw.n_cols, qw.n_rows
@@ -248,12 +298,13 @@ def linear_fwd_noalloc(qw, X, Y, A=None, B=None, alpha=16.0, U=None):
 
 
 def linear_bwd(qw, dY, X, A=None, B=None, alpha=16.0, U=None, need_dx=True, dX=None, dA=None,
-               dB=None, ws=None):
-    """(dX, dA, dB) of the QLoRA linear; no gradient for the frozen weight."""
-    return _bwd(qw, 1, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws)
+               dB=None, ws=None, dropout=None):
+    """(dX, dA, dB) of the QLoRA linear; no gradient for the frozen weight.  ``dropout``:
+    the Dropout of the forward call."""
+    return _bwd(qw, 1, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws, dropout)
 
 
-def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws):
+def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws, dropout=None):
     torch = _torch()
     chk = _Args(qw.codes.device)
     K, N = qw.n_cols, qw.n_rows
@@ -274,7 +325,9 @@ def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws):
         chk.need(U, torch.bfloat16, "U", (M, R))
     if need_dx and dX is not None:
         chk.need(dX, torch.bfloat16, "dX", (M, K))
-    nbytes = qlora_workspace_bytes_fused(1, M, K, N, r, parts) if R else 0
+    drop = None if dropout is None or not R else dropout.descriptor(dY.device)
+    need = qlora_workspace_bytes_fused if drop is None else qlora_workspace_bytes_dropout
+    nbytes = need(1, M, K, N, r, parts) if R else 0
     if R:
         if dA is not None:
             chk.need(dA, torch.bfloat16, "dA", (R, K))
@@ -292,6 +345,13 @@ def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws):
             dB = torch.empty((N, r), dtype=torch.bfloat16, device=dev)
         if ws is None:
             ws = torch.zeros(max(nbytes, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=dev)
+    if drop is not None:
+        with _guard(dev):
+            st = qlora_linear_bwd_dropout(qw.descriptor(), parts, dY.data_ptr(), _ptr(X), M, _ptr(A), _ptr(B), r,
+                                          float(alpha), drop, _ptr(U), _ptr(dX) if need_dx else None, _ptr(dA),
+                                          _ptr(dB), _ptr(ws), ws.numel(), _stream(dY))
+        _lib.check(st, "qlora_linear_bwd_dropout")
+        return (dX if need_dx else None), dA, dB
     fn = qlora_linear_bwd_fused if parts > 1 else None
     dxp = _ptr(dX) if need_dx else None
     wsn = 0 if ws is None else ws.numel()
@@ -377,9 +437,11 @@ def concat_rows(qws):
     return out
 
 
-def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None):
+def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None,
+                     dropout=None):
     """Fused forward of n_parts linears sharing X: A [n_parts r, K] and B [N, r] stack the
-    parts' adapters; Y [M, N] holds the parts' outputs side by side."""
+    parts' adapters; Y [M, N] holds the parts' outputs side by side.  ``dropout``: one mask
+    of X for all parts' adapters."""
     torch = _torch()
     chk = _Args(qw.codes.device)
     K, N = qw.n_cols, qw.n_rows
@@ -396,7 +458,9 @@ def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=
         chk.need(Y, torch.bfloat16, "Y", (M, N))
     if r and save_u and U is not None:
         chk.need(U, torch.bfloat16, "U", (M, R))
-    nbytes = qlora_workspace_bytes_fused(0, M, K, N, r, n_parts)
+    drop = None if dropout is None or not R else dropout.descriptor(X.device)
+    need = qlora_workspace_bytes_fused if drop is None else qlora_workspace_bytes_dropout
+    nbytes = need(0, M, K, N, r, n_parts)
     chk.workspace(ws, nbytes)
     chk.devices()
     dev = chk.device
@@ -406,6 +470,13 @@ def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=
         U = torch.empty((M, R), dtype=torch.bfloat16, device=dev)
     if ws is None and nbytes > 0:
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    if drop is not None:
+        with _guard(dev):
+            st = qlora_linear_fwd_dropout(qw.descriptor(), n_parts, X.data_ptr(), M, _ptr(A), _ptr(B), r,
+                                          float(alpha), drop, Y.data_ptr(), _ptr(U) if save_u else None, _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(X))
+        _lib.check(st, "qlora_linear_fwd_dropout")
+        return Y, (U if save_u else None)
     _lib.check(qlora_linear_fwd_fused(qw.descriptor(), n_parts, X.data_ptr(), M, _ptr(A), _ptr(B), r,
                                       float(alpha), Y.data_ptr(), _ptr(U) if save_u else None, _ptr(ws),
                                       0 if ws is None else ws.numel(), _stream(X)),
@@ -414,6 +485,26 @@ def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=
 
 
 def linear_bwd_fused(qw, n_parts, dY, X, A=None, B=None, alpha=16.0, U=None, need_dx=True, dX=None,
-                     dA=None, dB=None, ws=None):
+                     dA=None, dB=None, ws=None, dropout=None):
     """(dX, dA, dB) of the fused linears; dA and dB are stacked like A and B."""
-    return _bwd(qw, n_parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws)
+    return _bwd(qw, n_parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws, dropout)
+
+
+def dropout(X, drop, out=None):
+    """Dropout of X (fp32 or bf16, contiguous) by itself: X / (1 - p) where kept, 0
+    elsewhere, by the Dropout ``drop``.  The backward is the same call on the gradient;
+    ``out=X`` works in place."""
+    torch = _torch()
+    if not isinstance(X, torch.Tensor) or X.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("X must be a float32 or bfloat16 tensor")
+    _need(X, X.dtype, "X")
+    if out is None:
+        out = torch.empty_like(X)
+    _need(out, X.dtype, "out", X.shape, X.device)
+    if X.numel() == 0:
+        return out
+    with _guard(X.device):
+        st = qlora_dropout(X.data_ptr(), QLORA_BF16 if X.dtype == torch.bfloat16 else QLORA_F32, X.numel(),
+                           drop.descriptor(X.device), out.data_ptr(), _stream(X))
+    _lib.check(st, "qlora_dropout")
+    return out

@@ -36,7 +36,8 @@ EXPORTED = (
     "qlora_linear_bwd", "qlora_time_next_gemm", "qlora_adamw_step", "qlora_lora_merge",
     "qlora_lora_unmerge", "qlora_workspace_bytes_fused", "qlora_linear_fwd_fused",
     "qlora_linear_bwd_fused", "qlora_nf4_concat_rows", "qlora_quantize", "qlora_codebook",
-    "qlora_linear_fwd_noalloc",
+    "qlora_linear_fwd_noalloc", "qlora_workspace_bytes_dropout", "qlora_linear_fwd_dropout",
+    "qlora_linear_bwd_dropout", "qlora_dropout",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 QLORA_WORKSPACE_HEADER_BYTES = 65792  # leading workspace bytes that must be zero at first use
@@ -54,6 +55,11 @@ class qlora_nf4_weight(ctypes.Structure):
         ("quant_type", ctypes.c_int32),
         ("const_type", ctypes.c_int32),
     ]
+
+
+class qlora_drop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("counter", ctypes.c_void_p)]
 
 
 _lib = None
@@ -116,6 +122,15 @@ def load(path=LIB_PATH):
     lib.qlora_quantize.restype = I32
     lib.qlora_codebook.argtypes = [I32, ctypes.POINTER(F32), ctypes.POINTER(F32)]
     lib.qlora_codebook.restype = I32
+    D = ctypes.POINTER(qlora_drop)
+    lib.qlora_workspace_bytes_dropout.argtypes = [I32, I64, I64, I64, I32, I32]
+    lib.qlora_workspace_bytes_dropout.restype = SZ
+    lib.qlora_linear_fwd_dropout.argtypes = [W, I32, P, I64, P, P, I32, F32, D, P, P, P, SZ, P]
+    lib.qlora_linear_fwd_dropout.restype = I32
+    lib.qlora_linear_bwd_dropout.argtypes = [W, I32, P, P, I64, P, P, I32, F32, D, P, P, P, P, P, SZ, P]
+    lib.qlora_linear_bwd_dropout.restype = I32
+    lib.qlora_dropout.argtypes = [P, I32, I64, D, P, P]
+    lib.qlora_dropout.restype = I32
     _lib = lib
     return lib
 
@@ -232,3 +247,27 @@ def qlora_nf4_concat_rows(parts, out, stream):
     """parts: a sequence of qlora_nf4_weight descriptors."""
     arr = (qlora_nf4_weight * len(parts))(*parts)
     return load().qlora_nf4_concat_rows(arr, len(parts), ctypes.byref(out), stream)
+
+
+def qlora_workspace_bytes_dropout(op, M, K, N, r, n_parts):
+    return load().qlora_workspace_bytes_dropout(op, M, K, N, r, n_parts)
+
+
+def qlora_linear_fwd_dropout(w, n_parts, X, M, A, B, r, alpha, drop, Y, U_saved, workspace, workspace_bytes,
+                             stream):
+    return load().qlora_linear_fwd_dropout(ctypes.byref(w), n_parts, X, M, A, B, r, alpha, _drop(drop), Y, U_saved,
+                                           workspace, workspace_bytes, stream)
+
+
+def qlora_linear_bwd_dropout(w, n_parts, dY, X, M, A, B, r, alpha, drop, U_saved, dX, dA, dB, workspace,
+                             workspace_bytes, stream):
+    return load().qlora_linear_bwd_dropout(ctypes.byref(w), n_parts, dY, X, M, A, B, r, alpha, _drop(drop), U_saved,
+                                           dX, dA, dB, workspace, workspace_bytes, stream)
+
+
+def qlora_dropout(X, dtype, n, drop, out, stream):
+    return load().qlora_dropout(X, dtype, n, _drop(drop), out, stream)
+
+
+def _drop(drop):
+    return None if drop is None else ctypes.byref(drop)

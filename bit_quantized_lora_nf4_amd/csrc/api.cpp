@@ -373,6 +373,302 @@ int bwd_impl(const char *who, const qlora_nf4_weight *w, int parts, const uint16
   return QLORA_OK;
 }
 
+// ---- dropout ----------------------------------------------------------------
+int check_drop(const char *who, const qlora_drop *drop, qlora::Dropout *d, float *c) {
+  *d = qlora::Dropout{0u, 0u, 0u, 0u, nullptr};
+  *c = 1.0f;
+  if (!drop) return QLORA_OK;
+  if (!(drop->p >= 0.0 && drop->p < 1.0))
+    return fail(QLORA_ERR_VALUE, "%s: drop probability %g outside [0, 1)", who, drop->p);
+  const double t = std::floor(drop->p * 65536.0 + 0.5);
+  if (t > 65535.0)
+    return fail(QLORA_ERR_VALUE, "%s: drop probability %g rounds to 1 (multiples of 2^-16)", who, drop->p);
+  if ((reinterpret_cast<uintptr_t>(drop->counter) & 7u) != 0)
+    return fail(QLORA_ERR_ALIGN, "%s: the dropout counter must be 8-byte aligned", who);
+  *d = qlora::Dropout{static_cast<uint32_t>(t), static_cast<uint32_t>(drop->seed),
+                      static_cast<uint32_t>(drop->seed >> 32), drop->offset, drop->counter};
+  *c = static_cast<float>(65536.0 / (65536.0 - t));
+  return QLORA_OK;
+}
+
+int round8(int r) { return (r + 7) & ~7; }
+int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
+
+// The operators with dropout work on adapters of aligned rank r8 = round_up(r, 8): an
+// unaligned rank is copied into zero-padded A [parts r8, K], B [N, r8] and U [M, parts r8]
+// first, and its results are copied out (a few MB each way; the aligned kernels are many
+// times faster than element-wise ones).
+struct PadLayout {
+  size_t a = 0, b = 0;
+};
+PadLayout pad_layout(size_t &off, int64_t K, int64_t N, int r, int parts) {
+  PadLayout P;
+  if (r % 8 == 0) return P;
+  const size_t r8 = round8(r);
+  P.a = off;
+  off += align_up(size_t(parts) * r8 * K * 2);
+  P.b = off;
+  off += align_up(size_t(N) * r8 * 2);
+  return P;
+}
+qlora::CopyJob pad_a(const uint16_t *A, uint16_t *Ap, int64_t K, int r, int parts) {
+  return {A, Ap, parts, r * K, round8(r) * K, r * K, round8(r) * K};
+}
+qlora::CopyJob pad_rank(const uint16_t *src, uint16_t *dst, int64_t rows, int r) {
+  return {src, dst, rows, r, round8(r), r, round8(r)};
+}
+qlora::CopyJob unpad_a(const uint16_t *Ap, uint16_t *A, int64_t K, int r, int parts) {
+  return {Ap, A, parts, r * K, r * K, round8(r) * K, r * K};
+}
+qlora::CopyJob unpad_rank(const uint16_t *src, uint16_t *dst, int64_t rows, int r) {
+  return {src, dst, rows, r, r, round8(r), r};
+}
+
+struct DropFwdLayout {
+  size_t u = 0, part = 0, total = 0;
+  PadLayout pad;
+};
+DropFwdLayout drop_fwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts) {
+  DropFwdLayout L;
+  if (r == 0) return L;
+  const int R8 = parts * round8(r);
+  size_t off = qlora::kGemvSyncBytes;
+  L.u = off;
+  off += align_up(size_t(M) * R8 * 2);
+  L.part = off;
+  off += align_up(qlora::lora_down_workspace(M, K, R8));
+  L.pad = pad_layout(off, K, N, r, parts);
+  L.total = off;
+  return L;
+}
+
+// dY's padded copy (odd part heights), U [M, R8], V [M, R8], A^T [K, R8], the fp32 partial
+// sums, the padded operands and the padded gradients.
+struct DropBwdLayout {
+  size_t dy = 0, u = 0, v = 0, at = 0, part = 0, part2 = 0, da = 0, db = 0, total = 0;
+  PadLayout pad;
+};
+DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts, bool own_dy) {
+  DropBwdLayout L;
+  const int64_t Np = N / parts, Np8 = round8(Np);
+  const int r8 = round8(r), R8 = parts * r8;
+  size_t off = qlora::kGemvSyncBytes;
+  L.dy = off;
+  if (own_dy) off += align_up(size_t(M) * parts * Np8 * 2);
+  if (r > 0) {
+    L.u = off;
+    off += align_up(size_t(M) * R8 * 2);
+    L.v = off;
+    off += align_up(size_t(M) * R8 * 2);
+    L.at = off;
+    off += align_up(size_t(K) * R8 * 2);
+    L.part = off;
+    size_t p = qlora::reduce_m_workspace(M, K, R8);
+    const size_t others[] = {qlora::lora_down_workspace(M, K, R8), qlora::vdb_workspace_v(M, Np, r8)};
+    for (size_t o : others) p = o > p ? o : p;
+    off += align_up(p);
+    L.part2 = off;
+    off += align_up(qlora::vdb_workspace_db(M, Np, r8));
+    L.pad = pad_layout(off, K, N, r, parts);
+    if (r % 8 != 0) {
+      L.da = off;
+      off += align_up(size_t(R8) * K * 2);
+      L.db = off;
+      off += align_up(size_t(N) * r8 * 2);
+    }
+  }
+  L.total = off;
+  return L;
+}
+
+int check_padded_rank(const char *who, int r, int parts) {
+  if (int64_t(parts) * round8(r) > QLORA_MAX_RANK)
+    return fail(QLORA_ERR_RANK, "%s: %d parts of rank %d, padded to a multiple of 8, exceed %d", who, parts, r,
+                QLORA_MAX_RANK);
+  return QLORA_OK;
+}
+
+int check_workspace(const char *who, const void *workspace, size_t given, size_t need) {
+  if (need == 0) return QLORA_OK;
+  if (!workspace || given < need)
+    return fail(QLORA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need, given);
+  if (!aligned16(workspace)) return fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  return QLORA_OK;
+}
+
+// U = bf16(scale (m X) A^T) [M, R8] into U8 (and U_saved, [M, parts r], when the rank is
+// padded), with the padded operands made first.  A8 and B8 receive the operands to use.
+int drop_down(const uint16_t *X, int64_t M, int64_t K, int64_t N, const uint16_t *A, const uint16_t *B, int r,
+              int parts, float scale, const qlora::Dropout &d, char *ws, const PadLayout &pad, size_t part,
+              uint16_t *U8, const uint16_t **A8, const uint16_t **B8, hipStream_t st) {
+  const int R8 = parts * round8(r);
+  *A8 = A;
+  *B8 = B;
+  if (r % 8 != 0) {
+    uint16_t *Ap = reinterpret_cast<uint16_t *>(ws + pad.a), *Bp = reinterpret_cast<uint16_t *>(ws + pad.b);
+    const qlora::CopyJob jobs[] = {pad_a(A, Ap, K, r, parts), pad_rank(B, Bp, N, r)};
+    const int s = launched(qlora::launch_copy_rows(jobs, 2, st), "pad(A, B)");
+    if (s != QLORA_OK) return s;
+    *A8 = Ap;
+    *B8 = Bp;
+  }
+  if (!U8) return QLORA_OK;
+  float *P = reinterpret_cast<float *>(ws + part);
+  return launched(d.thr ? qlora::launch_lora_down_drop(X, M, K, *A8, R8, scale, U8, P, d, st)
+                        : qlora::launch_lora_down(X, M, K, K, *A8, K, R8, scale, U8, R8, P, st),
+                  "lora_down(U)");
+}
+
+int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, const uint16_t *X, int64_t M,
+                     const uint16_t *A, const uint16_t *B, int r, float alpha, const qlora_drop *drop, uint16_t *Y,
+                     uint16_t *U_saved, void *workspace, size_t workspace_bytes, void *stream) {
+  qlora::Dropout d;
+  float c;
+  int s = check_drop(who, drop, &d, &c);
+  if (s != QLORA_OK) return s;
+  if (d.thr == 0 || r == 0)
+    return fwd_impl(who, w, parts, X, M, A, B, r, alpha, Y, U_saved, workspace, workspace_bytes, stream);
+  s = check_weight(w);
+  if (s == QLORA_OK) s = check_m(M);
+  if (s == QLORA_OK) s = check_rank(r, alpha);
+  if (s == QLORA_OK) s = check_parts(who, w->n_rows, r, parts);
+  if (s == QLORA_OK) s = check_padded_rank(who, r, parts);
+  if (s != QLORA_OK) return s;
+  if (!X || !Y || !A || !B) return fail(QLORA_ERR_NULL, "%s: X, Y, A and B are required", who);
+  const void *ptrs[] = {X, Y, A, B, U_saved};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+  const int64_t K = w->n_cols, N = w->n_rows;
+  const int r8 = round8(r), R8 = parts * r8;
+  const DropFwdLayout L = drop_fwd_layout(M, K, N, r, parts);
+  s = check_workspace(who, workspace, workspace_bytes, L.total);
+  if (s != QLORA_OK) return s;
+  const qlora::WeightView wv = view(w);
+  if (!qlora::gemm_supported(wv, M, R8) || !qlora::drop_shape_ok(M, K, R8))
+    return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
+                (long long)M, (long long)K, (long long)N);
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  const float scale = static_cast<float>(double(alpha) / r * c);
+  uint16_t *U = U_saved && r8 == r ? U_saved : reinterpret_cast<uint16_t *>(ws + L.u);
+  const uint16_t *A8, *B8;
+  s = drop_down(X, M, K, N, A, B, r, parts, scale, d, ws, L.pad, L.part, U, &A8, &B8, st);
+  if (s != QLORA_OK) return s;
+  if (U_saved && U != U_saved) {
+    const qlora::CopyJob job = unpad_rank(U, U_saved, M * parts, r);
+    s = launched(qlora::launch_copy_rows(&job, 1, st), "unpad(U)");
+    if (s != QLORA_OK) return s;
+  }
+  const int64_t part_rows = parts > 1 ? N / parts : 0;
+  return launched(
+      timed_launch(st, [&] { return qlora::launch_gemm_fwd(wv, X, M, U, R8, B8, r8, part_rows, Y, st); }),
+      "gemm_fwd");
+}
+
+// The backward's launches once dY stands in column blocks of ldp columns (ldp = Np, or
+// round_up(Np, 8) with zeros in the padding), row pitch ldy.
+int bwd_blocks(const qlora_nf4_weight *w, int parts, const uint16_t *dY, int64_t ldp, int64_t ldy, const uint16_t *X,
+               int64_t M, const uint16_t *A, const uint16_t *B, int r, float scale, const qlora::Dropout &d,
+               const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB, char *ws, const DropBwdLayout &L,
+               hipStream_t st) {
+  const int64_t K = w->n_cols, N = w->n_rows, Np = N / parts;
+  const int r8 = round8(r), R8 = parts * r8;
+  const qlora::WeightView wv = view(w);
+  int s = QLORA_OK;
+  uint16_t *V = nullptr, *At = nullptr, *dA8 = dA, *dB8 = dB;
+  qlora::FinalizeJob fin{nullptr, 0, 0, 0, 0, 0.0f, nullptr};
+  if (r > 0) {
+    float *part = reinterpret_cast<float *>(ws + L.part), *part2 = reinterpret_cast<float *>(ws + L.part2);
+    V = reinterpret_cast<uint16_t *>(ws + L.v);
+    At = reinterpret_cast<uint16_t *>(ws + L.at);
+    const uint16_t *A8, *B8, *U = U_saved;
+    uint16_t *Uw = reinterpret_cast<uint16_t *>(ws + L.u);
+    s = drop_down(X, M, K, N, A, B, r, parts, scale, d, ws, L.pad, L.part, U_saved ? nullptr : Uw, &A8, &B8, st);
+    if (s != QLORA_OK) return s;
+    if (!U_saved) {
+      U = Uw;
+    } else if (r8 != r) {
+      const qlora::CopyJob job = pad_rank(U_saved, Uw, M * parts, r);
+      s = launched(qlora::launch_copy_rows(&job, 1, st), "pad(U)");
+      if (s != QLORA_OK) return s;
+      U = Uw;
+    }
+    if (r8 != r) {
+      dA8 = reinterpret_cast<uint16_t *>(ws + L.da);
+      dB8 = reinterpret_cast<uint16_t *>(ws + L.db);
+    }
+    for (int q = 0; q < parts && s == QLORA_OK; ++q) {
+      const bool at = dX && q == 0;
+      s = launched(qlora::launch_vdb(dY + q * ldp, M, Np, ldy, B8 + q * Np * r8, U + q * r8, R8, r8, scale, V + q * r8,
+                                     dB8 + q * Np * r8, part, part2, at ? A8 : nullptr, R8, K, at ? At : nullptr, st,
+                                     ldp != Np),
+                   "lora(V, dB)");
+    }
+    if (s == QLORA_OK)
+      s = launched(d.thr ? qlora::launch_reduce_m_drop(X, M, K, V, R8, part, dA8, d, st, dX ? &fin : nullptr)
+                         : qlora::launch_reduce_m(X, M, K, K, V, R8, R8, part, dA8, true, st, dX ? &fin : nullptr),
+                   "reduce(dA)");
+    if (s != QLORA_OK) return s;
+  }
+  if (dX)
+    s = launched(
+        timed_launch(st, [&] { return qlora::launch_gemm_dx_ext(wv, dY, M, parts, V, At, R8, dX, d, st, &fin); }),
+        "gemm_dx");
+  if (s == QLORA_OK && r8 != r) {
+    const qlora::CopyJob jobs[] = {unpad_a(dA8, dA, K, r, parts), unpad_rank(dB8, dB, N, r)};
+    s = launched(qlora::launch_copy_rows(jobs, 2, st), "unpad(dA, dB)");
+  }
+  return s;
+}
+
+int bwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, const uint16_t *dY, const uint16_t *X,
+                     int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha, const qlora_drop *drop,
+                     const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  qlora::Dropout d;
+  float c;
+  int s = check_drop(who, drop, &d, &c);
+  if (s != QLORA_OK) return s;
+  if (d.thr == 0 || r == 0)
+    return bwd_impl(who, w, parts, dY, X, M, A, B, r, alpha, U_saved, dX, dA, dB, workspace, workspace_bytes, stream);
+  s = check_weight(w);
+  if (s == QLORA_OK) s = check_m(M);
+  if (s == QLORA_OK) s = check_rank(r, alpha);
+  if (s == QLORA_OK) s = check_parts(who, w->n_rows, r, parts);
+  if (s == QLORA_OK) s = check_padded_rank(who, r, parts);
+  if (s != QLORA_OK) return s;
+  if (!dY || !A || !B || !X || !dA || !dB)
+    return fail(QLORA_ERR_NULL, "%s: dY, X, A, B, dA and dB are required", who);
+  const void *ptrs[] = {dY, X, A, B, U_saved, dX, dA, dB};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+  const int64_t K = w->n_cols, N = w->n_rows, Np = N / parts, ldp = round8(Np);
+  const int r8 = round8(r), R8 = parts * r8;
+  const bool copy = ldp != Np;  // one part (several have multiples of 256 rows)
+  const DropBwdLayout L = drop_bwd_layout(M, K, N, r, parts, copy);
+  s = check_workspace(who, workspace, workspace_bytes, L.total);
+  if (s != QLORA_OK) return s;
+  if (!qlora::gemm_supported(view(w), M, R8) || !qlora::drop_shape_ok(M, K, R8) ||
+      uint64_t(M) * ldp * parts * 2 > 0xFFFFFFF0ull || !qlora::vdb_fast(M, Np, ldp * parts, R8, r8, copy))
+    return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
+                (long long)M, (long long)K, (long long)N);
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  if (copy) {
+    uint16_t *dYp = reinterpret_cast<uint16_t *>(ws + L.dy);
+    const qlora::CopyJob job{dY, dYp, M, Np, ldp, Np, ldp};
+    s = launched(qlora::launch_copy_rows(&job, 1, st), "pad(dY)");
+    if (s != QLORA_OK) return s;
+    dY = dYp;
+  }
+  const float scale = static_cast<float>(double(alpha) / r * c);
+  return bwd_blocks(w, parts, dY, ldp, ldp * parts, X, M, A, B, r, scale, d, U_saved, dX, dA, dB, ws, L, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -518,6 +814,47 @@ int qlora_linear_bwd_fused(const qlora_nf4_weight *w, int n_parts, const uint16_
                            void *workspace, size_t workspace_bytes, void *stream) {
   return bwd_impl("linear_bwd_fused", w, n_parts, dY, X, M, A, B, r, alpha, U_saved, dX, dA, dB,
                   workspace, workspace_bytes, stream);
+}
+
+size_t qlora_workspace_bytes_dropout(int op, int64_t M, int64_t K, int64_t N, int r, int n_parts) {
+  const size_t base = qlora_workspace_bytes_fused(op, M, K, N, r, n_parts);
+  if ((op != 0 && op != 1) || M < 1 || K < 1 || N < 1 || K % 64 != 0 || r < 1 || n_parts < 1 ||
+      n_parts > QLORA_MAX_PARTS || N % n_parts != 0 || int64_t(n_parts) * round8(r) > QLORA_MAX_RANK)
+    return base;
+  const size_t need = op == 0 ? drop_fwd_layout(M, K, N, r, n_parts).total
+                              : drop_bwd_layout(M, K, N, r, n_parts, (N / n_parts) % 8 != 0).total;
+  return need > base ? need : base;
+}
+
+int qlora_linear_fwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *X, int64_t M,
+                             const uint16_t *A, const uint16_t *B, int r, float alpha, const qlora_drop *drop,
+                             uint16_t *Y, uint16_t *U_saved, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+  return fwd_dropout_impl("linear_fwd_dropout", w, n_parts, X, M, A, B, r, alpha, drop, Y, U_saved, workspace,
+                          workspace_bytes, stream);
+}
+
+int qlora_linear_bwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *dY, const uint16_t *X,
+                             int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha,
+                             const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA,
+                             uint16_t *dB, void *workspace, size_t workspace_bytes, void *stream) {
+  return bwd_dropout_impl("linear_bwd_dropout", w, n_parts, dY, X, M, A, B, r, alpha, drop, U_saved, dX, dA, dB,
+                          workspace, workspace_bytes, stream);
+}
+
+int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, void *out, void *stream) {
+  if (!X || !out || !drop) return fail(QLORA_ERR_NULL, "dropout: X, drop and out are required");
+  if (dtype != QLORA_F32 && dtype != QLORA_BF16)
+    return fail(QLORA_ERR_DTYPE, "dropout: dtype %d: expected QLORA_F32 or QLORA_BF16", dtype);
+  if (n < 1 || n > kMaxDim) return fail(QLORA_ERR_SHAPE, "dropout: n = %lld", (long long)n);
+  if (!aligned16(X) || !aligned16(out)) return fail(QLORA_ERR_ALIGN, "dropout: X and out must be 16-byte aligned");
+  qlora::Dropout d;
+  float c;
+  int s = check_drop("dropout", drop, &d, &c);
+  if (s == QLORA_OK) s = check_device();
+  if (s != QLORA_OK) return s;
+  return launched(qlora::launch_dropout(X, dtype == QLORA_BF16, n, d, c, out, static_cast<hipStream_t>(stream)),
+                  "dropout");
 }
 
 int qlora_nf4_concat_rows(const qlora_nf4_weight *parts, int n_parts, const qlora_nf4_weight *out,

@@ -254,6 +254,51 @@ __device__ __forceinline__ u32x4_t lookup8(uint32_t w, const Planes &P) {
   return r;
 }
 
+// ---- counter-based dropout ------------------------------------------------------------
+// Element e of a row-major tensor belongs to group g = e / 8.  The eight elements of a
+// group share one Philox4x32-7 block (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011; seven rounds are the fewest of that paper that pass
+// its test batteries): counter (g, offset) as two 64-bit words, key = the seed.  Element j
+// of the group takes 16 bits, word j / 2, the low half for even j, and is kept when they
+// are >= thr.  16 bits an element make one block serve a 16-byte bf16 load; the drop
+// probability is then a multiple of 2^-16 and the caller's 1 / (1 - p) uses that multiple.
+struct DropKey {
+  uint32_t k0, k1, o0, o1, thr;
+};
+__device__ __forceinline__ DropKey drop_key(const Dropout &d) {
+  const uint64_t o = d.offset + (d.counter ? *d.counter : 0ull);
+  return {d.k0, d.k1, static_cast<uint32_t>(o), static_cast<uint32_t>(o >> 32), d.thr};
+}
+__device__ __forceinline__ u32x4_t drop_words(uint32_t g_lo, uint32_t g_hi, const DropKey &d) {
+  uint32_t c0 = g_lo, c1 = g_hi, c2 = d.o0, c3 = d.o1, k0 = d.k0, k1 = d.k1;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4_t{c0, c1, c2, c3};
+}
+// All-ones 16-bit halves where the element is kept (thr >= 1): w >= thr exactly when the
+// saturating difference w - (thr - 1) is not zero.
+__device__ __forceinline__ u32x4_t drop_mask(u32x4_t w, uint32_t thr) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  const u16x2_t t = {static_cast<uint16_t>(thr - 1), static_cast<uint16_t>(thr - 1)};
+  const u16x2_t one = {1, 1}, zero = {0, 0};
+  u32x4_t m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t wi = w[i];  // (a bit cast of the element itself would read the vector's first one)
+    const u16x2_t k = __builtin_elementwise_min(__builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2_t, wi), t), one);
+    m[i] = __builtin_bit_cast(uint32_t, zero - k);
+  }
+  return m;
+}
+
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));

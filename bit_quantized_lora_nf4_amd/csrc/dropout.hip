@@ -1,0 +1,126 @@
+// Dropout from a counter-based generator (gfx950) and the row copies that bring operands
+// of unaligned row length into 16-byte rows.
+//
+//   out[e] = m[e] c x[e],  c = 1 / (1 - p),  m a function of (seed, offset, e)
+//
+// (lora_dropout of the adapter configuration, [Repro] "官方代码阅读路线".)  No mask is
+// stored: the backward of the operator is the operator itself with the same seed and
+// offset.  A thread takes whole groups of eight elements, one generator block each
+// (drop_words in device_common.h): 16-byte accesses for bf16, two of them for fp32.  The
+// kernel is bound by memory: a block costs about 14 32x32-bit products for 32 bytes moved
+// (bf16).
+
+#include "device_common.h"
+#include "qlora_internal.h"
+
+namespace qlora {
+namespace {
+
+constexpr int NT = 256;
+
+template <bool BF16>
+__global__ __launch_bounds__(NT) void dropout_kernel(const void *X, int64_t n, Dropout d, float c, void *out) {
+  const DropKey dk = drop_key(d);
+  const int64_t groups = n / 8, stride = static_cast<int64_t>(gridDim.x) * NT;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
+  for (int64_t g = t0; g < groups; g += stride) {
+    const u32x4_t w = drop_words(static_cast<uint32_t>(g), static_cast<uint32_t>(g >> 32), dk);
+    if constexpr (BF16) {
+      const u32x4_t x = reinterpret_cast<const u32x4_t *>(X)[g];
+      const u32x4_t m = drop_mask(w, dk.thr);
+      u32x4_t y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = pack_bf16x2(bf16_lo(x[i]) * c, bf16_hi(x[i]) * c) & m[i];
+      reinterpret_cast<u32x4_t *>(out)[g] = y;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t x = reinterpret_cast<const f32x4_t *>(X)[2 * g + h];
+        f32x4_t y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = w[2 * h + i / 2];
+          y[i] = ((i & 1) ? v >> 16 : v & 0xFFFFu) >= dk.thr ? x[i] * c : 0.0f;
+        }
+        reinterpret_cast<f32x4_t *>(out)[2 * g + h] = y;
+      }
+    }
+  }
+  // the last n % 8 elements
+  const int64_t e = 8 * groups + t0;
+  if (t0 < 8 && e < n) {
+    const u32x4_t w = drop_words(static_cast<uint32_t>(groups), static_cast<uint32_t>(groups >> 32), dk);
+    const uint32_t v = t0 < 2 ? w[0] : t0 < 4 ? w[1] : t0 < 6 ? w[2] : w[3];
+    const bool keep = ((t0 & 1) ? v >> 16 : v & 0xFFFFu) >= dk.thr;
+    if constexpr (BF16) {
+      const float x = bf16_to_f32(static_cast<const uint16_t *>(X)[e]);
+      static_cast<uint16_t *>(out)[e] = keep ? to_bf16(x * c) : static_cast<uint16_t>(0);
+    } else {
+      const float x = static_cast<const float *>(X)[e];
+      static_cast<float *>(out)[e] = keep ? x * c : 0.0f;
+    }
+  }
+}
+
+// Row copies with zero padding (CopyJob): a workgroup row of the grid per job, a wave per
+// row of the job, lanes along the row.  The jobs are adapter operands of unaligned rank
+// (a few MB) or a gradient of odd width; both sides may be unaligned, so the accesses are
+// two bytes a lane, 128 contiguous bytes a wave.
+struct CopyJobs {
+  CopyJob j[kMaxCopyJobs];
+};
+__global__ __launch_bounds__(NT) void copy_rows_kernel(CopyJobs jobs) {
+  const CopyJob jb = jobs.j[blockIdx.y];
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = static_cast<int64_t>(blockIdx.x) * (NT / 64) + (threadIdx.x >> 6);
+  const int64_t waves = static_cast<int64_t>(gridDim.x) * (NT / 64);
+  // rows longer than 2048 columns are split, so that few long rows spread too
+  const int64_t seg = 2048, segs = (jb.dcols + seg - 1) / seg;
+  for (int64_t i = wave; i < jb.rows * segs; i += waves) {
+    const int64_t row = i / segs, c0 = (i % segs) * seg;
+    const int64_t c1 = c0 + seg < jb.dcols ? c0 + seg : jb.dcols;
+    for (int64_t c = c0 + lane; c < c1; c += 64)
+      jb.dst[row * jb.ldd + c] = c < jb.cols ? jb.src[row * jb.lds + c] : static_cast<uint16_t>(0);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const void *X, bool bf16, int64_t n, const Dropout &d, float c, void *out,
+                          hipStream_t stream) {
+  if (d.thr == 0) {
+    if (X == out) return hipSuccess;
+    return hipMemcpyAsync(out, X, static_cast<size_t>(n) * (bf16 ? 2 : 4), hipMemcpyDeviceToDevice, stream);
+  }
+  int64_t blocks = (n / 8 + NT - 1) / NT;
+  if (blocks > 256 * 16) blocks = 256 * 16;
+  if (blocks < 1) blocks = 1;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
+  if (bf16)
+    hipLaunchKernelGGL(dropout_kernel<true>, grid, block, 0, stream, X, n, d, c, out);
+  else
+    hipLaunchKernelGGL(dropout_kernel<false>, grid, block, 0, stream, X, n, d, c, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_copy_rows(const CopyJob *jobs, int n, hipStream_t stream) {
+  CopyJobs a;
+  int used = 0;
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    if (jobs[i].rows <= 0) continue;
+    if (used == kMaxCopyJobs) return hipErrorInvalidValue;
+    a.j[used++] = jobs[i];
+    const int64_t units = jobs[i].rows * ((jobs[i].dcols + 2047) / 2048);
+    most = units > most ? units : most;
+  }
+  if (used == 0) return hipSuccess;
+  for (int i = used; i < kMaxCopyJobs; ++i) a.j[i] = CopyJob{nullptr, nullptr, 0, 0, 0, 0, 0};
+  int64_t blocks = (most + 3) / 4;
+  if (blocks > 2048) blocks = 2048;
+  hipLaunchKernelGGL(copy_rows_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(used)), dim3(NT), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

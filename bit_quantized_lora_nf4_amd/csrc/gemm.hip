@@ -67,6 +67,15 @@ struct GemmParams {
   FinalizeJob fin;
 };
 
+// The dX GEMM's extension (launch_gemm_dx_ext): the dropout mask of the LoRA term, and dY
+// in column blocks of `half` columns of which the last `skip` are padding: contraction
+// position k stands for weight row k - skip floor(k / half) where k % half < half - skip.
+// Only two blocks or none (half = the whole contraction) are needed.
+struct DxExt {
+  Dropout drop;
+  int half, skip;
+};
+
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // byte offset of 16-byte chunk c of row `row` in a swizzled 256 x 64 bf16 tile
@@ -837,15 +846,66 @@ __device__ __forceinline__ void dx_schedule() {
 // holds the four waves' slices.
 constexpr int YWAVE_BYTES = 64 * TK * 2;
 
-template <int CT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_pipe_kernel(
-    GemmParams p) {
-  // two weight tiles and two dY stages, 128 KB; separate objects, so that the
-  // compiler can tell reads of one stage or tile from the loads into the other stage
-  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
+// The dropout mask of X on the LoRA term of dX (acc[i][j]: tokens tb + 32 i + l % 32,
+// output columns cb + 32 j + 8 g + 4 (l / 32) + 0..3): the eight columns of a generator
+// group are held by lanes l and l + 32, four each.  Of each pair of groups the lower half
+// makes the first one's block and the upper half the second one's; a half-wave swap of two
+// word pairs then gives every lane the two words of its own elements of both groups.
+// keep_bits packs a lane's keep decisions, element e of acc[i][j] in bit 16 (j % 2) + e of
+// word [i][j / 2], so that the generator runs while the first tiles' loads are in flight;
+// mask_lora applies them.
+__device__ __forceinline__ void keep_bits(const DropKey &dk, int tb, int cb, int K, uint32_t (&keep)[4][2]) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t top = dk.thr << 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t row = static_cast<uint32_t>(tb + 32 * i + (lane & 31)) * static_cast<uint32_t>(K / 8);
+#pragma unroll
+    for (int jp = 0; jp < 2; ++jp) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // groups 2 q and 2 q + 1 of the eight of two column tiles
+        const u32x4_t w = drop_words(row + (cb + 64 * jp + 16 * q) / 8 + (lane >> 5), 0u, dk);
+        const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t v[2] = {g ? lo[1] : lo[0], g ? hi[1] : hi[0]};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t h = (e & 1) ? v[e / 2] : v[e / 2] << 16;  // the element's bits on top
+            bits |= h >= top ? 1u << (8 * q + 4 * g + e) : 0u;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
+      }
+      keep[i][jp] = bits;
+    }
+  }
+}
+__device__ __forceinline__ void mask_lora(const uint32_t (&keep)[4][2], f32x16_t (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x16_t t = acc[i][j];
+      asm volatile("" : "+a"(t));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int m = static_cast<int>(keep[i][j >> 1] << (31 - (16 * (j & 1) + e))) >> 31;
+        t[e] = __uint_as_float(__float_as_uint(t[e]) & static_cast<uint32_t>(m));
+      }
+      // back in the accumulation registers tile by tile (left to itself the compiler
+      // carries all the tiles in the other half of the register file and spills)
+      asm volatile("" : "+a"(t));
+      acc[i][j] = t;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int CT, bool EXT>
+__device__ __forceinline__ void dx_pipe_body(const GemmParams &p, const DxExt &x, char *sW0, char *sW1, char *sY0,
+                                             char *sY1) {
   // the workgroups after the tiles (dispatched last, so in CUs the tiles have left) do
   // the finalize job that rides in this launch
   if (static_cast<int>(blockIdx.x) >= p.tiles) {
@@ -862,10 +922,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
   const int m0 = tmi * TM, k0 = tni * TN;
 
-  const int N = p.Kc, K = p.No;  // contraction over weight rows, outputs are weight columns
+  // contraction over weight rows (EXT: over the padded column blocks of dY that stand for
+  // them), outputs are weight columns
+  const int N = p.Kc, K = p.No, NW = EXT ? static_cast<int>(p.w.n_rows) : N;
   const __amdgpu_buffer_rsrc_t rdy = make_rsrc(p.A, static_cast<uint32_t>(uint64_t(p.M) * N * 2));
-  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.w.codes, static_cast<uint32_t>(uint64_t(N) * K / 2));
-  const ConstRsrc rq = make_const_rsrc<CT>(p.w, static_cast<uint32_t>(uint64_t(N) * K / 64));
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.w.codes, static_cast<uint32_t>(uint64_t(NW) * K / 2));
+  const ConstRsrc rq = make_const_rsrc<CT>(p.w, static_cast<uint32_t>(uint64_t(NW) * K / 64));
   const int nk = (N + TK - 1) / TK;
   const int last = nk - 1;
 
@@ -916,8 +978,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   const int dn = tid & 63, dc = (tid >> 6) * 64;
   const bool col_ok = k0 + dc < K;
   auto issue_codes = [&](int kt, CodeStageB &cs) {
-    const int n = kt + dn;
-    const bool ok = col_ok && n < N;
+    int n = kt + dn;
+    bool ok = col_ok && n < N;
+    if constexpr (EXT) {
+      const int nb = n < x.half ? n : n - x.half;  // position within its column block
+      ok = ok && nb < x.half - x.skip;
+      n = n < x.half ? n : n - x.skip;
+    }
     const uint32_t off = static_cast<uint32_t>(n) * (K / 2) + (k0 + dc) / 2;
     cs.code[0] = buf_load16(rc, ok ? off : kOOB);
     cs.code[1] = buf_load16(rc, ok ? off + 16 : kOOB);
@@ -970,6 +1037,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   } else if (p.r > 0) {
     lora_steps_dx(p, m0 + 128 * wr, k0 + 128 * wc, acc);
   }
+  uint32_t keep[4][2];
+  if constexpr (EXT) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep[i][0] = keep[i][1] = ~0u;
+    if (x.drop.thr != 0) keep_bits(drop_key(x.drop), m0 + 128 * wr, k0 + 128 * wc, K, keep);
+  }
   {
     const Planes pd = make_planes(const_value<CT>(S0.c), p.lvl);
     decode_part(S0, pd, sW0, 0, 8);
@@ -989,6 +1062,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
       }
     }
     __syncthreads();  // no wave reads the V tile any more when step 0 loads dY step 1 there
+  }
+  if constexpr (EXT) {
+    mask_lora(keep, acc);
   }
 
   u32x4_t wa[4], yb[4];
@@ -1082,6 +1158,27 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   }
 }
 
+template <int CT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_pipe_kernel(
+    GemmParams p) {
+  // two weight tiles and two dY stages, 128 KB; separate objects, so that the
+  // compiler can tell reads of one stage or tile from the loads into the other stage
+  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
+  dx_pipe_body<CT, false>(p, DxExt{}, sW0, sW1, sY0, sY1);
+}
+template <int CT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_ext_kernel(
+    GemmParams p, DxExt x) {
+  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
+  dx_pipe_body<CT, true>(p, x, sW0, sW1, sY0, sY1);
+}
+
 bool fits_32bit(int64_t M, int64_t N, int64_t K, int r) {
   const uint64_t lim = 0xFFFFFFF0ull;
   return uint64_t(M) * K * 2 <= lim && uint64_t(M) * N * 2 <= lim && uint64_t(N) * K / 2 <= lim &&
@@ -1150,6 +1247,30 @@ hipError_t launch_gemm_dx(const WeightView &w, const uint16_t *dY, int64_t M, co
     case kConstF32: return go(gemm_dx_pipe_kernel<kConstF32>, gemm_dx_kernel<false, kConstF32>);
     default: return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M, int parts, const uint16_t *V,
+                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, hipStream_t stream,
+                              const FinalizeJob *fin) {
+  const int64_t Np = w.n_rows / parts, half = (Np + 7) / 8 * 8, Kc = parts > 1 ? parts * half : half;
+  if (w.n_rows % parts != 0 || (parts > 2 && half != Np)) return hipErrorInvalidValue;
+  if (!fits_32bit(M, Kc, w.n_cols, r) || M > 0x7fffffff) return hipErrorInvalidValue;
+  GemmParams p = make_params(dY, w, V, At, dX, M, w.n_cols, Kc, r);
+  if (fin && fin->splits > 0) {
+    p.fin = *fin;
+    p.fin_wgs = static_cast<int>(finalize_workgroups(*fin));
+  }
+  if (int64_t(p.tiles) + p.fin_wgs > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(p.tiles + p.fin_wgs));
+  // without padding the column blocks are the contraction as it is
+  const DxExt x{d, static_cast<int>(half == Np ? Kc : half), static_cast<int>(half - Np)};
+  switch (w.const_type) {
+    case kConstDqInt8: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstDqInt8>, grid, dim3(NT), 0, stream, p, x); break;
+    case kConstDqFp8: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstDqFp8>, grid, dim3(NT), 0, stream, p, x); break;
+    case kConstF32: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstF32>, grid, dim3(NT), 0, stream, p, x); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
 }
 
 }  // namespace qlora

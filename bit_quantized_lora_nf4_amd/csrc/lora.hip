@@ -121,14 +121,37 @@ __device__ __forceinline__ void store_partials(char *sbuf, const f32x16_t (&acc)
   }
 }
 
+// The masked step of the DROP bodies: the generator blocks of this lane's two chunks (at
+// byte 0 and 4096 from `own`; groups g[u] + dg) while their loads are in flight, the wait
+// that leaves INFLIGHT later loads, the chunks read, masked and written back, and the
+// barrier that publishes them.
+template <int INFLIGHT>
+__device__ __forceinline__ void drop_own_chunks(char *own, const uint32_t (&g)[2], uint32_t dg, const DropKey &dk) {
+  u32x4_t m[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) m[u] = drop_mask(drop_words(g[u] + dg, 0u, dk), dk.thr);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(m[u]));  // made before the wait
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(INFLIGHT) : "memory");
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    u32x4_t *const c = reinterpret_cast<u32x4_t *>(own + 4096 * u);
+    *c = *c & m[u];
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // BK: the adapter operand is given as B [Kc, r] (rows of the contraction, row pitch
 // ldwt) instead of WT [r, Kc]; its step tile (64 contraction rows of r ranks) is staged
 // row-major like reduce_m's S tile and read with the transposing LDS read, so the
 // product V = dY B needs no transposed copy of B.
-template <int RT, int NB, bool BK = false>
+// DROP: IN is dense and carries the dropout mask.  Every lane clears the dropped elements
+// of the two 16-byte IN chunks it loaded (one generator block each) in LDS once they have
+// landed, before the barrier that publishes the step.
+template <int RT, int NB, bool BK = false, bool DROP = false>
 __device__ __forceinline__ void lora_down_dma_body(
     char *sbuf, int bx, int by, const uint16_t *__restrict__ IN, int M, int Kc, int ldin,
-    const uint16_t *__restrict__ WT, int ldwt, int r, int KR, float *__restrict__ P) {
+    const uint16_t *__restrict__ WT, int ldwt, int r, int KR, float *__restrict__ P, const Dropout &drop = Dropout{}) {
   constexpr int ROWS = 64 + 32 * RT;       // staged rows per step (IN then WT)
   constexpr int BUF = ROWS * 128;          // bytes per buffer
   constexpr int NLD = ROWS / 8;            // 1 KB loads per step
@@ -190,11 +213,24 @@ __device__ __forceinline__ void lora_down_dma_body(
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[u][e] = 0.0f;
 
+  DropKey dk{};
+  uint32_t dgrp[2] = {0u, 0u};  // generator groups of this lane's IN chunks at step 0
+  if constexpr (DROP) {
+    dk = drop_key(drop);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      dgrp[u] = static_cast<uint32_t>(m0 + 8 * (wave + 4 * u) + (lane >> 3)) * (Kc / 8) + kbeg / 8 + chk[u];
+  }
+
 #pragma unroll
   for (int s = 0; s < NB - 1; ++s) dma(s);
   for (int i = 0; i < nsteps; ++i) {
     // step i has landed for every wave, and no wave still reads buffer (i - 1) % NB
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * LPW) : "memory");
+    if constexpr (DROP) {
+      drop_own_chunks<(NB - 2) * LPW>(sbuf + (i % NB) * BUF + wave * 1024 + lane * 16, dgrp, 8u * i, dk);
+    } else {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * LPW) : "memory");
+    }
     dma(i + NB - 1);
     const char *sb = sbuf + (i % NB) * BUF;
     // all fragments of the step first, then the MFMAs (one LDS latency per step)
@@ -241,6 +277,16 @@ __global__ __launch_bounds__(NT) void lora_down_partial_kernel(
   lora_down_dma_body<RT, staged_nb<RT>()>(sbuf, blockIdx.x, blockIdx.y, IN, M, Kc, ldin, WT, ldwt, r, KR, P);
 }
 
+// The masked down-projection (dropout of X ahead of the adapter).
+template <int RT>
+__global__ __launch_bounds__(NT) void drop_down_kernel(const uint16_t *__restrict__ IN, int M, int Kc,
+                                                       const uint16_t *__restrict__ WT, int r, int KR,
+                                                       float *__restrict__ P, Dropout drop) {
+  __shared__ __attribute__((aligned(16))) char sbuf[staged_bytes<RT>()];
+  lora_down_dma_body<RT, staged_nb<RT>(), false, true>(sbuf, blockIdx.x, blockIdx.y, IN, M, Kc, Kc, WT, Kc, r, KR, P,
+                                                        drop);
+}
+
 // ---------------------------------------------------------------------------------
 // reduce_m: partial sums over a split of rows m of IN[m][no] * S[m][j].
 //   JMAJOR = false: P[s][no][j]  (A = S rows j, B = IN columns no)   -> dB [N, r]
@@ -254,10 +300,10 @@ __global__ __launch_bounds__(NT) void lora_down_partial_kernel(
 // column i of those four rows.  NB buffers, one barrier per 64-row step; wave w owns
 // output tiles w, w + 4, ... of the 2 x RT tiles of 32 x 32.
 
-template <int RT, bool JMAJOR, int NB>
+template <int RT, bool JMAJOR, int NB, bool DROP = false>
 __device__ __forceinline__ void reduce_m_dma_body(
     char *sbuf, int bx, int by, const uint16_t *__restrict__ IN, int M, int No, int ldin,
-    const uint16_t *__restrict__ S, int lds, int r, int MR, float *__restrict__ P) {
+    const uint16_t *__restrict__ S, int lds, int r, int MR, float *__restrict__ P, const Dropout &drop = Dropout{}) {
   constexpr int INB = 64 * 128;        // IN tile bytes
   constexpr int SROW = 64 * RT;        // S tile row bytes
   constexpr int BUF = INB + 64 * SROW;
@@ -330,11 +376,27 @@ __device__ __forceinline__ void reduce_m_dma_body(
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[u][e] = 0.0f;
 
+  DropKey dk{};
+  uint32_t dgrp[2] = {0u, 0u};  // generator groups of this lane's IN chunks at step 0
+  if constexpr (DROP) {
+    dk = drop_key(drop);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = (lane & 7) ^ ((lrow[u] & 7) ^ ((lrow[u] >> 3) & 1));
+      dgrp[u] = static_cast<uint32_t>(mb + lrow[u]) * (No / 8) + nb0 / 8 + c;
+    }
+  }
+
 #pragma unroll
   for (int s = 0; s < NB - 1; ++s) dma(s);
   for (int i = 0; i < nsteps; ++i) {
     // step i has landed for every wave, and no wave still reads buffer (i - 1) % NB
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * LPW) : "memory");
+    if constexpr (DROP) {
+      drop_own_chunks<(NB - 2) * LPW>(sbuf + (i % NB) * BUF + wave * 1024 + lane * 16, dgrp,
+                                      64u * i * static_cast<uint32_t>(No / 8), dk);
+    } else {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * LPW) : "memory");
+    }
     dma(i + NB - 1);
     const char *sb = sbuf + (i % NB) * BUF;
     u32x4_t fi[TPW][4], fs[TPW][4];
@@ -382,6 +444,15 @@ __global__ __launch_bounds__(NT) void reduce_m_partial_kernel(
     int r, int MR, float *__restrict__ P) {
   __shared__ __attribute__((aligned(16))) char sbuf[staged_bytes<RT>()];
   reduce_m_dma_body<RT, JMAJOR, staged_nb<RT>()>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, ldin, S, lds, r, MR, P);
+}
+
+// dA's reduction over tokens with the dropout mask on X.
+template <int RT>
+__global__ __launch_bounds__(NT) void drop_reduce_kernel(const uint16_t *__restrict__ IN, int M, int No,
+                                                         const uint16_t *__restrict__ S, int r, int MR,
+                                                         float *__restrict__ P, Dropout drop) {
+  __shared__ __attribute__((aligned(16))) char sbuf[staged_bytes<RT>()];
+  reduce_m_dma_body<RT, true, staged_nb<RT>(), true>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, No, S, r, r, MR, P, drop);
 }
 
 // Transposes of bf16 matrices: OUT[C, R] = IN[R, C]^T.  A workgroup moves one 64 x 64
@@ -736,6 +807,55 @@ hipError_t launch_lora_down(const uint16_t *IN, int64_t M, int64_t Kc, int64_t l
   return hipGetLastError();
 }
 
+bool drop_shape_ok(int64_t M, int64_t Kc, int r) {
+  return r >= 1 && r <= kMaxRank && down_fast(M, Kc, Kc, Kc, r, r) && reduce_fast(M, Kc, Kc, r, r);
+}
+
+hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *WT, int r, float scale,
+                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream) {
+  if (!drop_shape_ok(M, Kc, r) || d.thr == 0) return hipErrorInvalidValue;
+  const DownSplit sp = down_split(M, Kc);
+  dim3 grid(static_cast<unsigned>((M + 63) / 64), static_cast<unsigned>(sp.ksplit)), block(NT);
+  switch ((r + 31) / 32) {
+#define QLORA_CASE(T)                                                                                       \
+  case T:                                                                                                   \
+    hipLaunchKernelGGL(drop_down_kernel<T>, grid, block, 0, stream, IN, static_cast<int>(M),                \
+                       static_cast<int>(Kc), WT, r, sp.KR, ws, d);                                          \
+    break;
+    QLORA_CASE(1) QLORA_CASE(2) QLORA_CASE(3) QLORA_CASE(4)
+    QLORA_CASE(5) QLORA_CASE(6) QLORA_CASE(7) QLORA_CASE(8)
+#undef QLORA_CASE
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_finalize(ws, sp.ksplit, M * r, r, r, scale, OUT, stream);
+}
+
+hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *S, int r, float *partials,
+                                uint16_t *OUT, const Dropout &d, hipStream_t stream, FinalizeJob *defer) {
+  if (defer) defer->splits = 0;
+  if (!drop_shape_ok(M, Kc, r) || d.thr == 0) return hipErrorInvalidValue;
+  const MSplit sp = m_split(M, Kc);
+  dim3 grid(static_cast<unsigned>((Kc + 63) / 64), static_cast<unsigned>(sp.splits)), block(NT);
+  switch ((r + 31) / 32) {
+#define QLORA_CASE(T)                                                                                       \
+  case T:                                                                                                   \
+    hipLaunchKernelGGL(drop_reduce_kernel<T>, grid, block, 0, stream, IN, static_cast<int>(M),              \
+                       static_cast<int>(Kc), S, r, sp.MR, partials, d);                                     \
+    break;
+    QLORA_CASE(1) QLORA_CASE(2) QLORA_CASE(3) QLORA_CASE(4)
+    QLORA_CASE(5) QLORA_CASE(6) QLORA_CASE(7) QLORA_CASE(8)
+#undef QLORA_CASE
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (defer) {
+    *defer = FinalizeJob{partials, sp.splits, Kc * r, Kc * r, Kc * r, 1.0f, OUT};
+    return hipSuccess;
+  }
+  return launch_finalize(partials, sp.splits, Kc * r, Kc * r, Kc * r, 1.0f, OUT, stream);
+}
+
 hipError_t launch_transpose2_bf16(const uint16_t *IN0, int64_t R0, int64_t C0, uint16_t *OUT0, const uint16_t *IN1,
                                   int64_t R1, int64_t C1, uint16_t *OUT1, hipStream_t stream) {
   TransposeJob j0{IN0, OUT0, R0, C0, (C0 + 63) / 64}, j1{IN1, OUT1, R1, C1, (C1 + 63) / 64};
@@ -809,9 +929,11 @@ hipError_t launch_reduce_m(const uint16_t *IN, int64_t M, int64_t No, int64_t ld
   return hipGetLastError();
 }
 
-bool vdb_fast(int64_t M, int64_t Np, int64_t ldy, int64_t ldu, int r) {
-  // B [Np, r] is read with row pitch r (its part of a stacked B)
-  return down_fast(M, Np, ldy, r, r, ldu) && reduce_fast(M, Np, ldy, ldu, r) && uint64_t(Np) * r * 2 <= k4G;
+bool vdb_fast(int64_t M, int64_t Np, int64_t ldy, int64_t ldu, int r, bool padded) {
+  // B [Np, r] is read with row pitch r (its part of a stacked B); in padded rows the last
+  // 16-byte chunk of a row holds zeros past Np
+  const int64_t Nc = padded ? (Np + 7) / 8 * 8 : Np;
+  return down_fast(M, Nc, ldy, r, r, ldu) && reduce_fast(M, Nc, ldy, ldu, r) && uint64_t(Np) * r * 2 <= k4G;
 }
 
 size_t vdb_workspace_v(int64_t M, int64_t Np, int r) {
@@ -823,9 +945,9 @@ size_t vdb_workspace_db(int64_t M, int64_t Np, int r) {
 
 hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, const uint16_t *B, const uint16_t *U,
                       int64_t ldu, int r, float scale, uint16_t *V, uint16_t *dB, float *ws_v, float *ws_db,
-                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream) {
+                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream, bool padded) {
   const int rt = (r + 31) / 32;
-  if (rt < 1 || rt > 8 || !vdb_fast(M, Np, ldy, ldu, r)) return hipErrorInvalidValue;
+  if (rt < 1 || rt > 8 || !vdb_fast(M, Np, ldy, ldu, r, padded)) return hipErrorInvalidValue;
   const DownSplit sd = down_split(M, Np);
   const MSplit sq = m_split(M, Np);
   DownArgs d{dY, static_cast<int>(M), static_cast<int>(Np), static_cast<int>(ldy), B, r, r,

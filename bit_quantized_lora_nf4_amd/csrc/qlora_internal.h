@@ -55,7 +55,29 @@ struct WeightView {
   int const_type;
 };
 
+// Dropout from a counter-based generator (drop_words in device_common.h): an element is
+// kept when its 16 bits are >= thr; thr == 0: no dropout.  `counter` (nullable) is a
+// device word added to the offset when the kernel runs.
+struct Dropout {
+  uint32_t thr, k0, k1;
+  uint64_t offset;
+  const uint64_t *counter;
+};
+
 // ---- launchers (each returns the HIP error of its launches) -----------------
+// out = x c m of n elements (n >= 1): bf16 or fp32.
+hipError_t launch_dropout(const void *X, bool bf16, int64_t n, const Dropout &d, float c, void *out,
+                          hipStream_t stream);
+// One row of a copy job: `rows` rows of `cols` bf16 values from src (row pitch lds) to dst
+// (row pitch ldd); dst columns cols .. dcols - 1 are cleared.  launch_copy_rows runs all
+// jobs of the list (at most kMaxCopyJobs, rows == 0 skipped) in one launch.
+struct CopyJob {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t rows, cols, dcols, lds, ldd;
+};
+constexpr int kMaxCopyJobs = 4;
+hipError_t launch_copy_rows(const CopyJob *jobs, int n, hipStream_t stream);
 // absmax_f32 receives the fp32 block constants (required for kConstF32, optional
 // otherwise); absmax_q / dq_scale / dq_offset are written for the double-quantized types.
 hipError_t launch_quantize(const void *W, bool w_bf16, int64_t n_rows, int64_t n_cols, int quant_type,
@@ -70,6 +92,11 @@ size_t lora_down_workspace(int64_t M, int64_t Kc, int r);
 hipError_t launch_lora_down(const uint16_t *IN, int64_t M, int64_t Kc, int64_t ldin, const uint16_t *WT,
                             int64_t ldwt, int r, float scale, uint16_t *OUT, int64_t ldout, float *ws,
                             hipStream_t stream);
+// The same with the dropout mask on IN, a dense [M, Kc] tensor: OUT = bf16(scale (m IN) WT^T).
+// Needs r % 8 == 0 and the fast-path shapes (drop_shape_ok).
+hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *WT, int r, float scale,
+                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream);
+bool drop_shape_ok(int64_t M, int64_t Kc, int r);
 // OUT_q[C_q, R_q] = IN_q[R_q, C_q]^T for two bf16 matrices (dense row-major) in one
 // launch; IN1 may be NULL (one transpose).
 hipError_t launch_transpose2_bf16(const uint16_t *IN0, int64_t R0, int64_t C0, uint16_t *OUT0, const uint16_t *IN1,
@@ -101,19 +128,25 @@ size_t reduce_m_workspace(int64_t M, int64_t No, int r);
 hipError_t launch_reduce_m(const uint16_t *IN, int64_t M, int64_t No, int64_t ldin, const uint16_t *S,
                            int64_t lds, int r, float *partials, uint16_t *OUT, bool trans_out,
                            hipStream_t stream, FinalizeJob *defer = nullptr);
+// dA [r, Kc] = bf16(S^T (m IN)) with the dropout mask on IN, a dense [M, Kc] tensor (S
+// dense [M, r]); needs drop_shape_ok(M, Kc, r).
+hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *S, int r, float *partials,
+                                uint16_t *OUT, const Dropout &d, hipStream_t stream, FinalizeJob *defer);
 
 // The backward's two products over dY in one launch plus one finalize launch:
 // V[M, r] (row pitch ldu) = bf16(scale dY B) and dB[Np, r] = bf16(dY^T U), where dY has
 // row pitch ldy (a column slice of width Np), B is [Np, r] (dense rows) and U [M, r]
 // with row pitch ldu.  If A and At are given, the same launch also writes At[KA, RA] =
 // A[RA, KA]^T.  Needs the fast-path shapes (vdb_fast) and the two fp32 partial regions
-// sized by vdb_workspace_v / vdb_workspace_db.
-bool vdb_fast(int64_t M, int64_t Np, int64_t ldy, int64_t ldu, int r);
+// sized by vdb_workspace_v / vdb_workspace_db.  `padded`: dY's rows hold zeros in columns
+// Np .. round_up(Np, 8) - 1 of the slice, and Np need not be a multiple of 8.
+bool vdb_fast(int64_t M, int64_t Np, int64_t ldy, int64_t ldu, int r, bool padded = false);
 size_t vdb_workspace_v(int64_t M, int64_t Np, int r);
 size_t vdb_workspace_db(int64_t M, int64_t Np, int r);
 hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, const uint16_t *B, const uint16_t *U,
                       int64_t ldu, int r, float scale, uint16_t *V, uint16_t *dB, float *ws_v, float *ws_db,
-                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream);
+                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream,
+                      bool padded = false);
 
 // AdamW step (fp32 parameter and moments, bf16 gradient, optional bf16 parameter copy).
 struct AdamConsts {
@@ -158,5 +191,11 @@ hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const 
 hipError_t launch_gemm_dx(const WeightView &w, const uint16_t *dY, int64_t M, const uint16_t *V,
                           const uint16_t *At, int r, uint16_t *dX, hipStream_t stream,
                           const FinalizeJob *fin = nullptr);
+// The same with the dropout mask of X on the LoRA term, dX = bf16(dY . W' + m (V . At^T)),
+// and with dY given in `parts` column blocks of round_up(Np, 8) columns each (Np = N /
+// parts; the padding columns hold zeros), so that odd part heights keep 16-byte rows.
+hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M, int parts, const uint16_t *V,
+                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, hipStream_t stream,
+                              const FinalizeJob *fin);
 
 }  // namespace qlora

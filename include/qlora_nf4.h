@@ -111,6 +111,24 @@ typedef struct {
   int32_t const_type;
 } qlora_nf4_weight;
 
+/* Dropout from a counter-based generator ([Repro] "官方代码阅读路线", the adapter's
+ * lora_dropout).  No mask is stored: whether element e of a row-major tensor is kept is a
+ * function of (seed, offset, e).  With t = floor(65536 p + 1/2):
+ *   (w0, w1, w2, w3) = Philox4x32-7 of counter (e / 8 as 64 bits, o as 64 bits), key seed
+ *   h = 16 bits of w[(e % 8) / 2], the low half for even e;   kept (m = 1) iff h >= t
+ *   o = offset + *counter (mod 2^64);   c = 65536 / (65536 - t)
+ * so the drop probability is the multiple t / 65536 of 2^-16 nearest to p, and c m x has
+ * the mean x exactly.  t = 0 drops nothing; t = 65536 (p within 2^-17 of 1) is refused.
+ * `counter` (nullable) is a device word, 8-byte aligned, read when the kernels run: a
+ * captured graph draws new masks on each replay when the program advances the word in
+ * between.  A backward call must see the seed, offset and counter value of its forward. */
+typedef struct {
+  double p;                /* 0 <= p < 1 */
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t *counter; /* device pointer or NULL */
+} qlora_drop;
+
 /* ---- host-only helpers (no GPU needed) ------------------------------------ */
 
 /* Storage sizes of an n_rows x n_cols weight.  Any output pointer may be NULL.
@@ -255,6 +273,38 @@ int qlora_linear_bwd_fused(const qlora_nf4_weight *w, int n_parts, const uint16_
                            int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha,
                            const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB,
                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of caller workspace for qlora_linear_fwd_dropout (op = 0) or
+ * qlora_linear_bwd_dropout (op = 1); at least qlora_workspace_bytes_fused for the same
+ * shapes.  0 for invalid arguments. */
+size_t qlora_workspace_bytes_dropout(int op, int64_t M, int64_t K, int64_t N, int r, int n_parts);
+
+/* qlora_linear_fwd_fused (n_parts = 1: qlora_linear_fwd) with dropout on the adapter's
+ * input, D(X) = c m X over X [M, K] (one mask for all parts; see qlora_drop):
+ *   U_q = bf16((alpha / r) c . (m X) . A_q^T)
+ *   Y_q = bf16(X . W_q'^T + U_q . B_q^T)
+ * The base product sees X itself.  m X is exact and c enters with alpha / r (one fp32
+ * factor), so D(X) itself is never rounded.  drop NULL or t = 0: the call without dropout,
+ * bit for bit.  Further requirement with dropout: n_parts round_up(r, 8) <= 256. */
+int qlora_linear_fwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *X, int64_t M,
+                             const uint16_t *A, const uint16_t *B, int r, float alpha, const qlora_drop *drop,
+                             uint16_t *Y, uint16_t *U_saved, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Backward of qlora_linear_fwd_dropout with the same drop:
+ *   V_q = bf16((alpha / r) c . dY_q . B_q)       dB_q = bf16(dY_q^T . U_q)
+ *   dX = bf16(dY . W' + m (V . A))               dA   = bf16(V^T . (m X))
+ * U_saved is the forward's U (NULL: recomputed with the mask).  QLORA_ERR_SHAPE, before
+ * anything is launched, when a tensor exceeds 0xFFFFFFF0 bytes. */
+int qlora_linear_bwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *dY, const uint16_t *X,
+                             int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha,
+                             const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA,
+                             uint16_t *dB, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Dropout of a tensor by itself: out[e] = RN(c x[e]) where kept, else 0, for e < n; X and
+ * out both fp32 (dtype = QLORA_F32) or bf16 (QLORA_BF16).  Its backward is the same call
+ * on the gradient.  out may equal X (in place). */
+int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, void *out, void *stream);
 
 /* Concatenate quantized weights along rows into `out` (device copies on `stream`):
  * codes, block constants and group constants are appended part after part.  With

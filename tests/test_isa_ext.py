@@ -1,0 +1,95 @@
+"""Waits and registers of the kernels with dropout, read from their gfx950 assembly like
+tests/test_isa_waits.py does for the others: in the masked staging loops the wait ahead of a
+step's masking must retire that step's loads (vmcnt(N) with N <= loads before the loop minus
+loads per step, and no other vector memory operation inside the loop); at every barrier of
+the extended dX kernel each direct-to-LDS load issued before it must be retired; no kernel
+spills.  No GPU needed."""
+
+import os
+import re
+import subprocess
+
+import pytest
+
+from bit_quantized_lora_nf4_amd import build as libbuild
+from tests.test_isa_waits import _VMEM, _barrier_waits, _cfg, _dma, _events, HIPCC
+
+
+def _asm(tmp_path_factory, name):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    out = tmp_path_factory.mktemp("isa") / (name + ".s")
+    flags = [f for f in libbuild.FLAGS if f != "-fPIC"]
+    cmd = [HIPCC] + flags + ["--cuda-device-only", "-S", os.path.join(libbuild.CSRC, name + ".hip"), "-o", str(out)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    return out.read_text()
+
+
+@pytest.fixture(scope="module")
+def lora_asm(tmp_path_factory):
+    return _asm(tmp_path_factory, "lora")
+
+
+@pytest.fixture(scope="module")
+def gemm_asm(tmp_path_factory):
+    return _asm(tmp_path_factory, "gemm")
+
+
+def test_masked_staging_waits(lora_asm):
+    kernels = re.findall(r"^(_Z\S*drop_(?:down|reduce)_kernel\S*):", lora_asm, re.M)
+    assert len(kernels) == 16, kernels
+    for name in kernels:
+        body = re.search(r"^" + re.escape(name) + r":.*?^\.Lfunc_end", lora_asm, re.S | re.M).group(0)
+        blocks = _cfg(body)
+        found = 0
+        for h, hb in enumerate(blocks):
+            if not re.match(r"; =>This Inner Loop Header: Depth=1", hb["note"]):
+                continue
+            hid = hb["label"][2:]
+            members = {i for i, b in enumerate(blocks) if i == h or f"Header={hid} " in b["note"] + " "}
+            lines = [ln for i in sorted(members) for ln in blocks[i]["lines"]]
+            if not any(ln.startswith("s_barrier") for ln in lines):
+                continue
+            assert not [ln for ln in lines if _VMEM.match(ln) and not ln.endswith(" lds")], name
+            waits = [int(m.group(1)) for ln in lines if (m := re.match(r"s_waitcnt vmcnt\((\d+)\)", ln))]
+            per_step = _dma(lines)
+            # the masking reads the step's own chunks right after the one wait
+            assert len(waits) == 1, (name, waits)
+            pro = sum(_dma(blocks[i]["lines"]) for i in range(len(blocks)) if i not in members)
+            # the loads before the loop sit in straight-line blocks: NB - 1 steps of them
+            assert pro % per_step == 0 and pro >= per_step, (name, pro, per_step)
+            assert waits[0] <= pro - per_step, (name, waits, pro, per_step)
+            # the wait precedes the masking reads, which precede the barrier
+            order = [("W" if ln.startswith("s_waitcnt vmcnt") else "R" if ln.startswith("ds_read_b128") else
+                      "S" if ln.startswith("ds_write_b128") else "B" if ln.startswith("s_barrier") else "")
+                     for i in [h] + sorted(members - {h}) for ln in blocks[i]["lines"]]
+            order = "".join(order)
+            assert re.match(r"^W(RRSS|RSRS)B", order), (name, order[:20])
+            found += 1
+        assert found == 1, (name, found)
+
+
+@pytest.mark.parametrize("ct", [0, 1, 2])
+def test_ext_dx_barrier_waits(gemm_asm, ct):
+    name = re.search(r"^(_Z\S*gemm_dx_ext_kernelILi%d\S*):" % ct, gemm_asm, re.M).group(1)
+    ev = _events(gemm_asm, name)
+    waits = _barrier_waits(ev)
+    assert len(waits) >= 4
+    for i, n in waits:
+        j = i - 1
+        while j >= 0 and ev[j][0] != "D":
+            j -= 1
+        if j < 0:
+            continue
+        after = sum(1 for x in ev[j + 1:i] if x[0] == "R")
+        assert n <= after, f"barrier wait vmcnt({n}) with only {after} register loads after the last dY load"
+
+
+def test_no_register_spills(gemm_asm, lora_asm):
+    for asm, pat in ((gemm_asm, "gemm_dx_ext"), (lora_asm, "drop_")):
+        sizes = dict(re.findall(r"\.name:\s+(\S*" + pat + r"\S*kernel\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)",
+                                asm, re.S))
+        assert len(sizes) >= 3, sizes
+        for name, size in sizes.items():
+            assert int(size) <= 16, f"{name}: {size} bytes of scratch"
