@@ -17,6 +17,11 @@ Training with dropout on the adapter's input (``lora_dropout``): the same calls 
     d = Dropout(0.1, seed, offset=step)                # the same d in forward and backward
     Y, U = linear_fwd(qw, X, A, B, alpha, dropout=d)
     dX, dA, dB = linear_bwd(qw, dY, X, A, B, alpha, U, dropout=d)
+
+Gated feed-forward projections (``qw``: gate rows, then up rows; A [2 r, K], B [2 P, r]):
+
+    H, Y, U = gated_fwd(qw, X, A, B, alpha)            # H = silu(gate) * up in one kernel
+    dX, dA, dB = gated_bwd(qw, dH, Y, X, A, B, alpha, U)
 """
 
 from contextlib import nullcontext
@@ -31,7 +36,8 @@ from ._lib import (QLORA_BF16, QLORA_CONST_DQ_FP8, QLORA_CONST_DQ_INT8, QLORA_CO
                    qlora_nf4_codebook, qlora_nf4_concat_rows, qlora_nf4_sizes, qlora_quantize,
                    qlora_quantize_nf4, qlora_workspace_bytes, qlora_workspace_bytes_fused,
                    qlora_dropout, qlora_linear_bwd_dropout, qlora_linear_fwd_dropout,
-                   qlora_workspace_bytes_dropout)
+                   qlora_workspace_bytes_dropout, QLORA_ACT_GELU_TANH, QLORA_ACT_SILU, qlora_gated_bwd,
+                   qlora_gated_fwd, qlora_workspace_bytes_gated)
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "workspace",
            "adamw_step", "lora_merge", "lora_unmerge", "concat_rows", "linear_fwd_fused",
@@ -41,7 +47,9 @@ __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "w
            "qlora_linear_bwd_fused", "qlora_workspace_bytes_fused", "qlora_nf4_concat_rows",
            "qlora_quantize", "qlora_codebook", "qlora_linear_fwd_noalloc", "linear_fwd_noalloc", "QLORA_QUANT_NF4", "QLORA_QUANT_FP4", "QLORA_CONST_DQ_INT8",
            "QLORA_CONST_DQ_FP8", "QLORA_CONST_FP32", "Dropout", "dropout", "qlora_dropout",
-           "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_workspace_bytes_dropout"]
+           "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_workspace_bytes_dropout", "gated_fwd", "gated_bwd",
+           "qlora_gated_fwd", "qlora_gated_bwd", "qlora_workspace_bytes_gated", "QLORA_ACT_SILU",
+           "QLORA_ACT_GELU_TANH"]
 
 
 def _torch():
@@ -241,6 +249,14 @@ def workspace(op, M, K, N, r, device):
     torch = _torch()
     n = qlora_workspace_bytes(op, M, K, N, r)
     return torch.zeros(max(n, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=device)
+
+
+def _scratch(nbytes, device):
+    """A workspace for one call: only its header has to start at zero."""
+    torch = _torch()
+    ws = torch.empty(max(nbytes, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=device)
+    ws[:_lib.QLORA_WORKSPACE_HEADER_BYTES].zero_()
+    return ws
 
 
 def linear_fwd(qw, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None, dropout=None):
@@ -508,3 +524,116 @@ def dropout(X, drop, out=None):
                            drop.descriptor(X.device), out.data_ptr(), _stream(X))
     _lib.check(st, "qlora_dropout")
     return out
+
+
+# ---- gated feed-forward projections ----------------------------------------------------
+
+_ACTS = {"silu": QLORA_ACT_SILU, "gelu_tanh": QLORA_ACT_GELU_TANH}
+
+
+def _gated_checks(qw, X, A, B, act):
+    """(checker, M, K, P, r, activation value) of a gated call."""
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r}: expected one of {sorted(_ACTS)}")
+    K, N = qw.n_cols, qw.n_rows
+    if N % 2:
+        raise ValueError(f"{N} weight rows do not split into gate and up")
+    if X.dim() != 2:
+        raise ValueError(f"X must be 2-D [M, {K}], got shape {tuple(X.shape)}")
+    chk = _Args(qw.codes.device)
+    M = X.shape[0]
+    chk.need(X, _torch().bfloat16, "X", (M, K))
+    R = 0 if A is None else A.shape[0]
+    if R % 2:
+        raise ValueError(f"A has {R} rows, not a multiple of 2")
+    r = R // 2
+    chk.adapter(A, B, N, K, R=R, r=r)
+    return chk, M, K, N // 2, r, _ACTS[act]
+
+
+def gated_fwd(qw, X, A=None, B=None, alpha=16.0, act="silu", save=True, H=None, Y=None, U=None, ws=None,
+              dropout=None):
+    """Gated projections H = act(gate) * up in one kernel: qw holds P gate rows, then P up
+    rows; A [2 r, K] and B [2 P, r] stack their adapters.  Returns (H [M, P], Y [M, 2 P] =
+    [gate | up], U [M, 2 r]); Y and U are what gated_bwd needs and are None with
+    ``save=False``.  act: "silu" or "gelu_tanh"; ``dropout``: a Dropout of the adapters' X."""
+    torch = _torch()
+    chk, M, K, P, r, act = _gated_checks(qw, X, A, B, act)
+    bf = torch.bfloat16
+    if H is not None:
+        chk.need(H, bf, "H", (M, P))
+    if save and Y is not None:
+        chk.need(Y, bf, "Y", (M, 2 * P))
+    if save and r and U is not None:
+        chk.need(U, bf, "U", (M, 2 * r))
+    drop = None if dropout is None or not r else dropout.descriptor(X.device)
+    nbytes = qlora_workspace_bytes_gated(0, M, K, P, r)
+    chk.workspace(ws, nbytes)
+    chk.devices()
+    dev = chk.device
+    if H is None:
+        H = torch.empty((M, P), dtype=bf, device=dev)
+    if not save:
+        Y = U = None
+    else:
+        if Y is None:
+            Y = torch.empty((M, 2 * P), dtype=bf, device=dev)
+        if not r:
+            U = None
+        elif U is None:
+            U = torch.empty((M, 2 * r), dtype=bf, device=dev)
+    if ws is None and nbytes:
+        ws = _scratch(nbytes, dev)
+    with _guard(dev):
+        st = qlora_gated_fwd(qw.descriptor(), X.data_ptr(), M, _ptr(A), _ptr(B), r, float(alpha), act, drop,
+                             H.data_ptr(), _ptr(Y), _ptr(U), _ptr(ws), 0 if ws is None else ws.numel(), _stream(X))
+    _lib.check(st, "qlora_gated_fwd")
+    return H, Y, U
+
+
+def gated_bwd(qw, dH, Y, X=None, A=None, B=None, alpha=16.0, U=None, act="silu", need_dx=True, dX=None, dA=None,
+              dB=None, ws=None, dropout=None):
+    """(dX, dA, dB) of gated_fwd from the gradient dH of H and the saved Y (and U: None
+    recomputes it); alpha, act and dropout as in the forward."""
+    torch = _torch()
+    bf = torch.bfloat16
+    if dH.dim() != 2:
+        raise ValueError(f"dH must be 2-D, got shape {tuple(dH.shape)}")
+    if X is None and A is not None:
+        raise ValueError("X is required when the layer has an adapter")
+    chk, M, K, P, r, act = _gated_checks(qw, torch.empty((dH.shape[0], qw.n_cols), dtype=bf, device="meta")
+                                         if X is None else X, A, B, act)
+    if X is None:
+        chk.seen.clear()
+    chk.need(dH, bf, "dH", (M, P))
+    chk.need(Y, bf, "Y", (M, 2 * P))
+    if U is not None and r:
+        chk.need(U, bf, "U", (M, 2 * r))
+    if need_dx and dX is not None:
+        chk.need(dX, bf, "dX", (M, K))
+    if r and dA is not None:
+        chk.need(dA, bf, "dA", (2 * r, K))
+    if r and dB is not None:
+        chk.need(dB, bf, "dB", (2 * P, r))
+    drop = None if dropout is None or not r else dropout.descriptor(dH.device)
+    nbytes = qlora_workspace_bytes_gated(1, M, K, P, r)
+    chk.workspace(ws, nbytes)
+    chk.devices()
+    dev = chk.device
+    if need_dx and dX is None:
+        dX = torch.empty((M, K), dtype=bf, device=dev)
+    if not r:
+        dA = dB = U = None
+    else:
+        if dA is None:
+            dA = torch.empty((2 * r, K), dtype=bf, device=dev)
+        if dB is None:
+            dB = torch.empty((2 * P, r), dtype=bf, device=dev)
+    if ws is None:
+        ws = _scratch(nbytes, dev)
+    with _guard(dev):
+        st = qlora_gated_bwd(qw.descriptor(), dH.data_ptr(), Y.data_ptr(), _ptr(X), M, _ptr(A), _ptr(B), r,
+                             float(alpha), act, drop, _ptr(U), _ptr(dX) if need_dx else None, _ptr(dA), _ptr(dB),
+                             _ptr(ws), ws.numel(), _stream(dH))
+    _lib.check(st, "qlora_gated_bwd")
+    return (dX if need_dx else None), dA, dB

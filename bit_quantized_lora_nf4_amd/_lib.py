@@ -29,6 +29,8 @@ QLORA_QUANT_FP4 = 1
 QLORA_CONST_DQ_INT8 = 0
 QLORA_CONST_DQ_FP8 = 1
 QLORA_CONST_FP32 = 2
+QLORA_ACT_SILU = 0
+QLORA_ACT_GELU_TANH = 1
 
 EXPORTED = (
     "qlora_nf4_sizes", "qlora_nf4_codebook", "qlora_workspace_bytes", "qlora_status_string",
@@ -37,7 +39,8 @@ EXPORTED = (
     "qlora_lora_unmerge", "qlora_workspace_bytes_fused", "qlora_linear_fwd_fused",
     "qlora_linear_bwd_fused", "qlora_nf4_concat_rows", "qlora_quantize", "qlora_codebook",
     "qlora_linear_fwd_noalloc", "qlora_workspace_bytes_dropout", "qlora_linear_fwd_dropout",
-    "qlora_linear_bwd_dropout", "qlora_dropout",
+    "qlora_linear_bwd_dropout", "qlora_dropout", "qlora_workspace_bytes_gated", "qlora_gated_fwd",
+    "qlora_gated_bwd",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 QLORA_WORKSPACE_HEADER_BYTES = 65792  # leading workspace bytes that must be zero at first use
@@ -131,6 +134,12 @@ def load(path=LIB_PATH):
     lib.qlora_linear_bwd_dropout.restype = I32
     lib.qlora_dropout.argtypes = [P, I32, I64, D, P, P]
     lib.qlora_dropout.restype = I32
+    lib.qlora_workspace_bytes_gated.argtypes = [I32, I64, I64, I64, I32]
+    lib.qlora_workspace_bytes_gated.restype = SZ
+    lib.qlora_gated_fwd.argtypes = [W, P, I64, P, P, I32, F32, I32, D, P, P, P, P, SZ, P]
+    lib.qlora_gated_fwd.restype = I32
+    lib.qlora_gated_bwd.argtypes = [W, P, P, P, I64, P, P, I32, F32, I32, D, P, P, P, P, P, SZ, P]
+    lib.qlora_gated_bwd.restype = I32
     _lib = lib
     return lib
 
@@ -267,6 +276,21 @@ def qlora_linear_bwd_dropout(w, n_parts, dY, X, M, A, B, r, alpha, drop, U_saved
 
 def qlora_dropout(X, dtype, n, drop, out, stream):
     return load().qlora_dropout(X, dtype, n, _drop(drop), out, stream)
+
+
+def qlora_workspace_bytes_gated(op, M, K, P, r):
+    return load().qlora_workspace_bytes_gated(op, M, K, P, r)
+
+
+def qlora_gated_fwd(w, X, M, A, B, r, alpha, act, drop, H, Y_saved, U_saved, workspace, workspace_bytes, stream):
+    return load().qlora_gated_fwd(ctypes.byref(w), X, M, A, B, r, alpha, act, _drop(drop), H, Y_saved, U_saved,
+                                  workspace, workspace_bytes, stream)
+
+
+def qlora_gated_bwd(w, dH, Y_saved, X, M, A, B, r, alpha, act, drop, U_saved, dX, dA, dB, workspace,
+                    workspace_bytes, stream):
+    return load().qlora_gated_bwd(ctypes.byref(w), dH, Y_saved, X, M, A, B, r, alpha, act, _drop(drop), U_saved, dX,
+                                  dA, dB, workspace, workspace_bytes, stream)
 
 
 def _drop(drop):

@@ -31,6 +31,7 @@ FLAGS = [
 ]
 
 SOURCES = ["codebook.cpp", "api.cpp", "quantize.hip", "dequant.hip", "lora.hip", "gemm.hip", "adamw.hip", "merge.hip", "dropout.hip",
+           "gated.hip",
            "gemv.hip"]
 
 

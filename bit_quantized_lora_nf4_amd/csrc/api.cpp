@@ -540,11 +540,13 @@ int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
     if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
   const int64_t K = w->n_cols, N = w->n_rows;
   const int r8 = round8(r), R8 = parts * r8;
+  const bool small = qlora::gemv_shape_ok(M, N);
   const DropFwdLayout L = drop_fwd_layout(M, K, N, r, parts);
-  s = check_workspace(who, workspace, workspace_bytes, L.total);
+  s = check_workspace(who, workspace, workspace_bytes, small ? qlora::gemv_workspace(M, K, N, parts * r) : L.total);
   if (s != QLORA_OK) return s;
   const qlora::WeightView wv = view(w);
-  if (!qlora::gemm_supported(wv, M, R8) || !qlora::drop_shape_ok(M, K, R8))
+  if (small ? !qlora::gemv_supported(wv, M, parts * r)
+            : !qlora::gemm_supported(wv, M, R8) || !qlora::drop_shape_ok(M, K, R8))
     return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
                 (long long)M, (long long)K, (long long)N);
   s = check_device();
@@ -552,6 +554,13 @@ int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
   hipStream_t st = static_cast<hipStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   const float scale = static_cast<float>(double(alpha) / r * c);
+  const int64_t part_rows = parts > 1 ? N / parts : 0;
+  if (small)
+    return launched(timed_launch(st, [&] {
+                      return qlora::launch_gemv_ext(wv, X, M, A, parts * r, B, r, part_rows, scale, Y, U_saved,
+                                                    workspace, qlora::GemvExt{d, nullptr, 0}, st);
+                    }),
+                    "gemv");
   uint16_t *U = U_saved && r8 == r ? U_saved : reinterpret_cast<uint16_t *>(ws + L.u);
   const uint16_t *A8, *B8;
   s = drop_down(X, M, K, N, A, B, r, parts, scale, d, ws, L.pad, L.part, U, &A8, &B8, st);
@@ -561,7 +570,6 @@ int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
     s = launched(qlora::launch_copy_rows(&job, 1, st), "unpad(U)");
     if (s != QLORA_OK) return s;
   }
-  const int64_t part_rows = parts > 1 ? N / parts : 0;
   return launched(
       timed_launch(st, [&] { return qlora::launch_gemm_fwd(wv, X, M, U, R8, B8, r8, part_rows, Y, st); }),
       "gemm_fwd");
@@ -667,6 +675,117 @@ int bwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
   }
   const float scale = static_cast<float>(double(alpha) / r * c);
   return bwd_blocks(w, parts, dY, ldp, ldp * parts, X, M, A, B, r, scale, d, U_saved, dX, dA, dB, ws, L, st);
+}
+
+// ---- gated projections --------------------------------------------------------
+int check_gated(const char *who, const qlora_nf4_weight *w, int64_t M, int r, float alpha, int act) {
+  int s = check_weight(w);
+  if (s == QLORA_OK) s = check_m(M);
+  if (s == QLORA_OK) s = check_rank(r, alpha);
+  if (s != QLORA_OK) return s;
+  if (w->n_rows % 2 != 0)
+    return fail(QLORA_ERR_SHAPE, "%s: %lld weight rows do not split into gate and up", who, (long long)w->n_rows);
+  if (act != QLORA_ACT_SILU && act != QLORA_ACT_GELU_TANH)
+    return fail(QLORA_ERR_VALUE, "%s: act %d: expected QLORA_ACT_SILU or QLORA_ACT_GELU_TANH", who, act);
+  return check_padded_rank(who, r, 2);
+}
+static_assert(QLORA_ACT_SILU == int(qlora::kActSilu) && QLORA_ACT_GELU_TANH == int(qlora::kActGeluTanh),
+              "activation values");
+
+// The small-M path's workspace, or U, partial sums and padded operands (none without an
+// adapter).
+size_t gated_fwd_bytes(int64_t M, int64_t K, int64_t P, int r) {
+  return qlora::gemv_shape_ok(M, 2 * P) ? qlora::gemv_ext_workspace(M, K, 2 * P, r, 2)
+                                        : drop_fwd_layout(M, K, 2 * P, r, 2).total;
+}
+
+int gated_fwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *X, int64_t M, const uint16_t *A,
+                   const uint16_t *B, int r, float alpha, int act, const qlora_drop *drop, uint16_t *H,
+                   uint16_t *Y_saved, uint16_t *U_saved, void *workspace, size_t workspace_bytes, void *stream) {
+  qlora::Dropout d;
+  float c;
+  int s = check_gated(who, w, M, r, alpha, act);
+  if (s == QLORA_OK) s = check_drop(who, drop, &d, &c);
+  if (s != QLORA_OK) return s;
+  if (!X || !H) return fail(QLORA_ERR_NULL, "%s: X and H are required", who);
+  if (r > 0 && (!A || !B)) return fail(QLORA_ERR_NULL, "%s: A and B are required when r > 0", who);
+  const void *ptrs[] = {X, H, Y_saved, U_saved, r > 0 ? A : nullptr, r > 0 ? B : nullptr};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+  const int64_t K = w->n_cols, N = w->n_rows, P = N / 2;
+  const int r8 = round8(r), R8 = 2 * r8;
+  s = check_workspace(who, workspace, workspace_bytes, gated_fwd_bytes(M, K, P, r));
+  if (s != QLORA_OK) return s;
+  const qlora::WeightView wv = view(w);
+  const bool small = qlora::gemv_shape_ok(M, N);
+  if (small ? !qlora::gemv_supported(wv, M, 2 * r)
+            : !qlora::gemm_supported(wv, M, R8) || (r > 0 && !qlora::drop_shape_ok(M, K, R8)))
+    return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
+                (long long)M, (long long)K, (long long)N);
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const float scale = r > 0 ? static_cast<float>(double(alpha) / r * c) : 0.0f;
+  if (small)
+    return launched(timed_launch(st, [&] {
+                      return qlora::launch_gemv_ext(wv, X, M, A, 2 * r, B, r, 0, scale, Y_saved,
+                                                    r > 0 ? U_saved : nullptr, workspace, qlora::GemvExt{d, H, act},
+                                                    st);
+                    }),
+                    "gemv");
+  const uint16_t *A8 = nullptr, *B8 = nullptr;
+  uint16_t *U = nullptr;
+  if (r > 0) {
+    char *ws = static_cast<char *>(workspace);
+    const DropFwdLayout L = drop_fwd_layout(M, K, N, r, 2);
+    U = U_saved && r8 == r ? U_saved : reinterpret_cast<uint16_t *>(ws + L.u);
+    s = drop_down(X, M, K, N, A, B, r, 2, scale, d, ws, L.pad, L.part, U, &A8, &B8, st);
+    if (s != QLORA_OK) return s;
+    if (U_saved && U != U_saved) {
+      const qlora::CopyJob job = unpad_rank(U, U_saved, M * 2, r);
+      s = launched(qlora::launch_copy_rows(&job, 1, st), "unpad(U)");
+      if (s != QLORA_OK) return s;
+    }
+  }
+  return launched(
+      timed_launch(st, [&] { return qlora::launch_gemm_gated(wv, X, M, U, R8, B8, r8, act, H, Y_saved, st); }),
+      "gemm_gated");
+}
+
+int gated_bwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *dH, const uint16_t *Y_saved,
+                   const uint16_t *X, int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha, int act,
+                   const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+  qlora::Dropout d;
+  float c;
+  int s = check_gated(who, w, M, r, alpha, act);
+  if (s == QLORA_OK) s = check_drop(who, drop, &d, &c);
+  if (s != QLORA_OK) return s;
+  if (!dH || !Y_saved) return fail(QLORA_ERR_NULL, "%s: dH and Y_saved are required", who);
+  if (r > 0 && (!A || !B || !X || !dA || !dB))
+    return fail(QLORA_ERR_NULL, "%s: X, A, B, dA and dB are required when r > 0", who);
+  if (r == 0 && !dX) return fail(QLORA_ERR_NULL, "%s: nothing to compute (r = 0, dX NULL)", who);
+  const void *ptrs[] = {dH, Y_saved, X, A, B, U_saved, dX, dA, dB};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+  const int64_t K = w->n_cols, N = w->n_rows, P = N / 2, ldp = round8(P);
+  const int r8 = round8(r), R8 = 2 * r8;
+  const DropBwdLayout L = drop_bwd_layout(M, K, N, r, 2, true);
+  s = check_workspace(who, workspace, workspace_bytes, L.total);
+  if (s != QLORA_OK) return s;
+  if (!qlora::gemm_supported(view(w), M, R8) || uint64_t(M) * ldp * 4 > 0xFFFFFFF0ull ||
+      (r > 0 && (!qlora::drop_shape_ok(M, K, R8) || !qlora::vdb_fast(M, P, 2 * ldp, R8, r8, true))))
+    return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
+                (long long)M, (long long)K, (long long)N);
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  uint16_t *dY = reinterpret_cast<uint16_t *>(ws + L.dy);
+  s = launched(qlora::launch_gated_grad(dH, Y_saved, M, P, act, dY, st), "gated_grad");
+  if (s != QLORA_OK) return s;
+  const float scale = r > 0 ? static_cast<float>(double(alpha) / r * c) : 0.0f;
+  return bwd_blocks(w, 2, dY, ldp, 2 * ldp, X, M, A, B, r, scale, d, U_saved, dX, dA, dB, ws, L, st);
 }
 
 }  // namespace
@@ -840,6 +959,30 @@ int qlora_linear_bwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint1
                              uint16_t *dB, void *workspace, size_t workspace_bytes, void *stream) {
   return bwd_dropout_impl("linear_bwd_dropout", w, n_parts, dY, X, M, A, B, r, alpha, drop, U_saved, dX, dA, dB,
                           workspace, workspace_bytes, stream);
+}
+
+size_t qlora_workspace_bytes_gated(int op, int64_t M, int64_t K, int64_t P, int r) {
+  if (M < 1 || K < 1 || P < 1 || K % 64 != 0 || r < 0 || M > kMaxDim || P > kMaxDim / 2 ||
+      2 * int64_t(round8(r)) > QLORA_MAX_RANK)
+    return 0;
+  if (op == 0) return gated_fwd_bytes(M, K, P, r);
+  if (op == 1) return drop_bwd_layout(M, K, 2 * P, r, 2, true).total;
+  return 0;
+}
+
+int qlora_gated_fwd(const qlora_nf4_weight *w, const uint16_t *X, int64_t M, const uint16_t *A, const uint16_t *B,
+                    int r, float alpha, int act, const qlora_drop *drop, uint16_t *H, uint16_t *Y_saved,
+                    uint16_t *U_saved, void *workspace, size_t workspace_bytes, void *stream) {
+  return gated_fwd_impl("gated_fwd", w, X, M, A, B, r, alpha, act, drop, H, Y_saved, U_saved, workspace,
+                        workspace_bytes, stream);
+}
+
+int qlora_gated_bwd(const qlora_nf4_weight *w, const uint16_t *dH, const uint16_t *Y_saved, const uint16_t *X,
+                    int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha, int act,
+                    const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+  return gated_bwd_impl("gated_bwd", w, dH, Y_saved, X, M, A, B, r, alpha, act, drop, U_saved, dX, dA, dB, workspace,
+                        workspace_bytes, stream);
 }
 
 int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, void *out, void *stream) {

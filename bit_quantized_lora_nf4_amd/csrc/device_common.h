@@ -299,6 +299,32 @@ __device__ __forceinline__ u32x4_t drop_mask(u32x4_t w, uint32_t thr) {
   return m;
 }
 
+// ---- activations of the gated projections ---------------------------------------------
+// act(x) = x s and act'(x) = s + x s (1 - s) dz, s = 1 / (1 + exp(-z)):
+//   kActSilu      z = x
+//   kActGeluTanh  z = 2 sqrt(2 / pi) (x + 0.044715 x^3)  (0.5 (1 + tanh(z / 2)) = s)
+// The exponential overflows to infinity for z below -88, where s is 0 as it should be.
+// The hardware exponential and reciprocal are good to a few 2^-24 (times |z| for the
+// exponent's product), far below the bf16 rounding of the results.
+constexpr float kGelu2K = 1.5957691216057308f, kGeluC = 0.044715f;
+template <int ACT>
+__device__ __forceinline__ float act_logistic(float x) {
+  const float z = ACT == kActSilu ? x : kGelu2K * (x + kGeluC * x * x * x);
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+  return x * act_logistic<ACT>(x);
+}
+template <int ACT>
+__device__ __forceinline__ void act_grad(float x, float &f, float &df) {
+  const float s = act_logistic<ACT>(x);
+  f = x * s;
+  // past |x| = 1e4 s (1 - s) is 0: the bound on x^2 only keeps the product from 0 * inf
+  const float dz = ACT == kActSilu ? 1.0f : kGelu2K * (1.0f + 3.0f * kGeluC * fminf(x * x, 1e8f));
+  df = s + f * (1.0f - s) * dz;
+}
+
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));

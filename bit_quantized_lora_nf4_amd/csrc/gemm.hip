@@ -258,6 +258,99 @@ __device__ __forceinline__ void store_out_lds(const GemmParams &p, int m0, int c
   }
 }
 
+// ---- gated projections ------------------------------------------------------------------
+// Outputs of the gated forward: H [M, P], and Y [M, 2 P] = [G | L] or NULL.
+struct GatedOut {
+  uint16_t *H, *Y;
+  int act;
+};
+
+// The rank steps of the gated forward from memory (lora_steps with one part per 32-column
+// block j: acc[i][0] takes the gate's ranks, acc[i][1] the up projection's).
+__device__ __forceinline__ void lora_steps_gated(const GemmParams &p, int m0, int h, f32x16_t (&acc)[8][2]) {
+  const int lane = threadIdx.x & 63;
+  const int r = p.r, lda2 = p.lda2, P = p.part_rows;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A2, static_cast<uint32_t>(uint64_t(p.M) * lda2 * 2));
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.B2, static_cast<uint32_t>(uint64_t(p.No) * r * 2));
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    for (int r0 = 0; r0 < r; r0 += 16) {
+      const int j0 = r0 + (lane >> 5) * 8;
+      const u32x4_t wa = lora_frag(rb, true, h < P ? j * P + h : p.No, p.No, r, j0, r);
+      u32x4_t xb[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // columns [j r, j r + r) of U; ranks past r are zero on both sides
+        const int row = m0 + i * 32 + (lane & 31);
+        xb[i] = buf_load16(ra, row < p.M && j0 < r ? (static_cast<uint32_t>(row) * lda2 + j * r + j0) * 2 : kOOB);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][j] = mfma32x32x16(wa, xb[i], acc[i][j]);
+    }
+}
+
+// Epilogue of the gated forward: lane holds token m0 + 32 i + l % 32 and columns
+// h0 + 32 w + 8 g + 4 (l / 32) + 0..3 of G in acc[i][0] and of L in acc[i][1].  The
+// workgroup's 128 columns of H (and G, L when they are kept) go through LDS, 128 tokens at
+// a time (rows of 264 bytes: the 32 token rows of a lane half fall in distinct banks), and
+// are written back 4 rows x 256 bytes per store instruction, or element by element when P
+// is not a multiple of 8.  `lds` holds 3 x 128 x 264 bytes that no wave reads any more.
+constexpr int kGatedPitch = 264;
+constexpr int kGatedStage = 128 * kGatedPitch;
+template <int ACT>
+__device__ __forceinline__ void store_gated(const GemmParams &p, const GatedOut &o, int m0, int h0,
+                                            const f32x16_t (&acc)[8][2], char *lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int P = p.part_rows;
+  const bool keep = o.Y != nullptr, vec = P % 8 == 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x16_t &a = acc[4 * h + ii][0], &b = acc[4 * h + ii][1];
+        const int off = (ii * 32 + (lane & 31)) * kGatedPitch + (wave * 32 + g * 8 + (lane >> 5) * 4) * 2;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = act_value<ACT>(a[4 * g + e]) * b[4 * g + e];
+        *reinterpret_cast<u32x2_t *>(lds + off) = u32x2_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        if (keep) {
+          *reinterpret_cast<u32x2_t *>(lds + kGatedStage + off) =
+              u32x2_t{pack_bf16x2(a[4 * g], a[4 * g + 1]), pack_bf16x2(a[4 * g + 2], a[4 * g + 3])};
+          *reinterpret_cast<u32x2_t *>(lds + 2 * kGatedStage + off) =
+              u32x2_t{pack_bf16x2(b[4 * g], b[4 * g + 1]), pack_bf16x2(b[4 * g + 2], b[4 * g + 3])};
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a few elements' registers at a time
+      }
+    __syncthreads();
+    for (int t = 0; t < (keep ? 3 : 1); ++t) {
+      const char *const src = lds + t * kGatedStage;
+      uint16_t *const out = t == 0 ? o.H : o.Y + (t == 2 ? P : 0);
+      const int64_t ld = t == 0 ? P : 2 * int64_t(P);
+      if (vec) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int tok = 16 * q + (tid >> 4), ch = tid & 15;
+          const u32x2_t lo = *reinterpret_cast<const u32x2_t *>(src + tok * kGatedPitch + ch * 16);
+          const u32x2_t hi = *reinterpret_cast<const u32x2_t *>(src + tok * kGatedPitch + ch * 16 + 8);
+          const int m = m0 + 128 * h + tok, col = h0 + ch * 8;
+          if (m < p.M && col < P)
+            *reinterpret_cast<u32x4_t *>(out + m * ld + col) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        }
+      } else {
+        for (int q = tid; q < 128 * 128; q += NT) {
+          const int tok = q >> 7, c = q & 127;
+          const int m = m0 + 128 * h + tok;
+          if (m < p.M && h0 + c < P)
+            out[m * ld + h0 + c] = *reinterpret_cast<const uint16_t *>(src + tok * kGatedPitch + c * 2);
+        }
+      }
+    }
+    __syncthreads();  // read back before the next half overwrites it
+  }
+}
+
 // Map the linear workgroup id to (token tile, output tile): workgroups are dispatched
 // round-robin over the 8 XCDs, so consecutive tiles of the grouped raster order are
 // given to the same XCD (sharing its L2); groups of 4 token tiles sweep the outputs.
@@ -342,15 +435,19 @@ constexpr int loads_before_barrier() {
 // register copy ever waits for a load in flight.
 constexpr int NBUF = 3;
 
-template <int CT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_fwd_kernel(
-    GemmParams p) {
-  __shared__ __attribute__((aligned(16))) char sX[NBUF * TILE_BYTES];
+// GATED: a tile is 256 tokens x 128 gate columns and the same 128 up columns; wave w owns
+// 32 of each (its two 32-column blocks j = 0, 1 are weight rows of the two projections at
+// the same column), so that act(G) L of an element is formed in one lane's registers.
+template <int CT, bool GATED>
+__device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o, char *sX) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tmi, tni;
-  tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
-  const int m0 = tmi * TM, n0 = tni * TN;
+  if constexpr (GATED)
+    tile_coords((p.M + TM - 1) / TM, (p.part_rows + TN / 2 - 1) / (TN / 2), tmi, tni);
+  else
+    tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
+  const int m0 = tmi * TM, n0 = tni * (GATED ? TN / 2 : TN);
 
   const int K = p.Kc;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.A, static_cast<uint32_t>(uint64_t(p.M) * K * 2));
@@ -375,7 +472,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   uint32_t coff[2], boff[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int n = min(n0 + wave * 64 + j * 32 + (lane & 31), p.No - 1);
+    const int n = GATED ? j * p.part_rows + min(n0 + wave * 32 + (lane & 31), p.part_rows - 1)
+                        : min(n0 + wave * 64 + j * 32 + (lane & 31), p.No - 1);
     coff[j] = static_cast<uint32_t>(n) * (K / 2) + (lane >> 5) * 16;
     boff[j] = static_cast<uint32_t>(n) * (K / 64);
   }
@@ -420,7 +518,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   u32x4_t wl[4][2];
   char *const sU = sX + 2 * TILE_BYTES;  // not written by the prologue's tile loads
   if (lds_lora) {
-    const int qc = p.part_rows > 0 ? (n0 / p.part_rows) * p.r : 0;
+    const int qc = !GATED && p.part_rows > 0 ? (n0 / p.part_rows) * p.r : 0;
     const __amdgpu_buffer_rsrc_t ru = make_rsrc(p.A2, static_cast<uint32_t>(uint64_t(p.M) * p.lda2 * 2));
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.B2, static_cast<uint32_t>(uint64_t(p.No) * p.r * 2));
     char *dst = sU + wave * 8 * 1024;
@@ -432,15 +530,25 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
       const uint32_t off = c * 8 < p.r ? (static_cast<uint32_t>(row) * p.lda2 + qc + c * 8) * 2 : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (__attribute__((address_space(3))) void *)(dst + i * 1024), 16,
                                                off, 0, 0, 0);
+      // GATED: the up projection's rank columns in a fourth buffer
+      if constexpr (GATED)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            ru, (__attribute__((address_space(3))) void *)(dst + TILE_BYTES + i * 1024), 16,
+            c * 8 < p.r ? off + p.r * 2 : kOOB, 0, 0, 0);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        wl[s][j] = lora_frag(rb, true, n0 + wave * 64 + j * 32 + (lane & 31), p.No, p.r,
-                             32 * (lane >> 5) + 8 * s, p.r);
+      for (int j = 0; j < 2; ++j) {
+        const int h = n0 + wave * 32 + (lane & 31);
+        const int row = GATED ? (h < p.part_rows ? j * p.part_rows + h : p.No) : n0 + wave * 64 + j * 32 + (lane & 31);
+        wl[s][j] = lora_frag(rb, true, row, p.No, p.r, 32 * (lane >> 5) + 8 * s, p.r);
+      }
   } else if (p.r > 0) {
-    lora_steps(p, m0, n0, acc);
+    if constexpr (GATED)
+      lora_steps_gated(p, m0, n0 + wave * 32 + (lane & 31), acc);
+    else
+      lora_steps(p, m0, n0, acc);
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -450,10 +558,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
       if (8 * s < p.r) {
         u32x4_t xu[8];
         read_xfrags_fwd(sU, s, xu);
+        if constexpr (GATED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 8; ++i) acc[i][0] = mfma32x32x16(wl[s][0], xu[i], acc[i][0]);
+          read_xfrags_fwd(sU + TILE_BYTES, s, xu);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(wl[s][j], xu[i], acc[i][j]);
+          for (int i = 0; i < 8; ++i) acc[i][1] = mfma32x32x16(wl[s][1], xu[i], acc[i][1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(wl[s][j], xu[i], acc[i][j]);
+        }
       }
     }
     __syncthreads();  // no wave reads the U_s tile any more when step 0 loads tile 2 there
@@ -539,13 +655,33 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   if (it + 1 < nk) step(Ic<1>{}, Ic<0>{}, it + 1, S1, S2, S0);
   // drain the clamped prefetches of the last steps before the epilogue
   __builtin_amdgcn_s_waitcnt(0);
-  if (p.No % 8 == 0) {
+  if constexpr (GATED) {
+    static_assert(3 * kGatedStage <= (NBUF + 1) * TILE_BYTES, "output staging");
+    __syncthreads();  // every wave is done reading the activation buffers
+    if (o.act == kActSilu)
+      store_gated<kActSilu>(p, o, m0, n0, acc, sX);
+    else
+      store_gated<kActGeluTanh>(p, o, m0, n0, acc, sX);
+  } else if (p.No % 8 == 0) {
     static_assert(4 * 128 * kOutPitch <= NBUF * TILE_BYTES, "output staging");
     __syncthreads();  // every wave is done reading the activation buffers
     store_out_lds(p, m0, n0, acc, sX);
   } else {
     store_out(p, m0, n0, acc);
   }
+}
+
+template <int CT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_fwd_kernel(
+    GemmParams p) {
+  __shared__ __attribute__((aligned(16))) char sX[NBUF * TILE_BYTES];
+  gemm_fwd_body<CT, false>(p, GatedOut{}, sX);
+}
+template <int CT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_gated_kernel(
+    GemmParams p, GatedOut o) {
+  __shared__ __attribute__((aligned(16))) char sX[(NBUF + 1) * TILE_BYTES];
+  gemm_fwd_body<CT, true>(p, o, sX);
 }
 
 // ===================================== backward ====================================
@@ -904,7 +1040,7 @@ __device__ __forceinline__ void mask_lora(const uint32_t (&keep)[4][2], f32x16_t
 }
 
 template <int CT, bool EXT>
-__device__ __forceinline__ void dx_pipe_body(const GemmParams &p, const DxExt &x, char *sW0, char *sW1, char *sY0,
+__device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, char *sW1, char *sY0,
                                              char *sY1) {
   // the workgroups after the tiles (dispatched last, so in CUs the tiles have left) do
   // the finalize job that rides in this launch
@@ -1247,6 +1383,27 @@ hipError_t launch_gemm_dx(const WeightView &w, const uint16_t *dY, int64_t M, co
     case kConstF32: return go(gemm_dx_pipe_kernel<kConstF32>, gemm_dx_kernel<false, kConstF32>);
     default: return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_gemm_gated(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *U, int ldu,
+                             const uint16_t *Bl, int r, int act, uint16_t *H, uint16_t *Y, hipStream_t stream) {
+  const int64_t P = w.n_rows / 2;
+  if (w.n_rows % 2 != 0 || P < 1 || (r > 0 && (r % 8 != 0 || ldu != 2 * r))) return hipErrorInvalidValue;
+  if (!fits_32bit(M, w.n_rows, w.n_cols, ldu) || M > 0x7fffffff) return hipErrorInvalidValue;
+  GemmParams p = make_params(X, w, U, Bl, nullptr, M, w.n_rows, w.n_cols, r);
+  p.lda2 = ldu;
+  p.part_rows = static_cast<int>(P);
+  const int64_t tiles = ((M + TM - 1) / TM) * ((P + TN / 2 - 1) / (TN / 2));
+  if (tiles > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles));
+  const GatedOut o{H, Y, act};
+  switch (w.const_type) {
+    case kConstDqInt8: hipLaunchKernelGGL(gemm_gated_kernel<kConstDqInt8>, grid, dim3(NT), 0, stream, p, o); break;
+    case kConstDqFp8: hipLaunchKernelGGL(gemm_gated_kernel<kConstDqFp8>, grid, dim3(NT), 0, stream, p, o); break;
+    case kConstF32: hipLaunchKernelGGL(gemm_gated_kernel<kConstF32>, grid, dim3(NT), 0, stream, p, o); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M, int parts, const uint16_t *V,

@@ -224,20 +224,21 @@ __device__ __forceinline__ float constant_of(const StepLoads<CT, XLDS> &st, cons
 // fp32, then (R > 0) the workgroup's 16 RG rows of Bl (bf16, row pitch r8 = r rounded up
 // to 8, zeros past r), then, when X is staged, X [M] rows of xrow_bytes(KB) (each 64-element block
 // permuted per 8-element group), then (DIRECT hand-over) the part's U_s
-// [M][r8] bf16 (zeros past r).  The padded rows let every LoRA operand of the epilogue be
+// [M][r8] bf16 (zeros past r; the gated projections: both parts', one after the other).  The padded rows let every LoRA operand of the epilogue be
 // one 16-byte read (a lane whose 8 ranks start past r reads nothing).
 struct LdsPlan {
   int red, bt, x, u, total;
 };
 __host__ __device__ inline int up16(int b) { return (b + 15) & ~15; }
-__host__ __device__ inline LdsPlan lds_plan(int nW, int M, int R, int r, int KB, bool xlds, bool direct, int RG) {
+__host__ __device__ inline LdsPlan lds_plan(int nW, int M, int R, int r, int KB, bool xlds, bool direct, int RG,
+                                            int uparts = 1) {
   LdsPlan p;
   p.red = 0;
   const int r8 = (r + 7) & ~7;
   p.bt = nW * 1024;
   p.x = p.bt + (R > 0 ? 32 * r8 * RG : 0);
   p.u = p.x + (xlds ? M * xrow_bytes(KB) : 0);
-  p.total = p.u + (direct ? up16(2 * M * r8) : 0);
+  p.total = p.u + (direct ? up16(2 * M * r8 * uparts) : 0);
   return p;
 }
 
@@ -299,8 +300,9 @@ __device__ __forceinline__ LoraLoads<XLDS> lora_issue(const GemvArgs &a, int KB,
   return ll;
 }
 
-template <bool XLDS, bool DIRECT>
-__device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, const LoraLoads<XLDS> &ll) {
+template <bool XLDS, bool DIRECT, bool EXT = false>
+__device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, const LoraLoads<XLDS> &ll,
+                            const Dropout &drop = Dropout{}) {
   constexpr int STEPS = LoraLoads<XLDS>::STEPS;
   const int lane = threadIdx.x & 63;
   const int ml = lane & 15, g = lane >> 4;
@@ -313,18 +315,30 @@ __device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, co
   const int t = p / a.SP, s = p % a.SP;
   const int b_lo = s * a.LB, b_hi = min(KB, b_lo + a.LB);
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  // EXT, dropout: the fragment of 8 X elements is one generator group (of the token's row
+  // and block), so its mask is one block's
+  DropKey dk{};
+  if constexpr (EXT) dk = drop_key(drop);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int b = b_lo + 4 * i + g;
     const bool ok = b < b_hi;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
+      u32x4_t keep;
+      if constexpr (EXT) {
+        keep = u32x4_t{~0u, ~0u, ~0u, ~0u};
+        if (dk.thr != 0) keep = drop_mask(drop_words(static_cast<uint32_t>((tok * KB + b) * 8 + u), 0u, dk), dk.thr);
+      }
       if constexpr (XLDS) {
         // the staged X is permuted per 8-element group: permute A the same way
-        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(sx + tok * xrow_bytes(KB) + (ok ? b : 0) * 128 + u * 16);
+        u32x4_t x = *reinterpret_cast<const u32x4_t *>(sx + tok * xrow_bytes(KB) + (ok ? b : 0) * 128 + u * 16);
+        if constexpr (EXT) x = x & permute8(keep);
         acc = mfma16x16x32(permute8(ll.av[i][u]), x, acc);
       } else {
-        acc = mfma16x16x32(ll.av[i][u], ll.xv[i][u], acc);
+        u32x4_t x = ll.xv[i][u];
+        if constexpr (EXT) x = x & keep;
+        acc = mfma16x16x32(ll.av[i][u], x, acc);
       }
     }
   }
@@ -395,7 +409,9 @@ __device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, co
 // order, of the partial sums), the same value the ticket path publishes.  It writes them
 // to LDS ([M][r8] bf16, zeros past r) for the epilogue, and the first workgroup of the
 // part also stores them to U_saved.
-__device__ void gather_u(const GemvArgs &a, uint16_t *su, int n0) {
+// Gated projections: both parts' columns, [2][M][r8], and the first workgroup saves them.
+template <bool EXT = false>
+__device__ void gather_u(const GemvArgs &a, uint16_t *su, int n0, bool gated = false) {
   const int lane = threadIdx.x & 63;
   uint32_t *cnt = a.sync + (kFlagBase + blockIdx.x * kFlagStride) / 4;
   const uint32_t want = static_cast<uint32_t>(a.PT * a.SP);
@@ -405,14 +421,19 @@ __device__ void gather_u(const GemvArgs &a, uint16_t *su, int n0) {
   }
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   if (lane == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int q = a.part_rows > 0 ? n0 / a.part_rows : 0;
+  const int q0 = a.part_rows > 0 ? n0 / a.part_rows : 0;
   const bool saver = a.U_saved && (a.part_rows > 0 ? n0 % a.part_rows == 0 : blockIdx.x == 0);
   const __amdgpu_buffer_rsrc_t rp = make_rsrc(a.PU, static_cast<uint32_t>(a.PT) * a.SP * a.M * 64);
   const int r8 = (a.r + 7) & ~7;
-  const int n = a.M * r8;
+  const int n = a.M * r8 * (EXT && gated ? 2 : 1);
   for (int e0 = 0; e0 < n; e0 += 64) {
     const int e = e0 + lane;
-    const int m = e / r8, jr = e % r8;
+    int m = e / r8, q = q0;
+    if (EXT && gated) {
+      q = m >= a.M;
+      m -= q * a.M;
+    }
+    const int jr = e % r8;
     const bool ok = e < n && jr < a.r;
     const int j = q * a.r + (ok ? jr : 0);
     const int t = j >> 4, jj = j & 15;
@@ -440,13 +461,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char *dst, uint3
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
 }
 
-template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA = false>
-__global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  // XDMA: the two X stages of every weight wave, separate objects so that the waits the
-  // compiler derives for a stage's reads cover only that stage's loads
-  __shared__ __attribute__((aligned(16))) char xst0[XDMA ? kXdmaWaves * kXdmaStage : 16];
-  __shared__ __attribute__((aligned(16))) char xst1[XDMA ? kXdmaWaves * kXdmaStage : 16];
+// EXT: dropout of X ahead of the adapter (x.drop), and the gated projections (x.H): a tile
+// of 16 weight rows is then 8 gate rows and the same 8 up rows, so that a reduction's lanes
+// l and l + 32 hold G and L of the same four columns of a token.
+template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA, bool EXT>
+__device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char *xst0, char *xst1) {
   static_assert(!(XLDS && XDMA), "X is staged for the workgroup or per wave, not both");
   constexpr int D = XLDS ? 4 : 2;  // steps whose loads are in flight (the register ring)
   constexpr bool XREG = !XLDS && !XDMA;  // X fragments loaded into registers with every step
@@ -454,14 +473,18 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
   // RG row groups of W weight waves each; wave RG W (R > 0) is the LoRA wave
   const int W = a.W, RG = a.RG, nW = RG * W;
   const int N = static_cast<int>(a.w.n_rows), KB = static_cast<int>(a.w.n_cols / 64), K = KB * 64;
-  const LdsPlan lp = lds_plan(nW, a.M, a.R, a.r, KB, XLDS, DIRECT, RG);
+  const bool gated = EXT && x.H != nullptr;
+  const int P = N / 2;  // gated: rows of each projection
+  const LdsPlan lp = lds_plan(nW, a.M, a.R, a.r, KB, XLDS, DIRECT, RG, gated ? 2 : 1);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ml = lane & 15, g = lane >> 4;
   const int grp = wave / W, wv = wave - grp * W;  // row group and wave within it
   const int n0w = static_cast<int>(blockIdx.x) * RG * 16;  // first row of the workgroup
   const int n0 = n0w + grp * 16;
-  const int n = n0 + ml;  // weight row of this lane's operand
-  const bool row_ok = n < N;
+  // weight row of this lane's operand (gated: n0 counts 16 per 8 columns)
+  const int hc = n0 / 2 + (ml & 7);
+  const int n = gated ? (ml >> 3) * P + hc : n0 + ml;
+  const bool row_ok = gated ? hc < P : n < N;
   const int tok = ml < a.M ? ml : 0;
   const bool tok_ok = ml < a.M;
   const int kb0 = (KB * wv) / W, kb1 = (KB * (wv + 1)) / W;
@@ -488,17 +511,18 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
     LoraLoads<XLDS> ll;
     if (static_cast<int>(blockIdx.x) < npieces) ll = lora_issue<XLDS>(a, KB, blockIdx.x);
     __syncthreads();
-    if (static_cast<int>(blockIdx.x) < npieces) lora_finish<XLDS, DIRECT>(a, lds + lp.x, KB, blockIdx.x, ll);
+    if (static_cast<int>(blockIdx.x) < npieces)
+      lora_finish<XLDS, DIRECT, EXT>(a, lds + lp.x, KB, blockIdx.x, ll, x.drop);
     if constexpr (MULTI) {
       // more pieces than workgroups (few output rows): the later ones one after another
       // (a separate instantiation: the loop costs the kernel about 35 registers)
       for (int p = blockIdx.x + gridDim.x; p < npieces; p += gridDim.x) {
         const LoraLoads<XLDS> lp2 = lora_issue<XLDS>(a, KB, p);
-        lora_finish<XLDS, DIRECT>(a, lds + lp.x, KB, p, lp2);
+        lora_finish<XLDS, DIRECT, EXT>(a, lds + lp.x, KB, p, lp2, x.drop);
       }
     }
     // DIRECT: U_s for the epilogue, in LDS before the reduction barrier
-    if constexpr (DIRECT) gather_u(a, reinterpret_cast<uint16_t *>(lds + lp.u), n0w);
+    if constexpr (DIRECT) gather_u<EXT>(a, reinterpret_cast<uint16_t *>(lds + lp.u), n0w, gated);
     __syncthreads();
     return;
   }
@@ -521,6 +545,14 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
     }
   }
   auto load_b = [&](int c) {
+    if (gated) {
+      // 16-byte piece c of the tile's rows of r ranks: row t of the workgroup's 16 RG
+      if (c >= bpieces) return u32x4_t{0u, 0u, 0u, 0u};
+      const int t = c / (a.r / 8), col = n0w / 2 + (t >> 4) * 8 + (t & 7);
+      const uint32_t off =
+          (static_cast<uint32_t>(((t >> 3) & 1) * P + col) * a.r + (c % (a.r / 8)) * 8) * 2;
+      return buf_load16(rb, col < P ? off : kOOB);
+    }
     const uint32_t off = b_base + static_cast<uint32_t>(c) * 16;
     if (c >= bpieces || off >= b_bytes) return u32x4_t{0u, 0u, 0u, 0u};
     if (off + 16 <= b_bytes) return buf_load16(rb, off);
@@ -624,9 +656,15 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
   } else if (a.R > 0) {
     for (int e = tid; e < 16 * RG * r8; e += nthr) {
       const int row = e / r8, j = e % r8;
-      const bool ok = j < a.r && n0w + row < N;
+      int wr = n0w + row;
+      bool ok = j < a.r && wr < N;
+      if (gated) {
+        const int col = n0w / 2 + (row >> 4) * 8 + (row & 7);
+        wr = ((row >> 3) & 1) * P + col;
+        ok = j < a.r && col < P;
+      }
       sb[e] = ok ? static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
-                       rb, static_cast<uint32_t>((n0w + row) * a.r + j) * 2, 0, 0))
+                       rb, static_cast<uint32_t>(wr * a.r + j) * 2, 0, 0))
                  : static_cast<uint16_t>(0);
     }
   }
@@ -664,15 +702,17 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
     // U_s of this part is in LDS (the LoRA wave put it there before the barrier)
     const uint16_t *urow = reinterpret_cast<const uint16_t *>(lds + lp.u) + tok * r8;
     const uint16_t *brow = sb + (grp * 16 + ml) * r8;
-    for (int c = 0; c < a.r; c += 32) {
-      const int j0 = c + 8 * g;
-      const bool in = j0 < a.r;
-      u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (in ? j0 : 0));
-      u32x4_t uf = *reinterpret_cast<const u32x4_t *>(urow + (in ? j0 : 0));
-      if (!in) bf = u32x4_t{0u, 0u, 0u, 0u};
-      if (!(in && tok_ok)) uf = u32x4_t{0u, 0u, 0u, 0u};
-      y = mfma16x16x32(bf, uf, y);
-    }
+    // gated: once per part, the other part's B rows cleared
+    for (int q = 0; q < (gated ? 2 : 1); ++q, urow += a.M * r8)
+      for (int c = 0; c < a.r; c += 32) {
+        const int j0 = c + 8 * g;
+        const bool in = j0 < a.r;
+        u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (in ? j0 : 0));
+        u32x4_t uf = *reinterpret_cast<const u32x4_t *>(urow + (in ? j0 : 0));
+        if (!in || (gated && (ml >> 3) != q)) bf = u32x4_t{0u, 0u, 0u, 0u};
+        if (!(in && tok_ok)) uf = u32x4_t{0u, 0u, 0u, 0u};
+        y = mfma16x16x32(bf, uf, y);
+      }
   } else if (a.R > 0) {
     // U_s from the LoRA waves: poll this workgroup's flag (and clear it for the next
     // call), then read this workgroup's copy of U_s (one row group per workgroup on this
@@ -688,33 +728,70 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
     const __amdgpu_buffer_rsrc_t ru = make_rsrc(a.Uc, static_cast<uint32_t>(a.NC) * a.UCE * 2);
     // Y += U_s[:, q r : q r + r] . Bl[rows]^T on the same accumulator: rows (the A
     // operand) from the staged Bl tile, tokens (the B operand) from U_s
-    const int q = a.part_rows > 0 ? n0 / a.part_rows : 0;
     const bool aligned = (a.r & 7) == 0;
     const uint16_t *brow = sb + (grp * 16 + ml) * r8;
-    const uint32_t ubase = static_cast<uint32_t>((blockIdx.x % a.NC) * a.UCE + tok * RP + q * a.r);
-    for (int c = 0; c < a.r; c += 32) {
-      const int j0 = c + 8 * g;
-      u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (j0 < a.r ? j0 : 0));
-      if (j0 >= a.r) bf = u32x4_t{0u, 0u, 0u, 0u};
-      u32x4_t uf = u32x4_t{0u, 0u, 0u, 0u};
-      if (tok_ok && j0 < a.r) {
-        if (aligned) {
-          uf = load16_sc1(ru, (ubase + j0) * 2);
-        } else {
+    auto up = [&](int q, bool own) {  // own: this lane's B row is of part q
+      const uint32_t ubase = static_cast<uint32_t>((blockIdx.x % a.NC) * a.UCE + tok * RP + q * a.r);
+      for (int c = 0; c < a.r; c += 32) {
+        const int j0 = c + 8 * g;
+        u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (j0 < a.r ? j0 : 0));
+        if (j0 >= a.r || !own) bf = u32x4_t{0u, 0u, 0u, 0u};
+        u32x4_t uf = u32x4_t{0u, 0u, 0u, 0u};
+        if (tok_ok && j0 < a.r) {
+          if (aligned) {
+            uf = load16_sc1(ru, (ubase + j0) * 2);
+          } else {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int j = j0 + 2 * h;
-            const uint32_t lo = j < a.r ? __builtin_amdgcn_raw_buffer_load_b16(ru, (ubase + j) * 2, 0, kSC1) : 0u;
-            const uint32_t hi =
-                j + 1 < a.r ? __builtin_amdgcn_raw_buffer_load_b16(ru, (ubase + j + 1) * 2, 0, kSC1) : 0u;
-            uf[h] = lo | (hi << 16);
+            for (int h = 0; h < 4; ++h) {
+              const int j = j0 + 2 * h;
+              const uint32_t lo = j < a.r ? __builtin_amdgcn_raw_buffer_load_b16(ru, (ubase + j) * 2, 0, kSC1) : 0u;
+              const uint32_t hi =
+                  j + 1 < a.r ? __builtin_amdgcn_raw_buffer_load_b16(ru, (ubase + j + 1) * 2, 0, kSC1) : 0u;
+              uf[h] = lo | (hi << 16);
+            }
           }
         }
+        y = mfma16x16x32(bf, uf, y);
       }
-      y = mfma16x16x32(bf, uf, y);
+    };
+    if (gated) {
+      up(0, ml < 8);
+      up(1, ml >= 8);
+    } else {
+      up(a.part_rows > 0 ? n0 / a.part_rows : 0, true);
     }
   }
-  if (tok_ok) {
+  if (gated) {
+    // lanes l and l + 32 hold G and L of token ml, columns h .. h + 3
+    const int h = n0 / 2 + 4 * (g & 1);
+    float l4[4], out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) l4[e] = __shfl_xor(y[e], 32, 64);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      out[e] = (x.act == kActSilu ? act_value<kActSilu>(y[e]) : act_value<kActGeluTanh>(y[e])) * l4[e];
+    const bool whole = h + 3 < P && (P & 3) == 0;
+    if (tok_ok && a.Y) {
+      uint16_t *yr = a.Y + static_cast<int64_t>(ml) * N + (g >> 1) * P;
+      if (whole) {
+        *reinterpret_cast<u32x2_t *>(yr + h) = u32x2_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (h + e < P) yr[h + e] = to_bf16(y[e]);
+      }
+    }
+    if (tok_ok && g < 2) {
+      uint16_t *hr = x.H + static_cast<int64_t>(ml) * P;
+      if (whole) {
+        *reinterpret_cast<u32x2_t *>(hr + h) = u32x2_t{pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (h + e < P) hr[h + e] = to_bf16(out[e]);
+      }
+    }
+  } else if (tok_ok) {
     const int nb = n0 + 4 * g;
     uint16_t *yr = a.Y + static_cast<int64_t>(ml) * N;
     if (nb + 3 < N && (N & 3) == 0) {
@@ -725,6 +802,23 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
         if (nb + e < N) yr[nb + e] = to_bf16(y[e]);
     }
   }
+}
+
+template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA = false>
+__global__ __launch_bounds__(kMaxWaves * 64) void gemv_kernel(GemvArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  // XDMA: the two X stages of every weight wave, separate objects so that the waits the
+  // compiler derives for a stage's reads cover only that stage's loads
+  __shared__ __attribute__((aligned(16))) char xst0[XDMA ? kXdmaWaves * kXdmaStage : 16];
+  __shared__ __attribute__((aligned(16))) char xst1[XDMA ? kXdmaWaves * kXdmaStage : 16];
+  gemv_body<CT, XLDS, MULTI, DIRECT, XDMA, false>(a, GemvExt{}, lds, xst0, xst1);
+}
+template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA = false>
+__global__ __launch_bounds__(kMaxWaves * 64) void gemv_ext_kernel(GemvArgs a, GemvExt x) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ __attribute__((aligned(16))) char xst0[XDMA ? kXdmaWaves * kXdmaStage : 16];
+  __shared__ __attribute__((aligned(16))) char xst1[XDMA ? kXdmaWaves * kXdmaStage : 16];
+  gemv_body<CT, XLDS, MULTI, DIRECT, XDMA, true>(a, x, lds, xst0, xst1);
 }
 
 // Weight waves per workgroup (W) and steps per weight wave (T).  A launch of G tiles puts
@@ -873,54 +967,56 @@ bool gemv_supported(const WeightView &w, int64_t M, int r) {
 }
 
 namespace {
-template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA = false>
-hipError_t go_gemv1(const GemvArgs &a, int lds_bytes, hipStream_t stream) {
+template <bool EXT, int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA = false>
+hipError_t go_gemv1(const GemvArgs &a, const GemvExt &x, int lds_bytes, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.G)), block(64 * (a.RG * a.W + (a.R > 0 ? 1 : 0)));
   if (lds_bytes > 64 * 1024) {
     static std::once_flag once[64];
     static hipError_t err[64];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return hipErrorInvalidDevice;
     std::call_once(once[dev], [&] {
-      err[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(gemv_kernel<CT, XLDS, MULTI, DIRECT, XDMA>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      const void *k;
+      if constexpr (EXT)
+        k = reinterpret_cast<const void *>(gemv_ext_kernel<CT, XLDS, MULTI, DIRECT, XDMA>);
+      else
+        k = reinterpret_cast<const void *>(gemv_kernel<CT, XLDS, MULTI, DIRECT, XDMA>);
+      err[dev] = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     });
     if (err[dev] != hipSuccess) return err[dev];
   }
-  hipLaunchKernelGGL((gemv_kernel<CT, XLDS, MULTI, DIRECT, XDMA>), dim3(static_cast<unsigned>(a.G)),
-                     dim3(64 * (a.RG * a.W + (a.R > 0 ? 1 : 0))),
-                     static_cast<size_t>(lds_bytes), stream, a);
+  if constexpr (EXT)
+    hipLaunchKernelGGL((gemv_ext_kernel<CT, XLDS, MULTI, DIRECT, XDMA>), grid, block, static_cast<size_t>(lds_bytes),
+                       stream, a, x);
+  else
+    hipLaunchKernelGGL((gemv_kernel<CT, XLDS, MULTI, DIRECT, XDMA>), grid, block, static_cast<size_t>(lds_bytes),
+                       stream, a);
   return hipGetLastError();
 }
-template <int CT, bool XLDS>
-hipError_t go_gemv(const GemvArgs &a, bool direct, bool xdma, int lds_bytes, hipStream_t stream) {
+template <bool EXT, int CT, bool XLDS>
+hipError_t go_gemv(const GemvArgs &a, const GemvExt &x, bool direct, bool xdma, int lds_bytes, hipStream_t stream) {
   const bool multi = a.PT * a.SP > a.G;
   if constexpr (!XLDS) {
     // the XDMA layout with one row group and at most kXdmaWaves weight waves
     if (xdma && a.RG == 1 && a.W <= kXdmaWaves) {
       if (direct)
-        return multi ? go_gemv1<CT, false, true, true, true>(a, lds_bytes, stream)
-                     : go_gemv1<CT, false, false, true, true>(a, lds_bytes, stream);
-      return multi ? go_gemv1<CT, false, true, false, true>(a, lds_bytes, stream)
-                   : go_gemv1<CT, false, false, false, true>(a, lds_bytes, stream);
+        return multi ? go_gemv1<EXT, CT, false, true, true, true>(a, x, lds_bytes, stream)
+                     : go_gemv1<EXT, CT, false, false, true, true>(a, x, lds_bytes, stream);
+      return multi ? go_gemv1<EXT, CT, false, true, false, true>(a, x, lds_bytes, stream)
+                   : go_gemv1<EXT, CT, false, false, false, true>(a, x, lds_bytes, stream);
     }
   }
   if (direct)
-    return multi ? go_gemv1<CT, XLDS, true, true>(a, lds_bytes, stream)
-                 : go_gemv1<CT, XLDS, false, true>(a, lds_bytes, stream);
-  return multi ? go_gemv1<CT, XLDS, true, false>(a, lds_bytes, stream)
-               : go_gemv1<CT, XLDS, false, false>(a, lds_bytes, stream);
+    return multi ? go_gemv1<EXT, CT, XLDS, true, true>(a, x, lds_bytes, stream)
+                 : go_gemv1<EXT, CT, XLDS, false, true>(a, x, lds_bytes, stream);
+  return multi ? go_gemv1<EXT, CT, XLDS, true, false>(a, x, lds_bytes, stream)
+               : go_gemv1<EXT, CT, XLDS, false, false>(a, x, lds_bytes, stream);
 }
-}  // namespace
-
-hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
-                       const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y,
-                       uint16_t *U_saved, void *ws, hipStream_t stream) {
-  if (!gemv_supported(w, M, R) || R < r || (part_rows > 0 && (w.n_rows % part_rows != 0 || part_rows % 16 != 0)))
-    return hipErrorInvalidValue;
-  const int64_t N = w.n_rows, K = w.n_cols;
-  GemvPlan p = gemv_plan(M, K, N, R);
-  // the row groups of a workgroup must lie in one part (they share its U_s)
-  if (p.RG > 1 && part_rows > 0 && part_rows % (16 * p.RG) != 0) p = gemv_plan(M, K, N, R, false);
+template <bool EXT>
+hipError_t run_gemv(const GemvPlan &p, const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
+                    const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y, uint16_t *U_saved,
+                    void *ws, const GemvExt &x, hipStream_t stream) {
+  const int64_t N = w.n_rows;
   GemvArgs a;
   a.w = w;
   a.X = X;
@@ -948,16 +1044,60 @@ hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const 
   a.lvl = level_table(w.quant_type);
   switch (w.const_type) {
     case kConstDqInt8:
-      return p.xlds ? go_gemv<kConstDqInt8, true>(a, p.direct, false, p.lds_bytes, stream)
-                    : go_gemv<kConstDqInt8, false>(a, p.direct, p.xdma, p.lds_bytes, stream);
+      return p.xlds ? go_gemv<EXT, kConstDqInt8, true>(a, x, p.direct, false, p.lds_bytes, stream)
+                    : go_gemv<EXT, kConstDqInt8, false>(a, x, p.direct, p.xdma, p.lds_bytes, stream);
     case kConstDqFp8:
-      return p.xlds ? go_gemv<kConstDqFp8, true>(a, p.direct, false, p.lds_bytes, stream)
-                    : go_gemv<kConstDqFp8, false>(a, p.direct, p.xdma, p.lds_bytes, stream);
+      return p.xlds ? go_gemv<EXT, kConstDqFp8, true>(a, x, p.direct, false, p.lds_bytes, stream)
+                    : go_gemv<EXT, kConstDqFp8, false>(a, x, p.direct, p.xdma, p.lds_bytes, stream);
     case kConstF32:
-      return p.xlds ? go_gemv<kConstF32, true>(a, p.direct, false, p.lds_bytes, stream)
-                    : go_gemv<kConstF32, false>(a, p.direct, p.xdma, p.lds_bytes, stream);
+      return p.xlds ? go_gemv<EXT, kConstF32, true>(a, x, p.direct, false, p.lds_bytes, stream)
+                    : go_gemv<EXT, kConstF32, false>(a, x, p.direct, p.xdma, p.lds_bytes, stream);
     default: return hipErrorInvalidValue;
   }
+}
+}  // namespace
+
+hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
+                       const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y,
+                       uint16_t *U_saved, void *ws, hipStream_t stream) {
+  if (!gemv_supported(w, M, R) || R < r || (part_rows > 0 && (w.n_rows % part_rows != 0 || part_rows % 16 != 0)))
+    return hipErrorInvalidValue;
+  GemvPlan p = gemv_plan(M, w.n_cols, w.n_rows, R);
+  // the row groups of a workgroup must lie in one part (they share its U_s)
+  if (p.RG > 1 && part_rows > 0 && part_rows % (16 * p.RG) != 0) p = gemv_plan(M, w.n_cols, w.n_rows, R, false);
+  return run_gemv<false>(p, w, X, M, A, R, Bl, r, part_rows, scale, Y, U_saved, ws, GemvExt{}, stream);
+}
+
+// The plan of the gated projections takes the rank that the staged LoRA operands are padded
+// to (both parts of U_s, rows of round_up(r, 8)), so that its LDS sum covers them.
+namespace {
+int gated_plan_rank(int r) { return 2 * ((r + 7) & ~7); }
+}  // namespace
+
+size_t gemv_ext_workspace(int64_t M, int64_t K, int64_t N, int r, int parts) {
+  const size_t one = gemv_workspace(M, K, N, r * parts);
+  if (parts != 2 || r == 0) return one;
+  const size_t SP = static_cast<size_t>(gemv_plan(M, K, N, gated_plan_rank(r)).SP), PT = (2 * size_t(r) + 15) / 16;
+  const size_t two = kGemvSyncBytes + gemv_u_copies(M, 2 * r) * up256(size_t(M) * PT * 16 * 2) +
+                     up256(PT * SP * M * 16 * 4);
+  return two > one ? two : one;
+}
+
+hipError_t launch_gemv_ext(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
+                           const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y, uint16_t *U_saved,
+                           void *ws, const GemvExt &x, hipStream_t stream) {
+  if (!gemv_supported(w, M, R) || R < r) return hipErrorInvalidValue;
+  const int64_t N = w.n_rows, K = w.n_cols;
+  GemvPlan p;
+  if (x.H) {
+    if (N % 2 != 0 || R != 2 * r || part_rows != 0 || gated_plan_rank(r) > kMaxRank) return hipErrorInvalidValue;
+    p = gemv_plan(M, K, N, gated_plan_rank(r));
+  } else {
+    if (part_rows > 0 && (N % part_rows != 0 || part_rows % 16 != 0)) return hipErrorInvalidValue;
+    p = gemv_plan(M, K, N, R);
+    if (p.RG > 1 && part_rows > 0 && part_rows % (16 * p.RG) != 0) p = gemv_plan(M, K, N, R, false);
+  }
+  return run_gemv<true>(p, w, X, M, A, R, Bl, r, part_rows, scale, Y, U_saved, ws, x, stream);
 }
 
 }  // namespace qlora

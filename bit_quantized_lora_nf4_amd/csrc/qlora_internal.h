@@ -64,6 +64,9 @@ struct Dropout {
   const uint64_t *counter;
 };
 
+// Activations of the gated projections (the header's qlora_act values).
+enum : int { kActSilu = 0, kActGeluTanh = 1 };
+
 // ---- launchers (each returns the HIP error of its launches) -----------------
 // out = x c m of n elements (n >= 1): bf16 or fp32.
 hipError_t launch_dropout(const void *X, bool bf16, int64_t n, const Dropout &d, float c, void *out,
@@ -186,11 +189,33 @@ bool gemv_supported(const WeightView &w, int64_t M, int r);
 hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
                        const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y,
                        uint16_t *U_saved, void *ws, hipStream_t stream);
+// Its extensions: the dropout mask on X ahead of the adapter (drop.thr > 0), and the gated
+// projections (H not NULL: H[M, P] = bf16(act(G) L), Y NULL or receiving [G | L]; r is each
+// projection's rank, A [2 r, K], part_rows unused).  gemv_ext_workspace holds for both.
+struct GemvExt {
+  Dropout drop;
+  uint16_t *H;
+  int act;
+};
+size_t gemv_ext_workspace(int64_t M, int64_t K, int64_t N, int r, int parts);
+hipError_t launch_gemv_ext(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,
+                           const uint16_t *Bl, int r, int64_t part_rows, float scale, uint16_t *Y, uint16_t *U_saved,
+                           void *ws, const GemvExt &x, hipStream_t stream);
 // dX[M, K] = bf16(dY . W' + V . At^T)  (V [M, r], At [K, r]); r may be 0.  A finalize
 // job (NULL or splits == 0: none) runs in extra workgroups after the GEMM's tiles.
 hipError_t launch_gemm_dx(const WeightView &w, const uint16_t *dY, int64_t M, const uint16_t *V,
                           const uint16_t *At, int r, uint16_t *dX, hipStream_t stream,
                           const FinalizeJob *fin = nullptr);
+// Gated projections: weight rows [0, P) are the gate's, [P, 2 P) the up projection's
+// (P = n_rows / 2), U [M, 2 r] (pitch ldu) and Bl [2 P, r] their stacked adapter operands.
+// H[M, P] = bf16(act(G) L) for [G | L] = X W'^T + U Bl^T before any rounding; Y, if not
+// NULL, receives bf16 [G | L] [M, 2 P].
+hipError_t launch_gemm_gated(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *U, int ldu,
+                             const uint16_t *Bl, int r, int act, uint16_t *H, uint16_t *Y, hipStream_t stream);
+// [dG | dL] = [dH L act'(G) | dH act(G)] from the saved bf16 [G | L] (Y [M, 2 P]), as bf16
+// rows of two column blocks of round_up(P, 8) columns, zeros in the padding.
+hipError_t launch_gated_grad(const uint16_t *dH, const uint16_t *Y, int64_t M, int64_t P, int act, uint16_t *dY,
+                             hipStream_t stream);
 // The same with the dropout mask of X on the LoRA term, dX = bf16(dY . W' + m (V . At^T)),
 // and with dY given in `parts` column blocks of round_up(Np, 8) columns each (Np = N /
 // parts; the padding columns hold zeros), so that odd part heights keep 16-byte rows.

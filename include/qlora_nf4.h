@@ -306,6 +306,37 @@ int qlora_linear_bwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint1
  * on the gradient.  out may equal X (in place). */
 int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, void *out, void *stream);
 
+/* Gated feed-forward projections ([Ch. 11.3] and [Paper note] apply LoRA to the gate and up
+ * projections of the decoder's feed-forward block): both linears, the activation and the
+ * product in one kernel, so that neither projection is read back.  w holds the gate's rows
+ * [0, P) and the up projection's [P, 2 P) (qlora_nf4_concat_rows, or one quantization of
+ * the stacked matrix; any P >= 1), the adapters are stacked like qlora_linear_fwd_fused's:
+ * A [2 r, K], B [2 P, r].
+ *   U = bf16((alpha / r) c . (m X) . A^T)                    [M, 2 r]   (drop NULL: c m = 1)
+ *   [G | L] = X . W'^T + [U_0 B_0^T | U_1 B_1^T]             [M, 2 P], fp32 accumulation
+ *   H = bf16(act(G) L)                                       [M, P], from the unrounded G, L
+ *   act: QLORA_ACT_SILU x s(x); QLORA_ACT_GELU_TANH x s(2 sqrt(2 / pi) (x + 0.044715 x^3)),
+ *   s the logistic function (gated SiLU and the tanh form of gated GELU).
+ * Y_saved (nullable) receives bf16 [G | L] and U_saved (nullable) U, both for the backward;
+ * a call that only needs H passes NULL.  2 round_up(r, 8) <= 256.
+ * Workspace: qlora_workspace_bytes_gated(0, M, K, P, r).  M <= 16 and P <= 32768: one
+ * launch (the small-M path); the workspace's header rule above applies. */
+typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU_TANH = 1 } qlora_act;
+size_t qlora_workspace_bytes_gated(int op, int64_t M, int64_t K, int64_t P, int r);
+int qlora_gated_fwd(const qlora_nf4_weight *w, const uint16_t *X, int64_t M, const uint16_t *A, const uint16_t *B,
+                    int r, float alpha, int act, const qlora_drop *drop, uint16_t *H, uint16_t *Y_saved,
+                    uint16_t *U_saved, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of qlora_gated_fwd from its saved [G | L] (Y_saved) and U (NULL: recomputed):
+ *   dG = bf16(dH L act'(G)),  dL = bf16(dH act(G))
+ * and then dX, dA, dB of the two linears for dY = [dG | dL], as qlora_linear_bwd_dropout
+ * gives them.  dH [M, P]; dX [M, K] (skipped if NULL); dA, dB like A, B.  dY stays in the
+ * workspace, qlora_workspace_bytes_gated(1, M, K, P, r) bytes. */
+int qlora_gated_bwd(const qlora_nf4_weight *w, const uint16_t *dH, const uint16_t *Y_saved, const uint16_t *X,
+                    int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha, int act,
+                    const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA, uint16_t *dB,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Concatenate quantized weights along rows into `out` (device copies on `stream`):
  * codes, block constants and group constants are appended part after part.  With
  * double-quantized constants every part but the last must hold a multiple of 256

@@ -1,9 +1,11 @@
-"""Waits and registers of the kernels with dropout, read from their gfx950 assembly like
+"""Waits and registers of the kernels with dropout and of the gated projections, read from their gfx950 assembly like
 tests/test_isa_waits.py does for the others: in the masked staging loops the wait ahead of a
 step's masking must retire that step's loads (vmcnt(N) with N <= loads before the loop minus
 loads per step, and no other vector memory operation inside the loop); at every barrier of
-the extended dX kernel each direct-to-LDS load issued before it must be retired; no kernel
-spills.  No GPU needed."""
+the extended dX kernel each direct-to-LDS load issued before it must be retired; at each
+barrier of the gated forward's pipeline only loads issued after the published tile's may be
+in flight; the small-M path's per-wave X stages are read only after their loads' wait; no
+kernel spills.  No GPU needed."""
 
 import os
 import re
@@ -12,7 +14,7 @@ import subprocess
 import pytest
 
 from bit_quantized_lora_nf4_amd import build as libbuild
-from tests.test_isa_waits import _VMEM, _barrier_waits, _cfg, _dma, _events, HIPCC
+from tests.test_isa_waits import _BR, _VMEM, _all_retired, _barrier_waits, _cfg, _dma, _events, HIPCC
 
 
 def _asm(tmp_path_factory, name):
@@ -86,8 +88,60 @@ def test_ext_dx_barrier_waits(gemm_asm, ct):
         assert n <= after, f"barrier wait vmcnt({n}) with only {after} register loads after the last dY load"
 
 
+@pytest.mark.parametrize("ct", [0, 1, 2])
+def test_gated_barrier_waits(gemm_asm, ct):
+    name = re.search(r"^(_Z\S*gemm_gated_kernelILi%d\S*):" % ct, gemm_asm, re.M).group(1)
+    ev = _events(gemm_asm, name)
+    waits = _barrier_waits(ev)
+    assert len(waits) >= 4
+    checked = 0
+    for i, n in waits:
+        j = i - 1
+        while j >= 0 and ev[j][0] != "B":
+            j -= 1
+        if j < 0 or _all_retired(ev, j):
+            continue  # a prologue barrier: everything issued before it was retired
+        k, seen = j + 1, 0
+        while k < i and seen < 4:
+            seen += ev[k][0] in ("D", "R")
+            k += 1
+        after = sum(1 for x in ev[k:i] if x[0] in ("D", "R"))
+        assert n <= after, f"barrier wait vmcnt({n}) leaves {n - after} loads of the published tile in flight"
+        checked += 1
+    assert checked >= 3
+
+
+def test_gemv_ext_x_stage_waits(tmp_path_factory):
+    asm = _asm(tmp_path_factory, "gemv")
+    # gemv_ext_kernel<CT, XLDS = false, MULTI, DIRECT, XDMA = true>
+    kernels = re.findall(r"^(_Z\S*gemv_ext_kernelILi\dELb0ELb\dELb\dELb1E\S*):", asm, re.M)
+    assert len(kernels) == 12, kernels
+    for name in kernels:
+        body = re.search(r"^" + re.escape(name) + r":.*?^\.Lfunc_end", asm, re.S | re.M).group(0)
+        lines = [ln.strip() for ln in body.splitlines()]
+        labels = {m.group(1): i for i, ln in enumerate(lines) if (m := re.match(r"^(\.LBB\S+):", ln))}
+        loops = [(labels[m.group(2)], i) for i, ln in enumerate(lines)
+                 if (m := _BR.search(ln)) and m.group(2) in labels and labels[m.group(2)] < i]
+        loops = [lines[a:b + 1] for a, b in loops]
+        loop = max((x for x in loops if _dma(x) == 16), key=len)  # the main loop: two steps of eight stage loads
+        vmem = sum(1 for ln in loop if _VMEM.match(ln))
+        assert vmem % 2 == 0, (name, vmem)
+        waits, last, seen = [], None, True
+        for ln in loop:
+            if m := re.match(r"s_waitcnt vmcnt\((\d+)\)", ln):
+                last = int(m.group(1))
+            elif _VMEM.match(ln):
+                seen, last = True, None
+            elif ln.startswith("ds_read") and seen:
+                waits.append(last)
+                seen = False
+        assert len(waits) == 2 and all(n is not None and n <= vmem // 2 for n in waits), (name, waits, vmem)
+    sizes = re.findall(r"\.name:\s+(\S*gemv_ext\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)", asm, re.S)
+    assert len(sizes) == 36 and all(int(n) <= 16 for _, n in sizes), sizes
+
+
 def test_no_register_spills(gemm_asm, lora_asm):
-    for asm, pat in ((gemm_asm, "gemm_dx_ext"), (lora_asm, "drop_")):
+    for asm, pat in ((gemm_asm, "gemm_dx_ext"), (gemm_asm, "gemm_gated"), (lora_asm, "drop_")):
         sizes = dict(re.findall(r"\.name:\s+(\S*" + pat + r"\S*kernel\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)",
                                 asm, re.S))
         assert len(sizes) >= 3, sizes
