@@ -443,9 +443,9 @@ DropFwdLayout drop_fwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts)
 }
 
 // dY's padded copy (odd part heights), U [M, R8], V [M, R8], A^T [K, R8], the fp32 partial
-// sums, the padded operands and the padded gradients.
+// sums, the padded operands and the padded gradients, the fp32 partial sums of a split dX.
 struct DropBwdLayout {
-  size_t dy = 0, u = 0, v = 0, at = 0, part = 0, part2 = 0, da = 0, db = 0, total = 0;
+  size_t dy = 0, u = 0, v = 0, at = 0, part = 0, part2 = 0, da = 0, db = 0, dx = 0, total = 0;
   PadLayout pad;
 };
 DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts, bool own_dy) {
@@ -477,6 +477,8 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts,
       off += align_up(size_t(N) * r8 * 2);
     }
   }
+  L.dx = off;
+  off += align_up(qlora::gemm_dx_ext_workspace(M, K, parts * Np8));
   L.total = off;
   return L;
 }
@@ -622,7 +624,8 @@ int bwd_blocks(const qlora_nf4_weight *w, int parts, const uint16_t *dY, int64_t
   }
   if (dX)
     s = launched(
-        timed_launch(st, [&] { return qlora::launch_gemm_dx_ext(wv, dY, M, parts, V, At, R8, dX, d, st, &fin); }),
+        timed_launch(st, [&] { return qlora::launch_gemm_dx_ext(wv, dY, M, parts, V, At, R8, dX, d,
+                                                                      reinterpret_cast<float *>(ws + L.dx), st, &fin); }),
         "gemm_dx");
   if (s == QLORA_OK && r8 != r) {
     const qlora::CopyJob jobs[] = {unpad_a(dA8, dA, K, r, parts), unpad_rank(dB8, dB, N, r)};

@@ -71,9 +71,14 @@ struct GemmParams {
 // in column blocks of `half` columns of which the last `skip` are padding: contraction
 // position k stands for weight row k - skip floor(k / half) where k % half < half - skip.
 // Only two blocks or none (half = the whole contraction) are needed.
+// With splits > 1 workgroup s tiles + t computes the contraction steps [s ksteps, (s + 1)
+// ksteps) of tile t and writes its fp32 accumulators to `part` (dx_join_kernel adds them);
+// the LoRA term belongs to split 0.
 struct DxExt {
   Dropout drop;
   int half, skip;
+  int splits, ksteps;
+  float *part;
 };
 
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
@@ -354,9 +359,8 @@ __device__ __forceinline__ void store_gated(const GemmParams &p, const GatedOut 
 // Map the linear workgroup id to (token tile, output tile): workgroups are dispatched
 // round-robin over the 8 XCDs, so consecutive tiles of the grouped raster order are
 // given to the same XCD (sharing its L2); groups of 4 token tiles sweep the outputs.
-__device__ __forceinline__ void tile_coords(int tiles_m, int tiles_n, int &tm, int &tn) {
+__device__ __forceinline__ void tile_coords(int b, int tiles_m, int tiles_n, int &tm, int &tn) {
   const int T = tiles_m * tiles_n;
-  int b = blockIdx.x;
   if ((T & 7) == 0) b = (b & 7) * (T >> 3) + (b >> 3);
   constexpr int G = 4;
   const int group = b / (G * tiles_n);
@@ -444,9 +448,9 @@ __device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o, char *sX
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tmi, tni;
   if constexpr (GATED)
-    tile_coords((p.M + TM - 1) / TM, (p.part_rows + TN / 2 - 1) / (TN / 2), tmi, tni);
+    tile_coords(blockIdx.x, (p.M + TM - 1) / TM, (p.part_rows + TN / 2 - 1) / (TN / 2), tmi, tni);
   else
-    tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
+    tile_coords(blockIdx.x, (p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
   const int m0 = tmi * TM, n0 = tni * (GATED ? TN / 2 : TN);
 
   const int K = p.Kc;
@@ -764,7 +768,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   }
   const int tid = threadIdx.x, lane = tid & 63;
   int tmi, tni;
-  tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
+  tile_coords(blockIdx.x, (p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
   const int m0 = tmi * TM, k0 = tni * TN;
 
   const int N = p.Kc, K = p.No;
@@ -1039,15 +1043,43 @@ __device__ __forceinline__ void mask_lora(const uint32_t (&keep)[4][2], f32x16_t
     }
 }
 
-template <int CT, bool EXT>
+// Partial sums of a split dX: accumulators acc[i][j] of wave w of tile t, split s, go to
+// part[((s tiles + t) 4 + w) 16 + 4 i + j] as four 16-byte pieces a lane ([g][lane]), so that
+// every store and the join's loads cover 1 KB contiguously.  32 x 32 blocks past M or K hold
+// nothing and are skipped on both sides.
+constexpr int kPartBlock = 32 * 32;  // floats of one accumulator block
+__device__ __forceinline__ int64_t part_index(int tiles, int split, int tile, int wave, int i, int j) {
+  return ((static_cast<int64_t>(split) * tiles + tile) * 4 + wave) * 16 + 4 * i + j;
+}
+__device__ __forceinline__ void store_dx_part(const GemmParams &p, float *part, int split, int tile, int tb, int cb,
+                                              const f32x16_t (&acc)[4][4]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float *const base = part + part_index(p.tiles, split, tile, wave, 0, 0) * kPartBlock;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (tb + 32 * i >= p.M || cb + 32 * j >= p.No) continue;
+      f32x4_t *dst = reinterpret_cast<f32x4_t *>(base + (4 * i + j) * kPartBlock) + lane;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        dst[64 * g] = f32x4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int CT, bool EXT, bool SPLIT = false>
 __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, char *sW1, char *sY0,
                                              char *sY1) {
   // the workgroups after the tiles (dispatched last, so in CUs the tiles have left) do
   // the finalize job that rides in this launch
-  if (static_cast<int>(blockIdx.x) >= p.tiles) {
-    finalize_part(p.fin, blockIdx.x - p.tiles, p.fin_wgs);
+  const int tile_wgs = SPLIT ? p.tiles * x.splits : p.tiles;
+  if (static_cast<int>(blockIdx.x) >= tile_wgs) {
+    finalize_part(p.fin, blockIdx.x - tile_wgs, p.fin_wgs);
     return;
   }
+  const int split = SPLIT ? static_cast<int>(blockIdx.x) / p.tiles : 0;
+  const int tile = static_cast<int>(blockIdx.x) - split * p.tiles;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // 2 x 2 waves: wave w computes tokens 128 (w / 2) .. + 128 and output columns
@@ -1055,7 +1087,7 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   const int wr = wave >> 1, wc = wave & 1;
   char *const sYw[2] = {sY0 + wave * YWAVE_BYTES, sY1 + wave * YWAVE_BYTES};
   int tmi, tni;
-  tile_coords((p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
+  tile_coords(tile, (p.M + TM - 1) / TM, (p.No + TN - 1) / TN, tmi, tni);
   const int m0 = tmi * TM, k0 = tni * TN;
 
   // contraction over weight rows (EXT: over the padded column blocks of dY that stand for
@@ -1064,8 +1096,11 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   const __amdgpu_buffer_rsrc_t rdy = make_rsrc(p.A, static_cast<uint32_t>(uint64_t(p.M) * N * 2));
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.w.codes, static_cast<uint32_t>(uint64_t(NW) * K / 2));
   const ConstRsrc rq = make_const_rsrc<CT>(p.w, static_cast<uint32_t>(uint64_t(NW) * K / 64));
-  const int nk = (N + TK - 1) / TK;
+  // this workgroup's contraction steps: from kb on, nk of them
+  const int kb = SPLIT ? split * x.ksteps * TK : 0;
+  const int nk = SPLIT ? min((N + TK - 1) / TK - split * x.ksteps, x.ksteps) : (N + TK - 1) / TK;
   const int last = nk - 1;
+  const int r = SPLIT && split > 0 ? 0 : p.r;
 
   // dY loads: load q of a step writes rows 8 q .. 8 q + 7 of the wave's slice (1 KB,
   // lane l at byte 16 l), so lane l fetches the chunk that belongs at slot l % 8 of
@@ -1144,15 +1179,15 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   CodeStageB S0, S1;
-  issue_codes(0, S0);
-  issue_codes(min(1, last) * TK, S1);
-  issue_y(Ic<1>{}, 0, sYw[0]);
+  issue_codes(kb, S0);
+  issue_codes(kb + min(1, last) * TK, S1);
+  issue_y(Ic<1>{}, kb, sYw[0]);
   // The LoRA term first, while the first tiles' loads are in flight.  Up to 64 ranks
   // with 16-byte aligned rows: the V tile of the 256 tokens (zeros past r) is loaded
   // into the second dY stage laid out like a dY stage and read with the same fragment
   // reads (sub-step s: ranks 16 s .. 16 s + 15); each wave loads only its own output
   // columns' At fragments.  Otherwise the rank steps load both operands from memory.
-  const bool lds_lora = p.r > 0 && p.r <= TK && (p.r % 8) == 0;
+  const bool lds_lora = r > 0 && r <= TK && (r % 8) == 0;
   u32x4_t wl[4][4];
   if (lds_lora) {
     const __amdgpu_buffer_rsrc_t rv = make_rsrc(p.A2, static_cast<uint32_t>(uint64_t(p.M) * p.r * 2));
@@ -1170,14 +1205,14 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         wl[s][j] = lora_frag(rb, true, k0 + 128 * wc + j * 32 + (lane & 31), p.No, p.r, 16 * s + (lane >> 5) * 8, p.r);
-  } else if (p.r > 0) {
+  } else if (r > 0) {
     lora_steps_dx(p, m0 + 128 * wr, k0 + 128 * wc, acc);
   }
   uint32_t keep[4][2];
   if constexpr (EXT) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) keep[i][0] = keep[i][1] = ~0u;
-    if (x.drop.thr != 0) keep_bits(drop_key(x.drop), m0 + 128 * wr, k0 + 128 * wc, K, keep);
+    if (x.drop.thr != 0 && split == 0) keep_bits(drop_key(x.drop), m0 + 128 * wr, k0 + 128 * wc, K, keep);
   }
   {
     const Planes pd = make_planes(const_value<CT>(S0.c), p.lvl);
@@ -1222,7 +1257,7 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
     char *swn = b2 ? sW0 : sW1;
     const char *sy = b2 ? sY1 : sY0;
     const char *syn = b2 ? sY0 : sY1;
-    const int kt1 = min(it + 1, last) * TK, kt2 = min(it + 2, last) * TK;
+    const int kt1 = kb + min(it + 1, last) * TK, kt2 = kb + min(it + 2, last) * TK;
     Planes pd;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -1284,13 +1319,57 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   if (it + 1 < nk) step(Ic<1>{}, Ic<1>{}, it + 1, S0, S1);
   if (it + 2 < nk) step(Ic<0>{}, Ic<1>{}, it + 2, S1, S0);
   __builtin_amdgcn_s_waitcnt(0);
-  if (p.No % 8 == 0) {
+  if constexpr (SPLIT) {
+    store_dx_part(p, x.part, split, tile, m0 + 128 * wr, k0 + 128 * wc, acc);
+  } else if (EXT || p.No % 8 == 0) {  // (K is a multiple of 64)
     static_assert(64 * kOutPitchDx <= TILE_BYTES, "output staging");
     __syncthreads();  // every wave is done reading the weight tiles and dY stages
     char *const reg = wave == 0 ? sW0 : wave == 1 ? sW1 : wave == 2 ? sY0 : sY1;
     store_out_dx_lds(p, m0 + 128 * wr, k0 + 128 * wc, acc, reg);
   } else {
     store_out_dx(p, m0 + 128 * wr, k0 + 128 * wc, acc);
+  }
+}
+
+// The join of a split dX: a wave adds, in split order, the partial sums of 32 tokens x 128
+// columns (block row i of wave w of tile t), rounds once and writes whole 256-byte rows
+// through LDS.  Workgroup 4 t + w, wave i.
+__global__ __launch_bounds__(NT) void dx_join_kernel(const float *__restrict__ part, int splits, int tiles, int M,
+                                                     int K, uint16_t *__restrict__ dX) {
+  __shared__ __attribute__((aligned(16))) char stage[4][32 * kOutPitchDx];
+  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+  const int tile = blockIdx.x >> 2, w = blockIdx.x & 3;
+  int tmi, tni;
+  tile_coords(tile, (M + TM - 1) / TM, (K + TN - 1) / TN, tmi, tni);
+  const int tb = tmi * TM + 128 * (w >> 1) + 32 * i, cb = tni * TN + 128 * (w & 1);
+  if (tb >= M || cb >= K) return;
+  char *const reg = stage[i];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (cb + 32 * j >= K) break;
+    f32x4_t s[4];
+    for (int k = 0; k < splits; ++k) {
+      const f32x4_t *src = reinterpret_cast<const f32x4_t *>(part + part_index(tiles, k, tile, w, i, j) * kPartBlock) + lane;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t v = src[64 * g];
+        s[g] = k == 0 ? v : s[g] + v;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<u32x2_t *>(reg + (lane & 31) * kOutPitchDx + (j * 32 + g * 8 + (lane >> 5) * 4) * 2) =
+          u32x2_t{pack_bf16x2(s[g][0], s[g][1]), pack_bf16x2(s[g][2], s[g][3])};
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes have landed
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int tok = 4 * q + (lane >> 4), ch = lane & 15;
+    const int m = tb + tok, col = cb + ch * 8;  // K is a multiple of 64
+    if (m >= M || col >= K) continue;
+    const u32x2_t lo = *reinterpret_cast<const u32x2_t *>(reg + tok * kOutPitchDx + ch * 16);
+    const u32x2_t hi = *reinterpret_cast<const u32x2_t *>(reg + tok * kOutPitchDx + ch * 16 + 8);
+    *reinterpret_cast<u32x4_t *>(dX + static_cast<int64_t>(m) * K + col) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
   }
 }
 
@@ -1313,6 +1392,15 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void
   __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
   __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
   dx_pipe_body<CT, true>(p, x, sW0, sW1, sY0, sY1);
+}
+template <int CT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_split_kernel(
+    GemmParams p, DxExt x) {
+  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
+  dx_pipe_body<CT, true, true>(p, x, sW0, sW1, sY0, sY1);
 }
 
 bool fits_32bit(int64_t M, int64_t N, int64_t K, int r) {
@@ -1406,9 +1494,43 @@ hipError_t launch_gemm_gated(const WeightView &w, const uint16_t *X, int64_t M, 
   return hipGetLastError();
 }
 
+namespace {
+// Splits of the extended dX GEMM's contraction: the tiles of 256 x 256 alone leave CUs idle
+// when there are few tokens.  A step of the tile costs about 1.6 us and a workgroup about
+// 8 us around its steps; the partial sums are written and read once (256 KB a workgroup at
+// about 4.5 TB/s over the card) and joined by one more launch of about 5 us.  The number of
+// splits minimises that sum (1000 x 24576 -> 8192: 128 tiles, 2 splits, 642 -> 374 us).
+struct DxSplit {
+  int splits, ksteps;
+};
+DxSplit dx_split(int64_t M, int64_t K, int64_t Kc) {
+  const int64_t tiles = ((M + TM - 1) / TM) * ((K + TN - 1) / TN), nk = (Kc + TK - 1) / TK;
+  DxSplit best{1, static_cast<int>(nk)};
+  if (tiles >= 256) return best;
+  double best_cost = 1.6 * nk + 8.0;
+  const double kb = double(M) * K * 8.0 / 4.5e6;  // us per split of partial sums, written and read
+  for (int64_t s = 2; s * tiles <= 512 && s * 2 <= nk; ++s) {
+    const int64_t steps = (nk + s - 1) / s, used = (nk + steps - 1) / steps;
+    const double rounds = double((tiles * used + 255) / 256);
+    const double cost = rounds * (1.6 * steps + 8.0) + 5.0 + kb * used;
+    if (cost < best_cost - 1e-9) {
+      best_cost = cost;
+      best = {static_cast<int>(used), static_cast<int>(steps)};
+    }
+  }
+  return best;
+}
+}  // namespace
+
+size_t gemm_dx_ext_workspace(int64_t M, int64_t K, int64_t Kc) {
+  const DxSplit sp = dx_split(M, K, Kc);
+  const int64_t tiles = ((M + TM - 1) / TM) * ((K + TN - 1) / TN);
+  return sp.splits > 1 ? static_cast<size_t>(sp.splits) * tiles * TM * TN * sizeof(float) : 0;
+}
+
 hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M, int parts, const uint16_t *V,
-                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, hipStream_t stream,
-                              const FinalizeJob *fin) {
+                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, float *part,
+                              hipStream_t stream, const FinalizeJob *fin) {
   const int64_t Np = w.n_rows / parts, half = (Np + 7) / 8 * 8, Kc = parts > 1 ? parts * half : half;
   if (w.n_rows % parts != 0 || (parts > 2 && half != Np)) return hipErrorInvalidValue;
   if (!fits_32bit(M, Kc, w.n_cols, r) || M > 0x7fffffff) return hipErrorInvalidValue;
@@ -1417,16 +1539,27 @@ hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M
     p.fin = *fin;
     p.fin_wgs = static_cast<int>(finalize_workgroups(*fin));
   }
-  if (int64_t(p.tiles) + p.fin_wgs > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(p.tiles + p.fin_wgs));
+  const DxSplit sp = dx_split(M, w.n_cols, Kc);
+  if (int64_t(p.tiles) * sp.splits + p.fin_wgs > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(p.tiles * sp.splits + p.fin_wgs));
   // without padding the column blocks are the contraction as it is
-  const DxExt x{d, static_cast<int>(half == Np ? Kc : half), static_cast<int>(half - Np)};
+  const DxExt x{d, static_cast<int>(half == Np ? Kc : half), static_cast<int>(half - Np), sp.splits, sp.ksteps, part};
+  auto go = [&](auto whole, auto split) {
+    if (sp.splits > 1)
+      hipLaunchKernelGGL(split, grid, dim3(NT), 0, stream, p, x);
+    else
+      hipLaunchKernelGGL(whole, grid, dim3(NT), 0, stream, p, x);
+  };
   switch (w.const_type) {
-    case kConstDqInt8: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstDqInt8>, grid, dim3(NT), 0, stream, p, x); break;
-    case kConstDqFp8: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstDqFp8>, grid, dim3(NT), 0, stream, p, x); break;
-    case kConstF32: hipLaunchKernelGGL(gemm_dx_ext_kernel<kConstF32>, grid, dim3(NT), 0, stream, p, x); break;
+    case kConstDqInt8: go(gemm_dx_ext_kernel<kConstDqInt8>, gemm_dx_split_kernel<kConstDqInt8>); break;
+    case kConstDqFp8: go(gemm_dx_ext_kernel<kConstDqFp8>, gemm_dx_split_kernel<kConstDqFp8>); break;
+    case kConstF32: go(gemm_dx_ext_kernel<kConstF32>, gemm_dx_split_kernel<kConstF32>); break;
     default: return hipErrorInvalidValue;
   }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || sp.splits == 1) return e;
+  hipLaunchKernelGGL(dx_join_kernel, dim3(static_cast<unsigned>(4 * p.tiles)), dim3(NT), 0, stream, part, sp.splits,
+                     p.tiles, static_cast<int>(M), static_cast<int>(w.n_cols), dX);
   return hipGetLastError();
 }
 

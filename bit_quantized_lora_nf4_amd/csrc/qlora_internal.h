@@ -218,9 +218,12 @@ hipError_t launch_gated_grad(const uint16_t *dH, const uint16_t *Y, int64_t M, i
                              hipStream_t stream);
 // The same with the dropout mask of X on the LoRA term, dX = bf16(dY . W' + m (V . At^T)),
 // and with dY given in `parts` column blocks of round_up(Np, 8) columns each (Np = N /
-// parts; the padding columns hold zeros), so that odd part heights keep 16-byte rows.
+// parts; the padding columns hold zeros), so that odd part heights keep 16-byte rows.  `part`
+// holds gemm_dx_ext_workspace(M, K, parts round_up(Np, 8)) bytes: with few output tiles the
+// contraction is split and a second launch joins the fp32 partial sums in a fixed order.
+size_t gemm_dx_ext_workspace(int64_t M, int64_t K, int64_t Kc);
 hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M, int parts, const uint16_t *V,
-                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, hipStream_t stream,
-                              const FinalizeJob *fin);
+                              const uint16_t *At, int r, uint16_t *dX, const Dropout &d, float *part,
+                              hipStream_t stream, const FinalizeJob *fin);
 
 }  // namespace qlora

@@ -72,10 +72,13 @@ def test_masked_staging_waits(lora_asm):
         assert found == 1, (name, found)
 
 
+@pytest.mark.parametrize("kernel", ["gemm_dx_ext", "gemm_dx_split"])
 @pytest.mark.parametrize("ct", [0, 1, 2])
-def test_ext_dx_barrier_waits(gemm_asm, ct):
-    name = re.search(r"^(_Z\S*gemm_dx_ext_kernelILi%d\S*):" % ct, gemm_asm, re.M).group(1)
-    ev = _events(gemm_asm, name)
+def test_ext_dx_barrier_waits(gemm_asm, ct, kernel):
+    name = re.search(r"^(_Z\S*%s_kernelILi%d\S*):" % (kernel, ct), gemm_asm, re.M).group(1)
+    # the whole function: an early exit's s_endpgm may come first in the text
+    body = re.search(r"^" + re.escape(name) + r":.*?^\.Lfunc_end", gemm_asm, re.S | re.M).group(0)
+    ev = _events(body.replace("s_endpgm", "") + "\ns_endpgm", name)
     waits = _barrier_waits(ev)
     assert len(waits) >= 4
     for i, n in waits:
@@ -141,7 +144,7 @@ def test_gemv_ext_x_stage_waits(tmp_path_factory):
 
 
 def test_no_register_spills(gemm_asm, lora_asm):
-    for asm, pat in ((gemm_asm, "gemm_dx_ext"), (gemm_asm, "gemm_gated"), (lora_asm, "drop_")):
+    for asm, pat in ((gemm_asm, "gemm_dx_ext"), (gemm_asm, "gemm_dx_split"), (gemm_asm, "gemm_gated"), (lora_asm, "drop_")):
         sizes = dict(re.findall(r"\.name:\s+(\S*" + pat + r"\S*kernel\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)",
                                 asm, re.S))
         assert len(sizes) >= 3, sizes
