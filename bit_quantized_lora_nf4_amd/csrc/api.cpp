@@ -424,20 +424,27 @@ qlora::CopyJob unpad_rank(const uint16_t *src, uint16_t *dst, int64_t rows, int 
   return {src, dst, rows, r, r, round8(r), r};
 }
 
+// U, the fp32 partial sums of the down-projection, the padded operands, and the fp32 partial
+// sums of a split forward.
 struct DropFwdLayout {
-  size_t u = 0, part = 0, total = 0;
+  size_t u = 0, part = 0, mid = 0, total = 0;
   PadLayout pad;
 };
-DropFwdLayout drop_fwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts) {
+DropFwdLayout drop_fwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts, bool gated) {
   DropFwdLayout L;
-  if (r == 0) return L;
-  const int R8 = parts * round8(r);
+  const size_t mid = qlora::mid_takes(M, K, N, gated) ? qlora::gemm_mid_workspace(M, K, N, gated) : 0;
+  if (r == 0 && mid == 0) return L;
   size_t off = qlora::kGemvSyncBytes;
-  L.u = off;
-  off += align_up(size_t(M) * R8 * 2);
-  L.part = off;
-  off += align_up(qlora::lora_down_workspace(M, K, R8));
-  L.pad = pad_layout(off, K, N, r, parts);
+  if (r > 0) {
+    const int R8 = parts * round8(r);
+    L.u = off;
+    off += align_up(size_t(M) * R8 * 2);
+    L.part = off;
+    off += align_up(qlora::lora_down_workspace(M, K, R8));
+    L.pad = pad_layout(off, K, N, r, parts);
+  }
+  L.mid = off;
+  off += align_up(mid);
   L.total = off;
   return L;
 }
@@ -542,8 +549,8 @@ int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
     if (p && !aligned16(p)) return fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
   const int64_t K = w->n_cols, N = w->n_rows;
   const int r8 = round8(r), R8 = parts * r8;
-  const bool small = qlora::gemv_shape_ok(M, N);
-  const DropFwdLayout L = drop_fwd_layout(M, K, N, r, parts);
+  const bool small = qlora::gemv_takes(M, K, N, parts * r, false);
+  const DropFwdLayout L = drop_fwd_layout(M, K, N, r, parts, false);
   s = check_workspace(who, workspace, workspace_bytes, small ? qlora::gemv_workspace(M, K, N, parts * r) : L.total);
   if (s != QLORA_OK) return s;
   const qlora::WeightView wv = view(w);
@@ -572,6 +579,12 @@ int fwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
     s = launched(qlora::launch_copy_rows(&job, 1, st), "unpad(U)");
     if (s != QLORA_OK) return s;
   }
+  if (qlora::mid_takes(M, K, N, false))
+    return launched(timed_launch(st, [&] {
+                      return qlora::launch_gemm_mid(wv, X, M, U, R8, B8, r8, part_rows, false, 0, nullptr, Y,
+                                                    reinterpret_cast<float *>(ws + L.mid), st);
+                    }),
+                    "gemm_mid");
   return launched(
       timed_launch(st, [&] { return qlora::launch_gemm_fwd(wv, X, M, U, R8, B8, r8, part_rows, Y, st); }),
       "gemm_fwd");
@@ -698,8 +711,8 @@ static_assert(QLORA_ACT_SILU == int(qlora::kActSilu) && QLORA_ACT_GELU_TANH == i
 // The small-M path's workspace, or U, partial sums and padded operands (none without an
 // adapter).
 size_t gated_fwd_bytes(int64_t M, int64_t K, int64_t P, int r) {
-  return qlora::gemv_shape_ok(M, 2 * P) ? qlora::gemv_ext_workspace(M, K, 2 * P, r, 2)
-                                        : drop_fwd_layout(M, K, 2 * P, r, 2).total;
+  return qlora::gemv_takes(M, K, 2 * P, 2 * r, true) ? qlora::gemv_ext_workspace(M, K, 2 * P, r, 2)
+                                        : drop_fwd_layout(M, K, 2 * P, r, 2, true).total;
 }
 
 int gated_fwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *X, int64_t M, const uint16_t *A,
@@ -720,7 +733,7 @@ int gated_fwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *X
   s = check_workspace(who, workspace, workspace_bytes, gated_fwd_bytes(M, K, P, r));
   if (s != QLORA_OK) return s;
   const qlora::WeightView wv = view(w);
-  const bool small = qlora::gemv_shape_ok(M, N);
+  const bool small = qlora::gemv_takes(M, K, N, 2 * r, true);
   if (small ? !qlora::gemv_supported(wv, M, 2 * r)
             : !qlora::gemm_supported(wv, M, R8) || (r > 0 && !qlora::drop_shape_ok(M, K, R8)))
     return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
@@ -738,9 +751,9 @@ int gated_fwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *X
                     "gemv");
   const uint16_t *A8 = nullptr, *B8 = nullptr;
   uint16_t *U = nullptr;
+  char *ws = static_cast<char *>(workspace);
+  const DropFwdLayout L = drop_fwd_layout(M, K, N, r, 2, true);
   if (r > 0) {
-    char *ws = static_cast<char *>(workspace);
-    const DropFwdLayout L = drop_fwd_layout(M, K, N, r, 2);
     U = U_saved && r8 == r ? U_saved : reinterpret_cast<uint16_t *>(ws + L.u);
     s = drop_down(X, M, K, N, A, B, r, 2, scale, d, ws, L.pad, L.part, U, &A8, &B8, st);
     if (s != QLORA_OK) return s;
@@ -750,6 +763,12 @@ int gated_fwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *X
       if (s != QLORA_OK) return s;
     }
   }
+  if (qlora::mid_takes(M, K, N, true))
+    return launched(timed_launch(st, [&] {
+                      return qlora::launch_gemm_mid(wv, X, M, U, R8, B8, r8, 0, true, act, H, Y_saved,
+                                                    reinterpret_cast<float *>(ws + L.mid), st);
+                    }),
+                    "gemm_mid");
   return launched(
       timed_launch(st, [&] { return qlora::launch_gemm_gated(wv, X, M, U, R8, B8, r8, act, H, Y_saved, st); }),
       "gemm_gated");
@@ -943,7 +962,7 @@ size_t qlora_workspace_bytes_dropout(int op, int64_t M, int64_t K, int64_t N, in
   if ((op != 0 && op != 1) || M < 1 || K < 1 || N < 1 || K % 64 != 0 || r < 1 || n_parts < 1 ||
       n_parts > QLORA_MAX_PARTS || N % n_parts != 0 || int64_t(n_parts) * round8(r) > QLORA_MAX_RANK)
     return base;
-  const size_t need = op == 0 ? drop_fwd_layout(M, K, N, r, n_parts).total
+  const size_t need = op == 0 ? drop_fwd_layout(M, K, N, r, n_parts, false).total
                               : drop_bwd_layout(M, K, N, r, n_parts, (N / n_parts) % 8 != 0).total;
   return need > base ? need : base;
 }

@@ -39,6 +39,7 @@
 // forward's activations, and the four waves split the output tile 2 x 2.
 
 #include "device_common.h"
+#include "gemm_tile.h"
 #include "qlora_internal.h"
 
 namespace qlora {
@@ -80,11 +81,6 @@ struct DxExt {
   int splits, ksteps;
   float *part;
 };
-
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
-// byte offset of 16-byte chunk c of row `row` in a swizzled 256 x 64 bf16 tile
-__device__ __forceinline__ int tile_off(int row, int c) { return row * 128 + ((c ^ swz(row)) << 4); }
 
 // ---- activation tile staging: 256 rows x 64 columns, 8 chunks of 16 B per thread ----
 struct ActStage {
@@ -354,21 +350,6 @@ __device__ __forceinline__ void store_gated(const GemmParams &p, const GatedOut 
     }
     __syncthreads();  // read back before the next half overwrites it
   }
-}
-
-// Map the linear workgroup id to (token tile, output tile): workgroups are dispatched
-// round-robin over the 8 XCDs, so consecutive tiles of the grouped raster order are
-// given to the same XCD (sharing its L2); groups of 4 token tiles sweep the outputs.
-__device__ __forceinline__ void tile_coords(int b, int tiles_m, int tiles_n, int &tm, int &tn) {
-  const int T = tiles_m * tiles_n;
-  if ((T & 7) == 0) b = (b & 7) * (T >> 3) + (b >> 3);
-  constexpr int G = 4;
-  const int group = b / (G * tiles_n);
-  const int first = group * G;
-  const int gsize = min(tiles_m - first, G);
-  const int in = b - group * G * tiles_n;
-  tm = first + in % gsize;
-  tn = in / gsize;
 }
 
 // ===================================== forward =====================================

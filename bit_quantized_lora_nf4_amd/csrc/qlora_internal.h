@@ -212,6 +212,18 @@ hipError_t launch_gemm_dx(const WeightView &w, const uint16_t *dY, int64_t M, co
 // NULL, receives bf16 [G | L] [M, 2 P].
 hipError_t launch_gemm_gated(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *U, int ldu,
                              const uint16_t *Bl, int r, int act, uint16_t *H, uint16_t *Y, hipStream_t stream);
+// The same two forwards on tiles of 128 weight rows, with the contraction split when the
+// tiles are few (`part`: gemm_mid_workspace bytes): Y [M, N] as launch_gemm_fwd, or (gated)
+// H and Y as launch_gemm_gated.  r % 8 == 0.
+// mid_takes: whether this shape runs on them (else on the 256 x 256 tiles).
+bool mid_takes(int64_t M, int64_t K, int64_t N, bool gated);
+// gemv_takes: whether a small-M call with dropout or gate runs on launch_gemv_ext (else on
+// the above).
+bool gemv_takes(int64_t M, int64_t K, int64_t N, int r, bool gated);
+size_t gemm_mid_workspace(int64_t M, int64_t K, int64_t N, bool gated);
+hipError_t launch_gemm_mid(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *U, int ldu,
+                           const uint16_t *Bl, int r, int64_t part_rows, bool gated, int act, uint16_t *H, uint16_t *Y,
+                           float *part, hipStream_t stream);
 // [dG | dL] = [dH L act'(G) | dH act(G)] from the saved bf16 [G | L] (Y [M, 2 P]), as bf16
 // rows of two column blocks of round_up(P, 8) columns, zeros in the padding.
 hipError_t launch_gated_grad(const uint16_t *dH, const uint16_t *Y, int64_t M, int64_t P, int act, uint16_t *dY,

@@ -319,8 +319,9 @@ int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, v
  *   s the logistic function (gated SiLU and the tanh form of gated GELU).
  * Y_saved (nullable) receives bf16 [G | L] and U_saved (nullable) U, both for the backward;
  * a call that only needs H passes NULL.  2 round_up(r, 8) <= 256.
- * Workspace: qlora_workspace_bytes_gated(0, M, K, P, r).  M <= 16 and P <= 32768: one
- * launch (the small-M path); the workspace's header rule above applies. */
+ * Workspace: qlora_workspace_bytes_gated(0, M, K, P, r).  Calls of up to 16 tokens on all
+ * but the largest weights take one launch (the small-M path); the workspace's header rule
+ * above applies. */
 typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU_TANH = 1 } qlora_act;
 size_t qlora_workspace_bytes_gated(int op, int64_t M, int64_t K, int64_t P, int r);
 int qlora_gated_fwd(const qlora_nf4_weight *w, const uint16_t *X, int64_t M, const uint16_t *A, const uint16_t *B,

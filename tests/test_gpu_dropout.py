@@ -91,6 +91,8 @@ CASES = [
     (70, 512, 136, 256, 1, 0.1),      # the largest rank
     (300, 320, 256, 16, 3, 0.1), (65, 256, 256, 12, 2, 0.5), (33, 192, 256, 8, 4, 0.1), (5, 256, 512, 64, 2, 0.1),
     (530, 2048, 776, 64, 1, 0.1),     # several workgroups of every kind
+    (20, 64, 1000, 8, 1, 0.1), (40, 704, 130, 40, 1, 0.1), (100, 320, 513, 72, 1, 0.1),
+    (50, 448, 512, 72, 3, 0.1),       # parts of stacked ranks that straddle 64-rank tiles
 ]
 
 

@@ -97,6 +97,11 @@ CASES = [
     (300, 512, 320, 16, "silu", 0.1), (257, 320, 129, 0, "gelu_tanh", 0.0), (333, 320, 501, 12, "gelu_tanh", 0.25),
     (200, 256, 72, 1, "silu", 0.0), (130, 256, 136, 80, "silu", 0.1), (70, 512, 136, 128, "silu", 0.0),
     (65, 256, 1000, 20, "silu", 0.5), (530, 1024, 776, 64, "silu", 0.1),
+    # every remainder of the contraction's four-step groups, with and without splits; one to
+    # three blocks of 32 tokens; both parts' ranks in one and in several 64-rank tiles
+    (18, 64, 2200, 8, "silu", 0.0), (31, 320, 70, 32, "silu", 0.0), (40, 448, 65, 40, "gelu_tanh", 0.0),
+    (64, 704, 3000, 16, "silu", 0.0), (96, 576, 130, 96, "silu", 0.1), (129, 2112, 40, 8, "silu", 0.0),
+    (20, 17408, 33, 8, "silu", 0.0),  # more than 256 steps: always split
 ]
 
 
@@ -135,9 +140,10 @@ def test_gated_number_types(q, M, quant, const):
 
 
 def test_saved_y_is_the_fused_linear(q):
-    """[G | L] is bit for bit what the horizontally fused linear gives on the same weight."""
+    """On the tiles that the horizontally fused linear runs on, [G | L] is bit for bit what it
+    gives for the same weight (smaller calls take other tiles, which sum in another order)."""
     import torch
-    M, K, P, r = 300, 512, 512, 16
+    M, K, P, r = 700, 2048, 5632, 16
     h = inputs(M, K, P, r, seed=2)
     dev = {k: gc.dev_bf16(v) for k, v in h.items()}
     qw = q.quantize(dev["W"])

@@ -114,6 +114,35 @@ def test_gated_barrier_waits(gemm_asm, ct):
     assert checked >= 3
 
 
+def test_mid_barrier_waits(tmp_path_factory):
+    """The smaller forward tiles: in the main loop, which alternates barriers that publish two
+    X tiles each, the wait at a barrier may leave in flight only the codes issued after those
+    tiles' loads; no kernel spills."""
+    asm = _asm(tmp_path_factory, "gemm_mid")
+    kernels = re.findall(r"^(_Z\S*gemm_mid_kernelILi(\d)ELb\dELi(\d)ELb\d\S*):", asm, re.M)
+    assert len(kernels) == 36, len(kernels)
+    for name, ct, ni in kernels:
+        body = re.search(r"^" + re.escape(name) + r":.*?^\.Lfunc_end", asm, re.S | re.M).group(0)
+        lines = [ln.strip() for ln in body.splitlines()]
+        labels = {m.group(1): i for i, ln in enumerate(lines) if (m := re.match(r"^(\.LBB\S+):", ln))}
+        loops = [lines[labels[m.group(2)]:i + 1] for i, ln in enumerate(lines)
+                 if (m := _BR.search(ln)) and m.group(2) in labels and labels[m.group(2)] < i]
+        loop = max((x for x in loops if _dma(x) == 8 * int(ni)), key=len)
+        # twice around: every wait has the loads of the iteration before it behind it
+        pending, seen = [], 0
+        for ln in loop + loop:
+            if _VMEM.match(ln):
+                pending.append("D" if ln.endswith(" lds") else "R")
+            elif m := re.match(r"s_waitcnt vmcnt\((\d+)\) lgkmcnt\(0\)$", ln):
+                n = int(m.group(1))
+                left = pending[len(pending) - n:] if n else []
+                assert "D" not in left, (name, n, left)
+                pending, seen = left, seen + 1
+        assert seen == 8, (name, seen)
+    sizes = re.findall(r"\.name:\s+(\S*gemm_mid_\S*kernel\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)", asm, re.S)
+    assert len(sizes) == 42 and all(int(n) <= 16 for _, n in sizes), sizes
+
+
 def test_gemv_ext_x_stage_waits(tmp_path_factory):
     asm = _asm(tmp_path_factory, "gemv")
     # gemv_ext_kernel<CT, XLDS = false, MULTI, DIRECT, XDMA = true>
