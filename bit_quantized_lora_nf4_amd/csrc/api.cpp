@@ -471,11 +471,11 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts,
     off += align_up(size_t(K) * R8 * 2);
     L.part = off;
     size_t p = qlora::reduce_m_workspace(M, K, R8);
-    const size_t others[] = {qlora::lora_down_workspace(M, K, R8), qlora::vdb_workspace_v(M, Np, r8)};
+    const size_t others[] = {qlora::lora_down_workspace(M, K, R8), parts * qlora::vdb_workspace_v(M, Np, r8)};
     for (size_t o : others) p = o > p ? o : p;
     off += align_up(p);
     L.part2 = off;
-    off += align_up(qlora::vdb_workspace_db(M, Np, r8));
+    off += align_up(parts * qlora::vdb_workspace_db(M, Np, r8));
     L.pad = pad_layout(off, K, N, r, parts);
     if (r % 8 != 0) {
       L.da = off;
@@ -622,13 +622,10 @@ int bwd_blocks(const qlora_nf4_weight *w, int parts, const uint16_t *dY, int64_t
       dA8 = reinterpret_cast<uint16_t *>(ws + L.da);
       dB8 = reinterpret_cast<uint16_t *>(ws + L.db);
     }
-    for (int q = 0; q < parts && s == QLORA_OK; ++q) {
-      const bool at = dX && q == 0;
-      s = launched(qlora::launch_vdb(dY + q * ldp, M, Np, ldy, B8 + q * Np * r8, U + q * r8, R8, r8, scale, V + q * r8,
-                                     dB8 + q * Np * r8, part, part2, at ? A8 : nullptr, R8, K, at ? At : nullptr, st,
-                                     ldp != Np),
-                   "lora(V, dB)");
-    }
+    // V, dB and A^T (for the dX GEMM's rank steps) of all parts
+    s = launched(qlora::launch_vdb_parts(parts, dY, M, Np, ldp, ldy, B8, U, r8, scale, V, dB8, part, part2,
+                                         dX ? A8 : nullptr, K, dX ? At : nullptr, st),
+                 "lora(V, dB)");
     if (s == QLORA_OK)
       s = launched(d.thr ? qlora::launch_reduce_m_drop(X, M, K, V, R8, part, dA8, d, st, dX ? &fin : nullptr)
                          : qlora::launch_reduce_m(X, M, K, K, V, R8, R8, part, dA8, true, st, dX ? &fin : nullptr),

@@ -1312,46 +1312,40 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   }
 }
 
-// The join of a split dX: a wave adds, in split order, the partial sums of 32 tokens x 128
-// columns (block row i of wave w of tile t), rounds once and writes whole 256-byte rows
-// through LDS.  Workgroup 4 t + w, wave i.
+// The join of a split dX: a wave adds one 32 x 32 block's partial sums in split order (the
+// loads of four splits in flight at a time: with few tiles and many splits the chain of
+// loads is what the join waits for), rounds once and writes four columns a lane.
 __global__ __launch_bounds__(NT) void dx_join_kernel(const float *__restrict__ part, int splits, int tiles, int M,
                                                      int K, uint16_t *__restrict__ dX) {
-  __shared__ __attribute__((aligned(16))) char stage[4][32 * kOutPitchDx];
-  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
-  const int tile = blockIdx.x >> 2, w = blockIdx.x & 3;
+  const int lane = threadIdx.x & 63;
+  const int unit = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 6);
+  const int j = unit & 3, i = (unit >> 2) & 3, w = (unit >> 4) & 3, tile = unit >> 6;
   int tmi, tni;
   tile_coords(tile, (M + TM - 1) / TM, (K + TN - 1) / TN, tmi, tni);
-  const int tb = tmi * TM + 128 * (w >> 1) + 32 * i, cb = tni * TN + 128 * (w & 1);
+  const int tb = tmi * TM + 128 * (w >> 1) + 32 * i, cb = tni * TN + 128 * (w & 1) + 32 * j;
   if (tb >= M || cb >= K) return;
-  char *const reg = stage[i];
+  const f32x4_t *src = reinterpret_cast<const f32x4_t *>(part + part_index(tiles, 0, tile, w, i, j) * kPartBlock) + lane;
+  const int64_t pitch = static_cast<int64_t>(tiles) * 64 * (kPartBlock / 4);
+  f32x4_t s[4];
+  for (int k = 0; k < splits; k += 4) {
+    f32x4_t v[4][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (cb + 32 * j >= K) break;
-    f32x4_t s[4];
-    for (int k = 0; k < splits; ++k) {
-      const f32x4_t *src = reinterpret_cast<const f32x4_t *>(part + part_index(tiles, k, tile, w, i, j) * kPartBlock) + lane;
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t v = src[64 * g];
-        s[g] = k == 0 ? v : s[g] + v;
+      for (int g = 0; g < 4; ++g) v[u][g] = src[min(k + u, splits - 1) * pitch + 64 * g];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k + u < splits) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) s[g] = k + u == 0 ? v[u][g] : s[g] + v[u][g];
       }
-    }
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      *reinterpret_cast<u32x2_t *>(reg + (lane & 31) * kOutPitchDx + (j * 32 + g * 8 + (lane >> 5) * 4) * 2) =
-          u32x2_t{pack_bf16x2(s[g][0], s[g][1]), pack_bf16x2(s[g][2], s[g][3])};
   }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes have landed
+  const int m = tb + (lane & 31);
+  if (m >= M) return;
+  uint16_t *row = dX + static_cast<int64_t>(m) * K + cb + (lane >> 5) * 4;  // K is a multiple of 64
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int tok = 4 * q + (lane >> 4), ch = lane & 15;
-    const int m = tb + tok, col = cb + ch * 8;  // K is a multiple of 64
-    if (m >= M || col >= K) continue;
-    const u32x2_t lo = *reinterpret_cast<const u32x2_t *>(reg + tok * kOutPitchDx + ch * 16);
-    const u32x2_t hi = *reinterpret_cast<const u32x2_t *>(reg + tok * kOutPitchDx + ch * 16 + 8);
-    *reinterpret_cast<u32x4_t *>(dX + static_cast<int64_t>(m) * K + col) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-  }
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<u32x2_t *>(row + 8 * g) = u32x2_t{pack_bf16x2(s[g][0], s[g][1]), pack_bf16x2(s[g][2], s[g][3])};
 }
 
 template <int CT>
@@ -1539,7 +1533,7 @@ hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.splits == 1) return e;
-  hipLaunchKernelGGL(dx_join_kernel, dim3(static_cast<unsigned>(4 * p.tiles)), dim3(NT), 0, stream, part, sp.splits,
+  hipLaunchKernelGGL(dx_join_kernel, dim3(static_cast<unsigned>(16 * p.tiles)), dim3(NT), 0, stream, part, sp.splits,
                      p.tiles, static_cast<int>(M), static_cast<int>(w.n_cols), dX);
   return hipGetLastError();
 }

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr uint64_t k4G = 0xFFFFFFF0ull;
+constexpr int kMaxVdbParts = 8;  // = QLORA_MAX_PARTS
 constexpr int64_t kDownWGs = 256;  // lora_down workgroups aimed at (one per CU)
 
 // ---------------------------------------------------------------------------------
@@ -557,6 +558,44 @@ __global__ __launch_bounds__(NT) void down_reduce_partial_kernel(DownArgs d, Red
   }
 }
 
+// The same for several parts of stacked adapters in one launch: part q's dY columns start q
+// ldp after the first part's, its B rows q Np, its U and V columns q r; the partial sums of
+// each product are laid out part after part.
+struct PartStrides {
+  int parts;
+  int64_t in, wt, s, pv, pdb;  // elements between the parts of dY, B, U and the partial sums
+};
+template <int RT>
+__global__ __launch_bounds__(NT) void vdb_parts_kernel(DownArgs d, ReduceArgs q, int nd, int nq, TransposeJob tj,
+                                                       PartStrides ps) {
+  __shared__ __attribute__((aligned(16))) char sbuf[staged_bytes<RT>()];
+  const int per = nd + nq, part = static_cast<int>(blockIdx.x) / per;
+  const int b = static_cast<int>(blockIdx.x) - part * per;
+  if (part >= ps.parts) {
+    transpose_tile(tj, static_cast<int>(blockIdx.x) - ps.parts * per, reinterpret_cast<uint16_t(*)[72]>(sbuf));
+  } else if (b < nd) {
+    lora_down_dma_body<RT, staged_nb<RT>(), true>(sbuf, b % d.gx, b / d.gx, d.IN + part * ps.in, d.M, d.Kc, d.ldin,
+                                                   d.WT + part * ps.wt, d.ldwt, d.r, d.KR, d.P + part * ps.pv);
+  } else {
+    const int c = b - nd;
+    reduce_m_dma_body<RT, false, staged_nb<RT>()>(sbuf, c % q.gx, c / q.gx, q.IN + part * ps.in, q.M, q.No, q.ldin,
+                                                   q.S + part * ps.s, q.lds, q.r, q.MR, q.P + part * ps.pdb);
+  }
+}
+struct FinalizeJobs {
+  FinalizeJob j[2 * kMaxVdbParts];
+  int n;
+};
+__global__ __launch_bounds__(NT) void finalize_parts_kernel(FinalizeJobs jobs, int64_t total) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * NT) {
+    int64_t at = i;
+    int k = 0;
+    while (k + 1 < jobs.n && at >= jobs.j[k].count / 4) at -= jobs.j[k++].count / 4;
+    finalize_one(jobs.j[k], at);
+  }
+}
+
 // OUT = bf16(scale * sum_s P[s]) for the `count` partial sums (count % 4 == 0) laid out
 // as rows of `cols` values (cols % 4 == 0), written with row pitch ldout; fixed order
 // (split_sum in device_common.h).
@@ -945,9 +984,9 @@ size_t vdb_workspace_db(int64_t M, int64_t Np, int r) {
 
 hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, const uint16_t *B, const uint16_t *U,
                       int64_t ldu, int r, float scale, uint16_t *V, uint16_t *dB, float *ws_v, float *ws_db,
-                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream, bool padded) {
+                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream) {
   const int rt = (r + 31) / 32;
-  if (rt < 1 || rt > 8 || !vdb_fast(M, Np, ldy, ldu, r, padded)) return hipErrorInvalidValue;
+  if (rt < 1 || rt > 8 || !vdb_fast(M, Np, ldy, ldu, r)) return hipErrorInvalidValue;
   const DownSplit sd = down_split(M, Np);
   const MSplit sq = m_split(M, Np);
   DownArgs d{dY, static_cast<int>(M), static_cast<int>(Np), static_cast<int>(ldy), B, r, r,
@@ -977,6 +1016,51 @@ hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, co
   int64_t blocks = ((fv.count + fb.count) / 4 + NT - 1) / NT;
   if (blocks > 4096) blocks = 4096;
   hipLaunchKernelGGL(finalize2_kernel, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream, fv, fb);
+  return hipGetLastError();
+}
+
+hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
+                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, uint16_t *dB,
+                            float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
+                            hipStream_t stream) {
+  const int rt = (r + 31) / 32, R = parts * r;
+  if (rt < 1 || rt > 8 || parts < 1 || parts > kMaxVdbParts || !vdb_fast(M, Np, ldy, R, r, true))
+    return hipErrorInvalidValue;
+  const DownSplit sd = down_split(M, Np);
+  const MSplit sq = m_split(M, Np);
+  DownArgs d{dY, static_cast<int>(M), static_cast<int>(Np), static_cast<int>(ldy), B, r, r,
+             sd.KR, ws_v, static_cast<int>((M + 63) / 64)};
+  ReduceArgs q{dY, static_cast<int>(M), static_cast<int>(Np), static_cast<int>(ldy), U, R, r,
+               sq.MR, ws_db, static_cast<int>((Np + 63) / 64)};
+  const TransposeJob tj{A, At, R, KA, (KA + 63) / 64};
+  const PartStrides ps{parts, ldp, Np * r, r, int64_t(sd.ksplit) * M * r, int64_t(sq.splits) * Np * r};
+  const int64_t nd = int64_t(d.gx) * sd.ksplit, nq = int64_t(q.gx) * sq.splits;
+  const int64_t nt = (A && At) ? ((int64_t(R) + 63) / 64) * tj.tiles_c : 0;
+  if (parts * (nd + nq) + nt > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(parts * (nd + nq) + nt)), block(NT);
+  switch (rt) {
+#define QLORA_CASE(T)                                                                                     \
+  case T:                                                                                                 \
+    hipLaunchKernelGGL(vdb_parts_kernel<T>, grid, block, 0, stream, d, q, static_cast<int>(nd),           \
+                       static_cast<int>(nq), tj, ps);                                                     \
+    break;
+    QLORA_CASE(1) QLORA_CASE(2) QLORA_CASE(3) QLORA_CASE(4)
+    QLORA_CASE(5) QLORA_CASE(6) QLORA_CASE(7) QLORA_CASE(8)
+#undef QLORA_CASE
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  FinalizeJobs jobs;
+  jobs.n = 2 * parts;
+  int64_t total = 0;
+  for (int p = 0; p < parts; ++p) {
+    jobs.j[2 * p] = FinalizeJob{ws_v + p * ps.pv, sd.ksplit, M * r, r, R, scale, V + p * r};
+    jobs.j[2 * p + 1] = FinalizeJob{ws_db + p * ps.pdb, sq.splits, Np * r, Np * r, Np * r, 1.0f, dB + p * Np * r};
+    total += (M + Np) * r / 4;
+  }
+  int64_t blocks = (total + NT - 1) / NT;
+  if (blocks > 4096) blocks = 4096;
+  hipLaunchKernelGGL(finalize_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream, jobs, total);
   return hipGetLastError();
 }
 

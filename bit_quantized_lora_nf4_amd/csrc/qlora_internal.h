@@ -141,15 +141,24 @@ hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const
 // row pitch ldy (a column slice of width Np), B is [Np, r] (dense rows) and U [M, r]
 // with row pitch ldu.  If A and At are given, the same launch also writes At[KA, RA] =
 // A[RA, KA]^T.  Needs the fast-path shapes (vdb_fast) and the two fp32 partial regions
-// sized by vdb_workspace_v / vdb_workspace_db.  `padded`: dY's rows hold zeros in columns
-// Np .. round_up(Np, 8) - 1 of the slice, and Np need not be a multiple of 8.
+// sized by vdb_workspace_v / vdb_workspace_db.  vdb_fast's `padded`: dY's rows hold zeros in
+// columns Np .. round_up(Np, 8) - 1 of the slice, and Np need not be a multiple of 8
+// (launch_vdb_parts).
 bool vdb_fast(int64_t M, int64_t Np, int64_t ldy, int64_t ldu, int r, bool padded = false);
 size_t vdb_workspace_v(int64_t M, int64_t Np, int r);
 size_t vdb_workspace_db(int64_t M, int64_t Np, int r);
 hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, const uint16_t *B, const uint16_t *U,
                       int64_t ldu, int r, float scale, uint16_t *V, uint16_t *dB, float *ws_v, float *ws_db,
-                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream,
-                      bool padded = false);
+                      const uint16_t *A, int64_t RA, int64_t KA, uint16_t *At, hipStream_t stream);
+
+// launch_vdb for `parts` stacked parts at once (one launch and one finalize): part q's dY
+// columns are [q ldp, q ldp + Np) of rows of pitch ldy (zeros up to the next multiple of 8),
+// B [parts Np, r], U and V [M, parts r], dB [parts Np, r]; the partial regions are `parts`
+// times vdb_workspace_v / vdb_workspace_db; At[KA, parts r] = A^T if both are given.
+hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
+                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, uint16_t *dB,
+                            float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
+                            hipStream_t stream);
 
 // AdamW step (fp32 parameter and moments, bf16 gradient, optional bf16 parameter copy).
 struct AdamConsts {
