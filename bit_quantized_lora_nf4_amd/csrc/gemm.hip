@@ -1130,13 +1130,10 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   const int dn = tid & 63, dc = (tid >> 6) * 64;
   const bool col_ok = k0 + dc < K;
   auto issue_codes = [&](int kt, CodeStageB &cs) {
+    // EXT: padding positions of the first block take rows of the second one, times zeros
     int n = kt + dn;
-    bool ok = col_ok && n < N;
-    if constexpr (EXT) {
-      const int nb = n < x.half ? n : n - x.half;  // position within its column block
-      ok = ok && nb < x.half - x.skip;
-      n = n < x.half ? n : n - x.skip;
-    }
+    if constexpr (EXT) n -= n >= x.half ? x.skip : 0;
+    const bool ok = col_ok && n < NW;
     const uint32_t off = static_cast<uint32_t>(n) * (K / 2) + (k0 + dc) / 2;
     cs.code[0] = buf_load16(rc, ok ? off : kOOB);
     cs.code[1] = buf_load16(rc, ok ? off + 16 : kOOB);
