@@ -172,12 +172,15 @@ __global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
     go[0] = __uint_as_float(buf_load4(rq.o, grp0 * 4u));
     go[1] = __uint_as_float(buf_load4(rq.o, grp1 * 4u));
   }
+  // the 8-bit codes as aligned dwords: from the dword that holds the array's first byte (the
+  // array may start anywhere) to the one that holds its last
+  const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.w.absmax_q)) & 3u;
   const __amdgpu_buffer_rsrc_t r8 =
-      make_rsrc(p.w.absmax_q, static_cast<uint32_t>((uint64_t(p.N) * K / 64 + 3) & ~uint64_t(3)));
+      make_rsrc(p.w.absmax_q - mis, static_cast<uint32_t>((uint64_t(p.N) * K / 64 + mis + 3) & ~uint64_t(3)));
   // c' (rounded once) of the block of step it = 4 a + 2 jp + half
   auto constant = [&](const Codes<CT> &cs, int jp, int it) {
     if constexpr (CT == kConstF32) return __uint_as_float(half ? cs.q[2 * jp + 1] : cs.q[2 * jp]);
-    const uint32_t first = b0 + (it - 2 * jp - half);
+    const uint32_t first = b0 + (it - 2 * jp - half) + mis;
     const uint32_t four = __builtin_amdgcn_alignbit(cs.q[1], cs.q[0], (first & 3u) * 8u);
     const bool low = ((b0 + it) >> 8) == grp0;
     return __builtin_fmaf(c8_value<CT>((four >> (8 * (2 * jp + half))) & 0xFFu), low ? gs[0] : gs[1],
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
     if constexpr (CT == kConstF32)
       cs.q = buf_load16(rq.s, b * 4u);
     else
-      cs.q = buf_load8(r8, b & ~3u);
+      cs.q = buf_load8(r8, (b + mis) & ~3u);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto issue_x = [&](int it) {

@@ -57,6 +57,19 @@ def test_dropout_empty_and_special_values(q):
     assert np.all(y[~m] == 0.0) and np.all(np.isnan(y[m]))
 
 
+def test_dropout_past_four_gib(q):
+    """A bf16 tensor of more than 4 GiB, in place: the mask around byte 2^32 and at the end."""
+    import torch
+    n = (1 << 31) + 12345
+    d = q.Dropout(0.5, seed=3, offset=8)
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    q.dropout(x, d, out=x)
+    for first in (0, (1 << 31) - 4096, n - 9000):
+        k = min(8192, n - first)
+        m = od.keep((k,), 0.5, 3, 8, first=first)
+        assert np.array_equal(x[first:first + k].float().cpu().numpy(), np.where(m, 2.0, 0.0))
+
+
 def test_counter_is_added_on_the_device(q):
     import torch
     x = torch.ones(1000, device="cuda")
@@ -127,10 +140,11 @@ def test_linear_dropout(q, M, K, Np, r, parts, p):
 
 
 @pytest.mark.parametrize("quant,const", [(0, 1), (0, 2), (1, 0), (1, 2)])
-def test_linear_dropout_number_types(q, quant, const):
+@pytest.mark.parametrize("M", [6, 150])
+def test_linear_dropout_number_types(q, M, quant, const):
     """Other level tables and block constants: against the same operator on the same stored
     weight, the dequantized weight as the reference's W'."""
-    M, K, N, r, p = 150, 256, 200, 16, 0.2
+    K, N, r, p = 320, 200, 16, 0.2
     print(f"types {quant} {const}", flush=True)
     h = dc.linear_inputs(M, K, N, r, 1, seed=5 + quant + const)
     dev = {k: gc.dev_bf16(v) for k, v in h.items()}
@@ -235,6 +249,35 @@ def test_captured_graph_draws_new_masks(q):
         seen.append(got["U"])
     assert not torch.equal(seen[0], seen[1])
     assert int(counter.item()) == 4
+
+
+def test_nothing_outside_the_outputs_is_written(q):
+    """Rows behind every output's last one, and the bytes behind a workspace of exactly the
+    documented size, stay as they were (aligned and padded rank and height)."""
+    import torch
+    for M, K, N, r, parts in ((5, 256, 72, 8, 1), (70, 256, 101, 12, 1), (300, 512, 512, 16, 2)):
+        h = dc.linear_inputs(M, K, N // parts, r, parts, seed=15)
+        dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+        qw = q.quantize(dev["W"])
+        d = q.Dropout(0.2, seed=5)
+        rows = dict(Y=M, U=M, dX=M, dA=parts * r, dB=N)
+        cols = dict(Y=N, U=parts * r, dX=K, dA=K, dB=r)
+        whole = {k: torch.full((rows[k] + 5, cols[k]), 9.0, dtype=torch.bfloat16, device="cuda") for k in rows}
+        o = {k: whole[k][:rows[k]] for k in whole}
+        sizes = [q.qlora_workspace_bytes_dropout(op, M, K, N, r, parts) for op in (0, 1)]
+        bufs = [torch.zeros(n + 4096, dtype=torch.uint8, device="cuda") for n in sizes]
+        for b, n in zip(bufs, sizes):
+            b[n:] = 0xA5
+        q.linear_fwd_fused(qw, parts, dev["X"], dev["A"], dev["B"], ALPHA, Y=o["Y"], U=o["U"],
+                           ws=bufs[0][:sizes[0]], dropout=d)
+        q.linear_bwd_fused(qw, parts, dev["dY"], dev["X"], dev["A"], dev["B"], ALPHA, o["U"], dX=o["dX"], dA=o["dA"],
+                           dB=o["dB"], ws=bufs[1][:sizes[1]], dropout=d)
+        torch.cuda.synchronize()
+        for k, t in whole.items():
+            assert bool((t[rows[k]:] == 9.0).all()), (M, k)
+            assert bool(torch.isfinite(t[:rows[k]]).all()), (M, k)
+        for b, n in zip(bufs, sizes):
+            assert bool((b[n:] == 0xA5).all()), M
 
 
 def test_two_streams(q):

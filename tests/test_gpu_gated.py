@@ -91,7 +91,7 @@ CASES = [
     (1, 64, 1, 0, "silu", 0.0), (1, 64, 8, 8, "silu", 0.0), (1, 512, 320, 16, "silu", 0.1),
     (3, 256, 101, 12, "gelu_tanh", 0.25), (5, 1024, 77, 4, "silu", 0.0), (16, 256, 256, 64, "gelu_tanh", 0.0),
     (16, 4096, 2050, 8, "silu", 0.0), (9, 2048, 515, 128, "silu", 0.1), (2, 4096, 40, 16, "silu", 0.3),
-    (16, 8192, 136, 1, "silu", 0.0),
+    (16, 8192, 136, 1, "silu", 0.0), (16, 8192, 136, 8, "silu", 0.1), (2, 8192, 4100, 24, "gelu_tanh", 0.1),
     # tiled path
     (17, 64, 1, 1, "silu", 0.0), (17, 128, 7, 8, "silu", 0.1), (64, 192, 128, 64, "gelu_tanh", 0.05),
     (300, 512, 320, 16, "silu", 0.1), (257, 320, 129, 0, "gelu_tanh", 0.0), (333, 320, 501, 12, "gelu_tanh", 0.25),
@@ -130,7 +130,7 @@ def test_gated(q, M, K, P, r, act, p):
 @pytest.mark.parametrize("quant,const", [(0, 1), (0, 2), (1, 0), (1, 2)])
 @pytest.mark.parametrize("M", [4, 140])
 def test_gated_number_types(q, M, quant, const):
-    K, P, r, p = 256, 200, 16, 0.2
+    K, P, r, p = 320, 200, 16, 0.2  # five blocks a row: no row starts on a dword of constants
     h = inputs(M, K, P, r, seed=9 + quant + const)
     dev = {k: gc.dev_bf16(v) for k, v in h.items()}
     qw = q.quantize(dev["W"], quant_type=quant, const_type=const)
@@ -279,6 +279,86 @@ def test_small_m_workspace_is_left_ready(q):
             if key in want:
                 assert all(torch.equal(a, b) for a, b in zip(want[key], (H, Y, U, L)))
             want[key] = tuple(t.clone() for t in (H, Y, U, L))
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_constants_at_any_address(q, M):
+    """The 8-bit block constants need no alignment: the same results from every start."""
+    import torch
+    K, P, r = 320, 72, 8
+    h = inputs(M, K, P, r, seed=5)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.2, seed=5)
+    want = run(q, qw, dev, r, "silu", d)
+    n = qw.absmax_q.numel()
+    for off in (1, 2, 3):
+        buf = torch.full((n + 8,), -77, dtype=torch.int8, device="cuda")
+        buf[off:off + n] = qw.absmax_q
+        q2 = q.NF4Weight(qw.codes, buf[off:off + n], qw.dq_scale, qw.dq_offset, qw.n_rows, qw.n_cols)
+        for a, b in zip(want, run(q, q2, dev, r, "silu", d)):
+            assert torch.equal(a, b), off
+
+
+@pytest.mark.parametrize("M,K,P,r", [(5, 256, 72, 8), (40, 256, 71, 12), (300, 512, 129, 16)])
+def test_nothing_outside_the_outputs_is_written(q, M, K, P, r):
+    """Rows behind the last one of every output, and the bytes behind a workspace of exactly
+    the documented size, stay as they were."""
+    import torch
+    h = inputs(M, K, P, r, seed=15)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.2, seed=5)
+    mk = lambda rows, cols: torch.full((rows + 5, cols), 9.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    whole = dict(H=mk(M, P), Y=mk(M, 2 * P), U=mk(M, 2 * r), dX=mk(M, K), dA=mk(2 * r, K), dB=mk(2 * P, r))
+    rows = dict(H=M, Y=M, U=M, dX=M, dA=2 * r, dB=2 * P)
+    o = {k: whole[k][:rows[k]] for k in whole}
+    sizes = [q.qlora_workspace_bytes_gated(op, M, K, P, r) for op in (0, 1)]
+    bufs = [torch.zeros(n + 4096, dtype=torch.uint8, device="cuda") for n in sizes]
+    for b, n in zip(bufs, sizes):
+        b[n:] = 0xA5
+    q.gated_fwd(qw, dev["X"], dev["A"], dev["B"], ALPHA, dropout=d, ws=bufs[0][:sizes[0]], H=o["H"], Y=o["Y"], U=o["U"])
+    q.gated_bwd(qw, dev["dH"], o["Y"], dev["X"], dev["A"], dev["B"], ALPHA, o["U"], dropout=d, ws=bufs[1][:sizes[1]],
+                dX=o["dX"], dA=o["dA"], dB=o["dB"])
+    torch.cuda.synchronize()
+    for k, t in whole.items():
+        assert bool((t[rows[k]:] == 9.0).all()), k
+        assert bool(torch.isfinite(t[:rows[k]]).all()), k
+    for b, n in zip(bufs, sizes):
+        assert bool((b[n:] == 0xA5).all())
+
+
+def test_tensors_near_four_gib(q):
+    """[G | L] and its gradient of almost 4 GiB: byte offsets past 31 bits.  The first and the
+    last rows against the definition."""
+    import torch
+    M, K, P, r = 48000, 64, 22016, 8
+    h = inputs(16, K, P, r, seed=77)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    X = dev["X"].repeat(M // 16, 1)
+    dH = dev["dH"].repeat(M // 16, 1)
+    d = q.Dropout(0.25, seed=3)
+    H, Y, U = q.gated_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+    dX, dA, dB = q.gated_bwd(qw, dH, Y, X, dev["A"], dev["B"], ALPHA, U, dropout=d)
+    torch.cuda.synchronize()
+    Wd = dc.weight64(qw)
+    Xf, A, B, dHf = dc.f64(h, "X", "A", "B", "dH")
+    from oracle import dropout as od
+    for first in (0, M - 16):
+        m = od.keep((16, K), 0.25, 3, 0, first=first * K).astype(np.float64)
+        c = od.scale(0.25)
+        rY, eY, rU, eU = dc.forward(Xf, Wd, A, B, ALPHA, r, 2, m, c)
+        sl = slice(first, first + 16)
+        dc.check("Y", dc.bits(Y[sl]), rY, eY + dc.H * (np.abs(rY) + eY))
+        rH = og.forward(rY, "silu")
+        eH = h_bound("silu", rY, eY)
+        dc.check("H", dc.bits(H[sl]), rH, eH + dc.H * (np.abs(rH) + eH))
+        Yd = dc.bits(Y[sl])
+        dY = og.backward(dHf, Yd, "silu")
+        want = dc.backward(dY, grad_bound("silu", dHf, Yd, dY), Xf, Wd, A, B, ALPHA, r, 2, m, c, dc.bits(U[sl]))
+        dc.check("dX", dc.bits(dX[sl]), *want["dX"])
+    assert bool(torch.isfinite(dA).all()) and bool(torch.isfinite(dB).all())
 
 
 def test_feed_forward_block_training_step(q):
