@@ -285,7 +285,8 @@ size_t qlora_workspace_bytes_dropout(int op, int64_t M, int64_t K, int64_t N, in
  *   Y_q = bf16(X . W_q'^T + U_q . B_q^T)
  * The base product sees X itself.  m X is exact and c enters with alpha / r (one fp32
  * factor), so D(X) itself is never rounded.  drop NULL or t = 0: the call without dropout,
- * bit for bit.  Further requirement with dropout: n_parts round_up(r, 8) <= 256. */
+ * bit for bit.  Further requirements with dropout: n_parts round_up(r, 8) <= 256, and no
+ * tensor larger than 0xFFFFFFF0 bytes (QLORA_ERR_SHAPE before anything is launched). */
 int qlora_linear_fwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *X, int64_t M,
                              const uint16_t *A, const uint16_t *B, int r, float alpha, const qlora_drop *drop,
                              uint16_t *Y, uint16_t *U_saved, void *workspace, size_t workspace_bytes,
@@ -318,7 +319,8 @@ int qlora_dropout(const void *X, int dtype, int64_t n, const qlora_drop *drop, v
  *   act: QLORA_ACT_SILU x s(x); QLORA_ACT_GELU_TANH x s(2 sqrt(2 / pi) (x + 0.044715 x^3)),
  *   s the logistic function (gated SiLU and the tanh form of gated GELU).
  * Y_saved (nullable) receives bf16 [G | L] and U_saved (nullable) U, both for the backward;
- * a call that only needs H passes NULL.  2 round_up(r, 8) <= 256.
+ * a call that only needs H passes NULL.  2 round_up(r, 8) <= 256, and no tensor larger
+ * than 0xFFFFFFF0 bytes, [G | L] included (QLORA_ERR_SHAPE before anything is launched).
  * Workspace: qlora_workspace_bytes_gated(0, M, K, P, r).  Calls of up to 16 tokens on all
  * but the largest weights take one launch (the small-M path); the workspace's header rule
  * above applies. */

@@ -280,6 +280,39 @@ def test_nothing_outside_the_outputs_is_written(q):
             assert bool((b[n:] == 0xA5).all()), M
 
 
+def test_tensors_near_four_gib(q):
+    """X and dX of almost 4 GiB: mask indexes and byte offsets past 31 bits.  The first and
+    the last rows against the definition."""
+    import torch
+    K, N, r, parts, p = 8192, 256, 8, 1, 0.25
+    M = 262128  # 16 rows short of 2^32 bytes
+    h = dc.linear_inputs(16, K, N, r, parts, seed=78)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    X = dev["X"].repeat(M // 16, 1)
+    dY = dev["dY"].repeat(M // 16, 1)
+    d = q.Dropout(p, seed=4)
+    Y, U = q.linear_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+    dX, dA, dB = q.linear_bwd(qw, dY, X, dev["A"], dev["B"], ALPHA, U, dropout=d)
+    torch.cuda.synchronize()
+    Wd = dc.weight64(qw)
+    Xf, A, B, dYf = dc.f64(h, "X", "A", "B", "dY")
+    c = od.scale(p)
+    for first in (0, M - 16):
+        m = od.keep((16, K), p, 4, 0, first=first * K).astype(np.float64)
+        rY, eY, rU, eU = dc.forward(Xf, Wd, A, B, ALPHA, r, parts, m, c)
+        sl = slice(first, first + 16)
+        dc.check("Y", dc.bits(Y[sl]), rY, eY + dc.H * (np.abs(rY) + eY))
+        dc.check("U", dc.bits(U[sl]), rU, eU)
+        want = dc.backward(dYf, np.zeros_like(dYf), Xf, Wd, A, B, ALPHA, r, parts, m, c, dc.bits(U[sl]))
+        dc.check("dX", dc.bits(dX[sl]), *want["dX"])
+    assert bool(torch.isfinite(dA).all()) and bool(torch.isfinite(dB).all())
+    # one row more than 2^32 - 16 bytes hold is refused before anything runs
+    big = torch.empty((1 << 18, K), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(Exception, match="32-bit"):
+        q.linear_fwd(qw, big, dev["A"], dev["B"], ALPHA, dropout=d)
+
+
 def test_two_streams(q):
     """Two calls at once on two streams with a workspace each."""
     import torch

@@ -328,6 +328,62 @@ def test_nothing_outside_the_outputs_is_written(q, M, K, P, r):
         assert bool((b[n:] == 0xA5).all())
 
 
+SHAPES = [(5, 256, 72, 8), (40, 256, 71, 12), (300, 512, 129, 16), (700, 512, 5632, 16)]
+
+
+@pytest.mark.parametrize("M,K,P,r", SHAPES)
+def test_workspace_contents_do_not_matter(q, M, K, P, r):
+    """A workspace of NaN patterns behind its header gives what a zeroed one gives."""
+    import torch
+    h = inputs(M, K, P, r, seed=25)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.2, seed=6)
+    outs = []
+    for fill in (0, 0xFF):
+        ws = [torch.full((q.qlora_workspace_bytes_gated(op, M, K, P, r),), fill, dtype=torch.uint8, device="cuda")
+              for op in (0, 1)]
+        for w in ws:
+            w[:65792] = 0
+        H, Y, U = q.gated_fwd(qw, dev["X"], dev["A"], dev["B"], ALPHA, dropout=d, ws=ws[0])
+        outs.append((H, Y, U) + q.gated_bwd(qw, dev["dH"], Y, dev["X"], dev["A"], dev["B"], ALPHA, U, dropout=d,
+                                            ws=ws[1]))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+@pytest.mark.parametrize("M,K,P,r", SHAPES)
+def test_nan_stays_in_its_row_and_out_of_dropped_places(q, M, K, P, r):
+    import torch
+    h = inputs(M, K, P, r, seed=26)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.3, seed=8)
+    H, Y, U, dX, dA, dB = run(q, qw, dev, r, "silu", d)
+    m, _ = dc.mask(M, K, 0.3, 8, 0)
+    i, j = M // 2, M - 1
+    rest = [n for n in range(M) if n not in (i, j)]
+    kept, dropped = int(np.flatnonzero(m[i])[0]), int(np.flatnonzero(m[j] == 0)[-1])
+    X = dev["X"].clone()
+    X[j, dropped] = float("nan")
+    # the adapter does not see a dropped element, whatever it is
+    H2, Y2, U2 = q.gated_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+    assert torch.equal(U2, U) and torch.equal(H2[:j], H[:j]) and torch.equal(Y2[:j], Y[:j])
+    assert bool(torch.isnan(Y2[j]).all())
+    for a, b in zip(q.gated_bwd(qw, dev["dH"], Y, X, dev["A"], dev["B"], ALPHA, U, dropout=d), (dX, dA, dB)):
+        assert torch.equal(a, b)
+    X[i, kept] = float("inf")
+    H2, Y2, U2 = q.gated_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+    for a, b in ((H2, H), (Y2, Y), (U2, U)):
+        assert torch.equal(a[rest], b[rest])
+    assert not bool(torch.isfinite(U2[i]).any())
+    dH = dev["dH"].clone()
+    dH[i, P // 2] = float("nan")
+    dX2, _, _ = q.gated_bwd(qw, dH, Y, dev["X"], dev["A"], dev["B"], ALPHA, U, dropout=d)
+    rest = [n for n in range(M) if n != i]
+    assert torch.equal(dX2[rest], dX[rest]) and bool(torch.isnan(dX2[i]).all())
+
+
 def test_tensors_near_four_gib(q):
     """[G | L] and its gradient of almost 4 GiB: byte offsets past 31 bits.  The first and the
     last rows against the definition."""
