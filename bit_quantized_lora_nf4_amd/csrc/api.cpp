@@ -449,11 +449,12 @@ DropFwdLayout drop_fwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts,
   return L;
 }
 
-// dY's padded copy (odd part heights), U [M, R8], V [M, R8], A^T [K, R8], the fp32 partial
-// sums, the padded operands and the padded gradients, the fp32 partial sums of a split dX.
+// dY's padded copy (odd part heights), U [M, R8], V [M, R8] and what its rounding took off,
+// A^T [K, R8], the fp32 partial sums, the padded operands and the padded gradients, the fp32 partial sums of a split dX.
 struct DropBwdLayout {
-  size_t dy = 0, u = 0, v = 0, at = 0, part = 0, part2 = 0, da = 0, db = 0, dx = 0, total = 0;
+  size_t dy = 0, u = 0, v = 0, vlo = 0, at = 0, part = 0, part2 = 0, da = 0, db = 0, dx = 0, total = 0;
   PadLayout pad;
+  int64_t lo() const { return static_cast<int64_t>((vlo - v) / 2); }  // elements from V to its remainder
 };
 DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts, bool own_dy) {
   DropBwdLayout L;
@@ -466,6 +467,8 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts,
     L.u = off;
     off += align_up(size_t(M) * R8 * 2);
     L.v = off;
+    off += align_up(size_t(M) * R8 * 2);
+    L.vlo = off;
     off += align_up(size_t(M) * R8 * 2);
     L.at = off;
     off += align_up(size_t(K) * R8 * 2);
@@ -623,13 +626,11 @@ int bwd_blocks(const qlora_nf4_weight *w, int parts, const uint16_t *dY, int64_t
       dB8 = reinterpret_cast<uint16_t *>(ws + L.db);
     }
     // V, dB and A^T (for the dX GEMM's rank steps) of all parts
-    s = launched(qlora::launch_vdb_parts(parts, dY, M, Np, ldp, ldy, B8, U, r8, scale, V, dB8, part, part2,
+    s = launched(qlora::launch_vdb_parts(parts, dY, M, Np, ldp, ldy, B8, U, r8, scale, V, L.lo(), dB8, part, part2,
                                          dX ? A8 : nullptr, K, dX ? At : nullptr, st),
                  "lora(V, dB)");
     if (s == QLORA_OK)
-      s = launched(d.thr ? qlora::launch_reduce_m_drop(X, M, K, V, R8, part, dA8, d, st, dX ? &fin : nullptr)
-                         : qlora::launch_reduce_m(X, M, K, K, V, R8, R8, part, dA8, true, st, dX ? &fin : nullptr),
-                   "reduce(dA)");
+      s = launched(qlora::launch_reduce_pair(X, M, K, V, L.lo(), R8, part, dA8, d, st, dX ? &fin : nullptr), "reduce(dA)");
     if (s != QLORA_OK) return s;
   }
   if (dX)
@@ -671,7 +672,7 @@ int bwd_dropout_impl(const char *who, const qlora_nf4_weight *w, int parts, cons
   const DropBwdLayout L = drop_bwd_layout(M, K, N, r, parts, copy);
   s = check_workspace(who, workspace, workspace_bytes, L.total);
   if (s != QLORA_OK) return s;
-  if (!qlora::gemm_supported(view(w), M, R8) || !qlora::drop_shape_ok(M, K, R8) ||
+  if (!qlora::gemm_supported(view(w), M, R8) || !qlora::pair_shape_ok(M, K, R8, L.lo()) ||
       uint64_t(M) * ldp * parts * 2 > 0xFFFFFFF0ull || !qlora::vdb_fast(M, Np, ldp * parts, R8, r8, copy))
     return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
                 (long long)M, (long long)K, (long long)N);
@@ -793,7 +794,7 @@ int gated_bwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *d
   s = check_workspace(who, workspace, workspace_bytes, L.total);
   if (s != QLORA_OK) return s;
   if (!qlora::gemm_supported(view(w), M, R8) || uint64_t(M) * ldp * 4 > 0xFFFFFFF0ull ||
-      (r > 0 && (!qlora::drop_shape_ok(M, K, R8) || !qlora::vdb_fast(M, P, 2 * ldp, R8, r8, true))))
+      (r > 0 && (!qlora::pair_shape_ok(M, K, R8, L.lo()) || !qlora::vdb_fast(M, P, 2 * ldp, R8, r8, true))))
     return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
                 (long long)M, (long long)K, (long long)N);
   s = check_device();

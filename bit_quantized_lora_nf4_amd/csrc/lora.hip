@@ -301,14 +301,18 @@ __global__ __launch_bounds__(NT) void drop_down_kernel(const uint16_t *__restric
 // column i of those four rows.  NB buffers, one barrier per 64-row step; wave w owns
 // output tiles w, w + 4, ... of the 2 x RT tiles of 32 x 32.
 
-template <int RT, bool JMAJOR, int NB, bool DROP = false>
+// PAIR: S is the sum of two bf16 matrices, the second one `lo_off` bytes behind the first
+// (same pitch); its tile is staged behind the first one's and multiplied into the same sums.
+template <int RT, bool JMAJOR, int NB, bool DROP = false, bool PAIR = false>
 __device__ __forceinline__ void reduce_m_dma_body(
     char *sbuf, int bx, int by, const uint16_t *__restrict__ IN, int M, int No, int ldin,
-    const uint16_t *__restrict__ S, int lds, int r, int MR, float *__restrict__ P, const Dropout &drop = Dropout{}) {
+    const uint16_t *__restrict__ S, int lds, int r, int MR, float *__restrict__ P, const Dropout &drop = Dropout{},
+    uint32_t lo_off = 0) {
   constexpr int INB = 64 * 128;        // IN tile bytes
   constexpr int SROW = 64 * RT;        // S tile row bytes
-  constexpr int BUF = INB + 64 * SROW;
-  constexpr int NLD = BUF / 1024;      // 1 KB loads per step (8 + 4 RT)
+  constexpr int SB = 64 * SROW;        // S tile bytes
+  constexpr int BUF = INB + (PAIR ? 2 : 1) * SB;
+  constexpr int NLD = BUF / 1024;      // 1 KB loads per step (8 + 4 RT, PAIR: 8 + 8 RT)
   constexpr int LPW = NLD / 4;
   constexpr int TILES = 2 * RT, TPW = (TILES + 3) / 4;
   const int lane = threadIdx.x & 63;
@@ -317,7 +321,8 @@ __device__ __forceinline__ void reduce_m_dma_body(
   const int mb = by * MR, me = min(M, mb + MR);
   const int nsteps = me > mb ? (me - mb + 63) / 64 : 0;
   const __amdgpu_buffer_rsrc_t rin = make_rsrc(IN, static_cast<uint32_t>(uint64_t(M) * ldin * 2));
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(S, static_cast<uint32_t>(uint64_t(M) * lds * 2));
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc(S, static_cast<uint32_t>(uint64_t(M) * lds * 2) + lo_off);
 
   // per-lane tile row and global column of this wave's loads: load g < 8 covers IN rows
   // 8 g .. 8 g + 7; the others cover 1 KB of the S tile
@@ -332,11 +337,13 @@ __device__ __forceinline__ void reduce_m_dma_body(
       lrow[u] = x;
       lcol[u] = nb0 + c * 8 < No ? static_cast<uint32_t>(nb0 + c * 8) * 2 : kOOB;
     } else {
-      const int byte = (g - 8) * 1024 + lane * 16;
+      const bool second = PAIR && g >= 8 + SB / 1024;
+      const int byte = (g - 8) * 1024 + lane * 16 - (second ? SB : 0);
       const int x = byte / SROW, slot = (byte % SROW) / 16;
       const int c = slot ^ s_swz<RT>(x);
       lrow[u] = x;
       lcol[u] = c * 8 < r ? static_cast<uint32_t>(c * 8) * 2 : kOOB;
+      if (second && c * 8 < r) lcol[u] += lo_off;
     }
   }
   auto dma = [&](int step) {
@@ -370,6 +377,9 @@ __device__ __forceinline__ void reduce_m_dma_body(
     return v;
   };
   auto frag_s = [&](const char *sb, int s, int cb) { return frag_rows<RT>(sb + INB, s, cb); };
+  auto mul = [](u32x4_t in, u32x4_t sv, f32x16_t c) {
+    return JMAJOR ? mfma32x32x16(in, sv, c) : mfma32x32x16(sv, in, c);
+  };
 
   f32x16_t acc[TPW];
 #pragma unroll
@@ -400,7 +410,7 @@ __device__ __forceinline__ void reduce_m_dma_body(
     }
     dma(i + NB - 1);
     const char *sb = sbuf + (i % NB) * BUF;
-    u32x4_t fi[TPW][4], fs[TPW][4];
+    u32x4_t fi[TPW][4], fs[TPW][4], fl[PAIR ? TPW : 1][4];
 #pragma unroll
     for (int u = 0; u < TPW; ++u) {
       const int tile = wave + 4 * u;
@@ -410,6 +420,7 @@ __device__ __forceinline__ void reduce_m_dma_body(
       for (int s = 0; s < 4; ++s) {
         fi[u][s] = frag_in(sb, s, 32 * tn);
         fs[u][s] = frag_s(sb, s, 32 * tj);
+        if constexpr (PAIR) fl[u][s] = frag_s(sb + SB, s, 32 * tj);
       }
     }
     __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead of the MFMAs
@@ -419,7 +430,8 @@ __device__ __forceinline__ void reduce_m_dma_body(
       for (int u = 0; u < TPW; ++u) {
         const int tile = wave + 4 * u;
         if (TILES % 4 != 0 && tile >= TILES) continue;
-        acc[u] = JMAJOR ? mfma32x32x16(fi[u][s], fs[u][s], acc[u]) : mfma32x32x16(fs[u][s], fi[u][s], acc[u]);
+        acc[u] = mul(fi[u][s], fs[u][s], acc[u]);
+        if constexpr (PAIR) acc[u] = mul(fi[u][s], fl[u][s], acc[u]);
       }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the kernel ends
@@ -447,13 +459,33 @@ __global__ __launch_bounds__(NT) void reduce_m_partial_kernel(
   reduce_m_dma_body<RT, JMAJOR, staged_nb<RT>()>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, ldin, S, lds, r, MR, P);
 }
 
-// dA's reduction over tokens with the dropout mask on X.
+// dA = V^T (m X) with V held as the sum of two bf16 matrices (16 significant bits), with or
+// without the dropout mask on X.  Buffers: as many as leave two workgroups a CU, at least two
+// (rank 128: two buffers and two workgroups 27.2 us, four buffers and one workgroup 34.0).
+template <int RT>
+constexpr int pair_nb() {
+  constexpr int buf = 8192 * (1 + RT), n = 80 * 1024 / buf;
+  return n > 4 ? 4 : n < 2 ? 2 : n;
+}
+template <int RT>
+constexpr int pair_bytes() {
+  return pair_nb<RT>() * 8192 * (1 + RT);
+}
 template <int RT>
 __global__ __launch_bounds__(NT) void drop_reduce_kernel(const uint16_t *__restrict__ IN, int M, int No,
-                                                         const uint16_t *__restrict__ S, int r, int MR,
-                                                         float *__restrict__ P, Dropout drop) {
-  __shared__ __attribute__((aligned(16))) char sbuf[staged_bytes<RT>()];
-  reduce_m_dma_body<RT, true, staged_nb<RT>(), true>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, No, S, r, r, MR, P, drop);
+                                                         const uint16_t *__restrict__ S, uint32_t lo_off, int r,
+                                                         int MR, float *__restrict__ P, Dropout drop) {
+  __shared__ __attribute__((aligned(16))) char sbuf[pair_bytes<RT>()];
+  reduce_m_dma_body<RT, true, pair_nb<RT>(), true, true>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, No, S, r, r, MR, P,
+                                                         drop, lo_off);
+}
+template <int RT>
+__global__ __launch_bounds__(NT) void pair_reduce_kernel(const uint16_t *__restrict__ IN, int M, int No,
+                                                         const uint16_t *__restrict__ S, uint32_t lo_off, int r,
+                                                         int MR, float *__restrict__ P) {
+  __shared__ __attribute__((aligned(16))) char sbuf[pair_bytes<RT>()];
+  reduce_m_dma_body<RT, true, pair_nb<RT>(), false, true>(sbuf, blockIdx.x, blockIdx.y, IN, M, No, No, S, r, r, MR, P,
+                                                          Dropout{}, lo_off);
 }
 
 // Transposes of bf16 matrices: OUT[C, R] = IN[R, C]^T.  A workgroup moves one 64 x 64
@@ -582,17 +614,34 @@ __global__ __launch_bounds__(NT) void vdb_parts_kernel(DownArgs d, ReduceArgs q,
                                                    q.S + part * ps.s, q.lds, q.r, q.MR, q.P + part * ps.pdb);
   }
 }
+// One finalize for all of them, V's and dB's in turn; V's also leave what their rounding
+// took off, rounded in its turn, `lo` elements further on.
 struct FinalizeJobs {
   FinalizeJob j[2 * kMaxVdbParts];
   int n;
+  int64_t lo;
 };
+__device__ __forceinline__ void finalize_v(const FinalizeJob &j, int64_t i, int64_t lo) {
+  const f32x4_t v = split_sum(j.P, j.splits, j.count, i) * j.scale;
+  const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  // exact differences: hi is within half a step of v (and NaN or infinity leave NaN)
+  const u32x2_t rest = {pack_bf16x2(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
+                        pack_bf16x2(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
+  const int64_t e = 4 * i, row = e / j.cols, col = e % j.cols;
+  uint16_t *const out = j.OUT + row * j.ldout + col;
+  *reinterpret_cast<u32x2_t *>(out) = hi;
+  *reinterpret_cast<u32x2_t *>(out + lo) = rest;
+}
 __global__ __launch_bounds__(NT) void finalize_parts_kernel(FinalizeJobs jobs, int64_t total) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * NT) {
     int64_t at = i;
     int k = 0;
     while (k + 1 < jobs.n && at >= jobs.j[k].count / 4) at -= jobs.j[k++].count / 4;
-    finalize_one(jobs.j[k], at);
+    if (k % 2 == 0)
+      finalize_v(jobs.j[k], at, jobs.lo);
+    else
+      finalize_one(jobs.j[k], at);
   }
 }
 
@@ -870,17 +919,27 @@ hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, cons
   return launch_finalize(ws, sp.ksplit, M * r, r, r, scale, OUT, stream);
 }
 
-hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *S, int r, float *partials,
-                                uint16_t *OUT, const Dropout &d, hipStream_t stream, FinalizeJob *defer) {
+bool pair_shape_ok(int64_t M, int64_t Kc, int r, int64_t lo) {
+  return drop_shape_ok(M, Kc, r) && uint64_t(lo) * 2 + uint64_t(M) * r * 2 <= k4G;
+}
+
+hipError_t launch_reduce_pair(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *V, int64_t lo, int r,
+                              float *partials, uint16_t *OUT, const Dropout &d, hipStream_t stream,
+                              FinalizeJob *defer) {
   if (defer) defer->splits = 0;
-  if (!drop_shape_ok(M, Kc, r) || d.thr == 0) return hipErrorInvalidValue;
+  if (!pair_shape_ok(M, Kc, r, lo)) return hipErrorInvalidValue;
   const MSplit sp = m_split(M, Kc);
   dim3 grid(static_cast<unsigned>((Kc + 63) / 64), static_cast<unsigned>(sp.splits)), block(NT);
+  const uint32_t lo_off = static_cast<uint32_t>(lo * 2);
   switch ((r + 31) / 32) {
-#define QLORA_CASE(T)                                                                                       \
-  case T:                                                                                                   \
-    hipLaunchKernelGGL(drop_reduce_kernel<T>, grid, block, 0, stream, IN, static_cast<int>(M),              \
-                       static_cast<int>(Kc), S, r, sp.MR, partials, d);                                     \
+#define QLORA_CASE(T)                                                                                      \
+  case T:                                                                                                  \
+    if (d.thr)                                                                                             \
+      hipLaunchKernelGGL(drop_reduce_kernel<T>, grid, block, 0, stream, IN, static_cast<int>(M),           \
+                         static_cast<int>(Kc), V, lo_off, r, sp.MR, partials, d);                          \
+    else                                                                                                   \
+      hipLaunchKernelGGL(pair_reduce_kernel<T>, grid, block, 0, stream, IN, static_cast<int>(M),           \
+                         static_cast<int>(Kc), V, lo_off, r, sp.MR, partials);                             \
     break;
     QLORA_CASE(1) QLORA_CASE(2) QLORA_CASE(3) QLORA_CASE(4)
     QLORA_CASE(5) QLORA_CASE(6) QLORA_CASE(7) QLORA_CASE(8)
@@ -888,11 +947,12 @@ hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const FinalizeJob j{partials, sp.splits, Kc * r, Kc * r, Kc * r, 1.0f, OUT};
   if (defer) {
-    *defer = FinalizeJob{partials, sp.splits, Kc * r, Kc * r, Kc * r, 1.0f, OUT};
+    *defer = j;
     return hipSuccess;
   }
-  return launch_finalize(partials, sp.splits, Kc * r, Kc * r, Kc * r, 1.0f, OUT, stream);
+  return launch_finalize(j.P, j.splits, j.count, j.cols, j.ldout, j.scale, j.OUT, stream);
 }
 
 hipError_t launch_transpose2_bf16(const uint16_t *IN0, int64_t R0, int64_t C0, uint16_t *OUT0, const uint16_t *IN1,
@@ -1020,8 +1080,8 @@ hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, co
 }
 
 hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
-                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, uint16_t *dB,
-                            float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
+                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, int64_t lo,
+                            uint16_t *dB, float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
                             hipStream_t stream) {
   const int rt = (r + 31) / 32, R = parts * r;
   if (rt < 1 || rt > 8 || parts < 1 || parts > kMaxVdbParts || !vdb_fast(M, Np, ldy, R, r, true))
@@ -1052,6 +1112,7 @@ hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np
   if (e != hipSuccess) return e;
   FinalizeJobs jobs;
   jobs.n = 2 * parts;
+  jobs.lo = lo;
   int64_t total = 0;
   for (int p = 0; p < parts; ++p) {
     jobs.j[2 * p] = FinalizeJob{ws_v + p * ps.pv, sd.ksplit, M * r, r, R, scale, V + p * r};

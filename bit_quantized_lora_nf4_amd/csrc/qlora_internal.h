@@ -131,10 +131,16 @@ size_t reduce_m_workspace(int64_t M, int64_t No, int r);
 hipError_t launch_reduce_m(const uint16_t *IN, int64_t M, int64_t No, int64_t ldin, const uint16_t *S,
                            int64_t lds, int r, float *partials, uint16_t *OUT, bool trans_out,
                            hipStream_t stream, FinalizeJob *defer = nullptr);
-// dA [r, Kc] = bf16(S^T (m IN)) with the dropout mask on IN, a dense [M, Kc] tensor (S
-// dense [M, r]); needs drop_shape_ok(M, Kc, r).
-hipError_t launch_reduce_m_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *S, int r, float *partials,
-                                uint16_t *OUT, const Dropout &d, hipStream_t stream, FinalizeJob *defer);
+// dA [r, Kc] = bf16((V + V_lo)^T (m IN)) with the dropout mask on IN, a dense [M, Kc] tensor
+// (drop.thr = 0: none); V dense [M, r], V_lo `lo` elements (a multiple of 8) behind it.
+// V's rounding to bf16 would be as large an error of dA as its own last one, so what it
+// takes off is multiplied too: X is read once for both, and the second product costs 3 us
+// (4096 x 4096, rank 64: 18.8 us, 16.0 with V alone; rank 128: 27.2, 24.4).  Partial sums
+// as reduce_m's.  pair_shape_ok: the shapes it takes.
+bool pair_shape_ok(int64_t M, int64_t Kc, int r, int64_t lo);
+hipError_t launch_reduce_pair(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *V, int64_t lo, int r,
+                              float *partials, uint16_t *OUT, const Dropout &d, hipStream_t stream,
+                              FinalizeJob *defer);
 
 // The backward's two products over dY in one launch plus one finalize launch:
 // V[M, r] (row pitch ldu) = bf16(scale dY B) and dB[Np, r] = bf16(dY^T U), where dY has
@@ -154,10 +160,11 @@ hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, co
 // launch_vdb for `parts` stacked parts at once (one launch and one finalize): part q's dY
 // columns are [q ldp, q ldp + Np) of rows of pitch ldy (zeros up to the next multiple of 8),
 // B [parts Np, r], U and V [M, parts r], dB [parts Np, r]; the partial regions are `parts`
-// times vdb_workspace_v / vdb_workspace_db; At[KA, parts r] = A^T if both are given.
+// times vdb_workspace_v / vdb_workspace_db; At[KA, parts r] = A^T if both are given.  What
+// V's rounding took off goes, rounded in its turn, to the matrix `lo` elements behind V.
 hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
-                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, uint16_t *dB,
-                            float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
+                            const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, int64_t lo,
+                            uint16_t *dB, float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
                             hipStream_t stream);
 
 // AdamW step (fp32 parameter and moments, bf16 gradient, optional bf16 parameter copy).

@@ -294,9 +294,11 @@ int qlora_linear_fwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint1
 
 /* Backward of qlora_linear_fwd_dropout with the same drop:
  *   V_q = bf16((alpha / r) c . dY_q . B_q)       dB_q = bf16(dY_q^T . U_q)
- *   dX = bf16(dY . W' + m (V . A))               dA   = bf16(V^T . (m X))
+ *   dX = bf16(dY . W' + m (V . A))               dA   = bf16((V + V')^T . (m X))
+ * where V' = bf16 of what V's rounding took off: dA sees V to 16 significant bits.
  * U_saved is the forward's U (NULL: recomputed with the mask).  QLORA_ERR_SHAPE, before
- * anything is launched, when a tensor exceeds 0xFFFFFFF0 bytes. */
+ * anything is launched, when a tensor, or [V | V'] of rank round_up(r, 8), exceeds
+ * 0xFFFFFFF0 bytes. */
 int qlora_linear_bwd_dropout(const qlora_nf4_weight *w, int n_parts, const uint16_t *dY, const uint16_t *X,
                              int64_t M, const uint16_t *A, const uint16_t *B, int r, float alpha,
                              const qlora_drop *drop, const uint16_t *U_saved, uint16_t *dX, uint16_t *dA,

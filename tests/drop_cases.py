@@ -98,13 +98,15 @@ def backward(dY, edY, X, Wd, A, B, alpha, r, parts, m, c, U):
         eV[:, j] = abs(k) * (edY[:, o] @ np.abs(B[o]) + (n + 8) * S * (np.abs(dY[:, o]) @ np.abs(B[o])))
         dB[o] = dY[:, o].T @ U[:, j]
         eB[o] = edY[:, o].T @ np.abs(U[:, j]) + (M + 8) * S * (np.abs(dY[:, o]).T @ np.abs(U[:, j]))
+    # dA multiplies V and what its rounding took off, itself rounded: 2^-8 of 2^-8
+    eV2 = eV + H * H * (np.abs(V) + eV)
     eV = eV + H * (np.abs(V) + eV)
     low = m * (V @ A)
     dX = dX + low
     eX = eX + m * (eV @ np.abs(A) + (N + r + 8) * S * (np.abs(V) @ np.abs(A)))
     mX = m * X
     dA = V.T @ mX
-    eA = eV.T @ np.abs(mX) + (M + 8) * S * (np.abs(V).T @ np.abs(mX))
+    eA = eV2.T @ np.abs(mX) + 2 * (M + 8) * S * (np.abs(V).T @ np.abs(mX))
     fin = lambda v, e: (v, e + H * (np.abs(v) + e))  # noqa: E731
     return {"dX": fin(dX, eX), "dA": fin(dA, eA), "dB": fin(dB, eB)}
 
