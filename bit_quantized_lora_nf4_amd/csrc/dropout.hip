@@ -62,25 +62,44 @@ __global__ __launch_bounds__(NT) void dropout_kernel(const void *X, int64_t n, D
   }
 }
 
-// Row copies with zero padding (CopyJob): a workgroup row of the grid per job, a wave per
-// row of the job, lanes along the row.  The jobs are adapter operands of unaligned rank
-// (a few MB) or a gradient of odd width; both sides may be unaligned, so the accesses are
-// two bytes a lane, 128 contiguous bytes a wave.
+// Row copies with zero padding (CopyJob): a row of the grid per job, a thread per 8 columns
+// (16 bytes) of the destination.  A side whose rows are 16-byte aligned is accessed whole,
+// the other one element by element, all in flight together.  The jobs are adapter operands
+// of unaligned rank (a few MB: the launch is what they take, COPYUS us for A [24, 1280] and B
+// [2002, 12]) or a gradient of odd width.
 struct CopyJobs {
   CopyJob j[kMaxCopyJobs];
 };
 __global__ __launch_bounds__(NT) void copy_rows_kernel(CopyJobs jobs) {
   const CopyJob jb = jobs.j[blockIdx.y];
-  const int lane = threadIdx.x & 63;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * (NT / 64) + (threadIdx.x >> 6);
-  const int64_t waves = static_cast<int64_t>(gridDim.x) * (NT / 64);
-  // rows longer than 2048 columns are split, so that few long rows spread too
-  const int64_t seg = 2048, segs = (jb.dcols + seg - 1) / seg;
-  for (int64_t i = wave; i < jb.rows * segs; i += waves) {
-    const int64_t row = i / segs, c0 = (i % segs) * seg;
-    const int64_t c1 = c0 + seg < jb.dcols ? c0 + seg : jb.dcols;
-    for (int64_t c = c0 + lane; c < c1; c += 64)
-      jb.dst[row * jb.ldd + c] = c < jb.cols ? jb.src[row * jb.lds + c] : static_cast<uint16_t>(0);
+  const uint32_t chunks = static_cast<uint32_t>((jb.dcols + 7) / 8);
+  const uint32_t n = static_cast<uint32_t>(jb.rows) * chunks;  // of 16 bytes of a tensor below 4 GiB
+  const bool vs = jb.lds % 8 == 0, vd = jb.ldd % 8 == 0;
+  for (uint32_t i = blockIdx.x * NT + threadIdx.x; i < n; i += gridDim.x * NT) {
+    const uint32_t row = i / chunks, c = (i - row * chunks) * 8;
+    const uint16_t *src = jb.src + row * jb.lds + c;
+    uint16_t *dst = jb.dst + row * jb.ldd + c;
+    const int64_t have = jb.cols - c, want = jb.dcols - c;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (vs && have >= 8) {
+      v = *reinterpret_cast<const u32x4_t *>(src);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = 2 * e < have ? src[2 * e] : 0u, hi = 2 * e + 1 < have ? src[2 * e + 1] : 0u;
+        v[e] = lo | (hi << 16);
+      }
+    }
+    if (vd && want >= 8) {
+      *reinterpret_cast<u32x4_t *>(dst) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = v[e];
+        if (2 * e < want) dst[2 * e] = static_cast<uint16_t>(w);
+        if (2 * e + 1 < want) dst[2 * e + 1] = static_cast<uint16_t>(w >> 16);
+      }
+    }
   }
 }
 
@@ -109,14 +128,14 @@ hipError_t launch_copy_rows(const CopyJob *jobs, int n, hipStream_t stream) {
   int64_t most = 0;
   for (int i = 0; i < n; ++i) {
     if (jobs[i].rows <= 0) continue;
-    if (used == kMaxCopyJobs) return hipErrorInvalidValue;
+    const int64_t units = jobs[i].rows * ((jobs[i].dcols + 7) / 8);
+    if (used == kMaxCopyJobs || units > 0x7fffffff) return hipErrorInvalidValue;
     a.j[used++] = jobs[i];
-    const int64_t units = jobs[i].rows * ((jobs[i].dcols + 2047) / 2048);
     most = units > most ? units : most;
   }
   if (used == 0) return hipSuccess;
   for (int i = used; i < kMaxCopyJobs; ++i) a.j[i] = CopyJob{nullptr, nullptr, 0, 0, 0, 0, 0};
-  int64_t blocks = (most + 3) / 4;
+  int64_t blocks = (most + NT - 1) / NT;
   if (blocks > 2048) blocks = 2048;
   hipLaunchKernelGGL(copy_rows_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(used)), dim3(NT), 0,
                      stream, a);

@@ -69,9 +69,10 @@ struct GemmParams {
 };
 
 // The dX GEMM's extension (launch_gemm_dx_ext): the dropout mask of the LoRA term, and dY
-// in column blocks of `half` columns of which the last `skip` are padding: contraction
-// position k stands for weight row k - skip floor(k / half) where k % half < half - skip.
-// Only two blocks or none (half = the whole contraction) are needed.
+// in column blocks of `half` columns of which the last `skip` are padding (zeros in dY):
+// contraction position k stands for weight row k, or k - skip from `half` on.  The padding
+// positions thus read rows of the next block (past the last one: zeros) times zero.  Only
+// two blocks or none (half = the whole contraction) are needed.
 // With splits > 1 workgroup s tiles + t computes the contraction steps [s ksteps, (s + 1)
 // ksteps) of tile t and writes its fp32 accumulators to `part` (dx_join_kernel adds them);
 // the LoRA term belongs to split 0.
@@ -422,7 +423,12 @@ constexpr int NBUF = 3;
 
 // GATED: a tile is 256 tokens x 128 gate columns and the same 128 up columns; wave w owns
 // 32 of each (its two 32-column blocks j = 0, 1 are weight rows of the two projections at
-// the same column), so that act(G) L of an element is formed in one lane's registers.
+// the same column), so that act(G) L of an element is formed in one lane's registers and
+// neither projection is read back; H, and G and L where they are kept, leave through LDS in
+// whole rows.  Bound like the plain forward by the matrix units at the clock that the card's
+// power leaves them: 4096 x 4096 -> 2 x 11008 with rank 64, dropout and [G | L] kept, whole
+// call: 704 us, 1073 TFLOP/s (a bf16 library product of that size: 1239); 2048 x 8192 -> 2 x
+// 22016: 1330 us, 1121.
 template <int CT, bool GATED>
 __device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o, char *sX) {
   const int lane = threadIdx.x & 63;
@@ -1049,6 +1055,13 @@ __device__ __forceinline__ void store_dx_part(const GemmParams &p, float *part, 
     }
 }
 
+// EXT: dX = dY W' + m (V A) with dY in padded column blocks (DxExt).  The LoRA term comes
+// first, so the mask is applied to the accumulators once, before the base product is added
+// to them; the kept elements, one bit each in the accumulators' layout, are generated while
+// the first tiles' loads are in flight.  4096 x 4096 -> 4096, rank 64: 7 us over the same
+// product without a mask (144.5, 137.1; 1083 TFLOP/s on 4096 x 22016 -> 4096), bound by the
+// matrix units as the kernel without EXT is.
+// SPLIT: one part of the contraction, see dx_split.
 template <int CT, bool EXT, bool SPLIT = false>
 __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, char *sW1, char *sY0,
                                              char *sY1) {
@@ -1309,7 +1322,8 @@ __device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, c
   }
 }
 
-// The join of a split dX: a wave adds one 32 x 32 block's partial sums in split order (the
+// The join of a split dX (bound by memory: 4 bytes read an element and split, 2 written; 1000
+// x 8192 in two splits 15 us, 5.5 TB/s): a wave adds one 32 x 32 block's partial sums in split order (the
 // loads of four splits in flight at a time: with few tiles and many splits the chain of
 // loads is what the join waits for), rounds once and writes four columns a lane.
 __global__ __launch_bounds__(NT) void dx_join_kernel(const float *__restrict__ part, int splits, int tiles, int M,

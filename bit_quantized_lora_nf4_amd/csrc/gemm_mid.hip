@@ -20,6 +20,10 @@
 //     row's operand is zero in the other projection's ranks;
 //   - SPLIT: the contraction is divided over several workgroups that write their fp32
 //     accumulators, and gemm_mid_join adds them in a fixed order and does the epilogue.
+// Bound by the decode's vector instructions (busy 81 % of the kernel's cycles at 16 tokens).
+// Measured, whole calls: 16 x 8192 -> 2 x 22016 of rank 64 82 us (2.38 TB/s; the 256 x 256
+// tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 188 us (201), 333 x 1280 ->
+// 2 x 1001 43 us (82).
 
 #include <type_traits>
 
@@ -382,33 +386,33 @@ __global__ __launch_bounds__(NT) void gemm_mid_join_kernel(MidParams p) {
 }  // namespace
 
 namespace {
-// The tile height (the fewest tokens' blocks that hold M, at most four) and the number of
-// splits, by the time they take: a step of a workgroup costs its CU about 0.32 / 0.44 / 0.58
-// us (NI = 1 / 2 / 4; measured on 4096 -> 2 x 11008 and 8192 -> 2 x 22016), 15% more when it
-// is alone there; splits add the join's launch and the partial sums, written and read once.
+// The tile height (NI blocks of 32 tokens, no more than hold M) and the number of splits, by
+// the time they take: a step of a workgroup costs its CU about 0.32 / 0.44 / 0.58 us (NI = 1 /
+// 2 / 4; measured on 4096 -> 2 x 11008 and 8192 -> 2 x 22016), 15% more when it is alone
+// there; splits add the join's launch and the partial sums, written and read once.  Lower
+// tiles decode the weight more often but spread few tokens over more CUs without a join
+// (whole calls, us, the best with NI = 1, 2, 4: 128 x 4096 -> 2 x 2000: 25.9, 26.9, 28.9; 500
+// x 1536 -> 2 x 1200: 26.9, 21.4, 25.5; 160 x 8192 -> 2 x 4000: 70.6, 58.3, 57.1).
 struct MidPlan {
   int ni, tiles_m, tiles_n, splits, ksteps;
   double cost;
 };
 MidPlan mid_plan(int64_t M, int64_t K, int64_t cols) {
   MidPlan b;
-  b.ni = M <= 32 ? 1 : M <= 64 ? 2 : 4;
-  b.tiles_m = static_cast<int>((M + 32 * b.ni - 1) / (32 * b.ni));
-  b.tiles_n = static_cast<int>((cols + TN - 1) / TN);
-  const int64_t tiles = int64_t(b.tiles_m) * b.tiles_n, nk = K / TK;
-  const double step = b.ni == 4 ? 0.58 : b.ni == 2 ? 0.44 : 0.32;
   b.cost = 1e30;
-  const int64_t s_min = (nk + kMaxSteps - 1) / kMaxSteps;
-  for (int64_t s = s_min; s == s_min || (s * tiles <= 1024 && 2 * s <= nk); ++s) {
-    // whole code groups, which are whole lines when the rows are
-    const int64_t steps = s == 1 ? nk : (nk + s * RING - 1) / (s * RING) * RING, used = (nk + steps - 1) / steps;
-    const int64_t per_cu = (tiles * used + 255) / 256;
-    const double cost = (per_cu == 1 ? 1.15 : double(per_cu)) * step * steps + 5.0 +
-                        (used > 1 ? 5.0 + double(M) * cols * 8.0 * used / 4.5e6 : 0.0);
-    if (cost < b.cost - 1e-9) {
-      b.cost = cost;
-      b.splits = static_cast<int>(used);
-      b.ksteps = static_cast<int>(steps);
+  const int64_t nk = K / TK, tiles_n = (cols + TN - 1) / TN, s_min = (nk + kMaxSteps - 1) / kMaxSteps;
+  for (int ni = M <= 32 ? 1 : M <= 64 ? 2 : 4; ni >= 1; ni /= 2) {
+    const int64_t tiles_m = (M + 32 * ni - 1) / (32 * ni), tiles = tiles_m * tiles_n;
+    const double step = ni == 4 ? 0.58 : ni == 2 ? 0.44 : 0.32;
+    for (int64_t s = s_min; s == s_min || (s * tiles <= 1024 && 2 * s <= nk); ++s) {
+      // whole code groups, which are whole lines when the rows are
+      const int64_t steps = s == 1 ? nk : (nk + s * RING - 1) / (s * RING) * RING, used = (nk + steps - 1) / steps;
+      const int64_t per_cu = (tiles * used + 255) / 256;
+      const double cost = (per_cu == 1 ? 1.15 : double(per_cu)) * step * steps + 5.0 +
+                          (used > 1 ? 5.0 + double(M) * cols * 8.0 * used / 4.5e6 : 0.0);
+      if (cost < b.cost - 1e-9)
+        b = {ni, static_cast<int>(tiles_m), static_cast<int>(tiles_n), static_cast<int>(used),
+             static_cast<int>(steps), cost};
     }
   }
   return b;

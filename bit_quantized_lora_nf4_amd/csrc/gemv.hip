@@ -463,7 +463,9 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char *dst, uint3
 
 // EXT: dropout of X ahead of the adapter (x.drop), and the gated projections (x.H): a tile
 // of 16 weight rows is then 8 gate rows and the same 8 up rows, so that a reduction's lanes
-// l and l + 32 hold G and L of the same four columns of a token.
+// l and l + 32 hold G and L of the same four columns of a token.  Decode-bound like the plain
+// kernel: one token, 4096 -> 2 x 11008 of rank 16, 22.9 us a call, 2.08 TB/s of stored
+// weights (the plain kernel on 4096 -> 11008: 2.07).
 template <int CT, bool XLDS, bool MULTI, bool DIRECT, bool XDMA, bool EXT>
 __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char *xst0, char *xst1) {
   static_assert(!(XLDS && XDMA), "X is staged for the workgroup or per wave, not both");
