@@ -473,7 +473,7 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t K, int64_t N, int r, int parts,
     L.at = off;
     off += align_up(size_t(K) * R8 * 2);
     L.part = off;
-    size_t p = qlora::reduce_m_workspace(M, K, R8);
+    size_t p = qlora::reduce_pair_workspace(M, K, R8);
     const size_t others[] = {qlora::lora_down_workspace(M, K, R8), parts * qlora::vdb_workspace_v(M, Np, r8)};
     for (size_t o : others) p = o > p ? o : p;
     off += align_up(p);

@@ -919,6 +919,23 @@ hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, cons
   return launch_finalize(ws, sp.ksplit, M * r, r, r, scale, OUT, stream);
 }
 
+// Row splits of the paired reduction: as many workgroups as are on the card at once (two a
+// CU while pair_nb's buffers leave room for two), each with a step or more (rank 192, 1000 x
+// 8192: 27.8 us with 4 splits, which take two rounds, 23.8 with 2; 1254 x 4352: 26.8 with 8,
+// 17.3 with 3).
+MSplit pair_split(int64_t M, int64_t Kc, int r) {
+  const int64_t tiles = (Kc + 63) / 64, smax = (M + 63) / 64;
+  int64_t sp = (r <= 128 ? 512 : 256) / tiles;
+  if (sp > smax) sp = smax;
+  if (sp < 1) sp = 1;
+  const int64_t MR = ((M + sp - 1) / sp + 31) / 32 * 32;
+  sp = (M + MR - 1) / MR;
+  return {static_cast<int>(sp), static_cast<int>(MR)};
+}
+size_t reduce_pair_workspace(int64_t M, int64_t Kc, int r) {
+  return static_cast<size_t>(pair_split(M, Kc, r).splits) * Kc * r * sizeof(float);
+}
+
 bool pair_shape_ok(int64_t M, int64_t Kc, int r, int64_t lo) {
   return drop_shape_ok(M, Kc, r) && uint64_t(lo) * 2 + uint64_t(M) * r * 2 <= k4G;
 }
@@ -928,7 +945,7 @@ hipError_t launch_reduce_pair(const uint16_t *IN, int64_t M, int64_t Kc, const u
                               FinalizeJob *defer) {
   if (defer) defer->splits = 0;
   if (!pair_shape_ok(M, Kc, r, lo)) return hipErrorInvalidValue;
-  const MSplit sp = m_split(M, Kc);
+  const MSplit sp = pair_split(M, Kc, r);
   dim3 grid(static_cast<unsigned>((Kc + 63) / 64), static_cast<unsigned>(sp.splits)), block(NT);
   const uint32_t lo_off = static_cast<uint32_t>(lo * 2);
   switch ((r + 31) / 32) {

@@ -135,8 +135,9 @@ hipError_t launch_reduce_m(const uint16_t *IN, int64_t M, int64_t No, int64_t ld
 // (drop.thr = 0: none); V dense [M, r], V_lo `lo` elements (a multiple of 8) behind it.
 // V's rounding to bf16 would be as large an error of dA as its own last one, so what it
 // takes off is multiplied too: X is read once for both, and the second product costs 3 us
-// (4096 x 4096, rank 64: 18.8 us, 16.0 with V alone; rank 128: 27.2, 24.4).  Partial sums
-// as reduce_m's.  pair_shape_ok: the shapes it takes.
+// (4096 x 4096, rank 64: 18.8 us, 16.0 with V alone; rank 128: 27.2, 24.4).  pair_shape_ok:
+// the shapes it takes.
+size_t reduce_pair_workspace(int64_t M, int64_t Kc, int r);
 bool pair_shape_ok(int64_t M, int64_t Kc, int r, int64_t lo);
 hipError_t launch_reduce_pair(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *V, int64_t lo, int r,
                               float *partials, uint16_t *OUT, const Dropout &d, hipStream_t stream,
