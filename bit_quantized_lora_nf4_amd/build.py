@@ -30,9 +30,8 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 
-SOURCES = ["codebook.cpp", "api.cpp", "quantize.hip", "dequant.hip", "lora.hip", "gemm.hip", "gemm_mid.hip", "adamw.hip", "merge.hip", "dropout.hip",
-           "gated.hip",
-           "gemv.hip"]
+SOURCES = ["codebook.cpp", "api.cpp", "quantize.hip", "dequant.hip", "lora.hip", "gemm.hip", "gemm_mid.hip", "dx_mid.hip",
+           "adamw.hip", "merge.hip", "dropout.hip", "gated.hip", "gemv.hip"]
 
 
 def _compile(src, obj_dir, verbose):

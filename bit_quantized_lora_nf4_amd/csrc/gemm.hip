@@ -974,40 +974,17 @@ __device__ __forceinline__ void dx_schedule() {
 constexpr int YWAVE_BYTES = 64 * TK * 2;
 
 // The dropout mask of X on the LoRA term of dX (acc[i][j]: tokens tb + 32 i + l % 32,
-// output columns cb + 32 j + 8 g + 4 (l / 32) + 0..3): the eight columns of a generator
-// group are held by lanes l and l + 32, four each.  Of each pair of groups the lower half
-// makes the first one's block and the upper half the second one's; a half-wave swap of two
-// word pairs then gives every lane the two words of its own elements of both groups.
-// keep_bits packs a lane's keep decisions, element e of acc[i][j] in bit 16 (j % 2) + e of
-// word [i][j / 2], so that the generator runs while the first tiles' loads are in flight;
+// output columns cb + 32 j + 8 g + 4 (l / 32) + 0..3).  keep_bits packs a lane's keep
+// decisions, element e of acc[i][j] in bit 16 (j % 2) + e of word [i][j / 2] (keep_word in
+// gemm_tile.h), so that the generator runs while the first tiles' loads are in flight;
 // mask_lora applies them.
 __device__ __forceinline__ void keep_bits(const DropKey &dk, int tb, int cb, int K, uint32_t (&keep)[4][2]) {
   const int lane = threadIdx.x & 63;
-  const uint32_t top = dk.thr << 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t row = static_cast<uint32_t>(tb + 32 * i + (lane & 31)) * static_cast<uint32_t>(K / 8);
 #pragma unroll
-    for (int jp = 0; jp < 2; ++jp) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {  // groups 2 q and 2 q + 1 of the eight of two column tiles
-        const u32x4_t w = drop_words(row + (cb + 64 * jp + 16 * q) / 8 + (lane >> 5), 0u, dk);
-        const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-        const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t v[2] = {g ? lo[1] : lo[0], g ? hi[1] : hi[0]};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t h = (e & 1) ? v[e / 2] : v[e / 2] << 16;  // the element's bits on top
-            bits |= h >= top ? 1u << (8 * q + 4 * g + e) : 0u;
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
-      }
-      keep[i][jp] = bits;
-    }
+    for (int jp = 0; jp < 2; ++jp) keep[i][jp] = keep_word(dk, row + (cb + 64 * jp) / 8);
   }
 }
 __device__ __forceinline__ void mask_lora(const uint32_t (&keep)[4][2], f32x16_t (&acc)[4][4]) {
@@ -1488,27 +1465,30 @@ namespace {
 // splits minimises that sum (1000 x 24576 -> 8192: 128 tiles, 2 splits, 642 -> 374 us).
 struct DxSplit {
   int splits, ksteps;
+  double cost;
 };
 DxSplit dx_split(int64_t M, int64_t K, int64_t Kc) {
   const int64_t tiles = ((M + TM - 1) / TM) * ((K + TN - 1) / TN), nk = (Kc + TK - 1) / TK;
-  DxSplit best{1, static_cast<int>(nk)};
+  DxSplit best{1, static_cast<int>(nk), double((tiles + 255) / 256) * (1.6 * nk + 8.0)};
   if (tiles >= 256) return best;
-  double best_cost = 1.6 * nk + 8.0;
   const double kb = double(M) * K * 8.0 / 4.5e6;  // us per split of partial sums, written and read
   for (int64_t s = 2; s * tiles <= 512 && s * 2 <= nk; ++s) {
     const int64_t steps = (nk + s - 1) / s, used = (nk + steps - 1) / steps;
     const double rounds = double((tiles * used + 255) / 256);
     const double cost = rounds * (1.6 * steps + 8.0) + 5.0 + kb * used;
-    if (cost < best_cost - 1e-9) {
-      best_cost = cost;
-      best = {static_cast<int>(used), static_cast<int>(steps)};
-    }
+    if (cost < best.cost - 1e-9) best = {static_cast<int>(used), static_cast<int>(steps), cost};
   }
   return best;
 }
+// The smaller tiles of dx_mid.hip (whole backward calls, us, these tiles against those: 64 x
+// 4096 -> 4096 44, 36; 512 x 2048 -> 2048 47, 38; 270 x 4416 -> 9730 89, 81; 1319 x 3392 ->
+// 1608 82, 72; 400 x 4096 -> 1000 47, 35; 512 x 4096 -> 22016 140, 146; 1000 x 8192 -> 24576
+// 429, 489; the sums above leave out about 6 us that these tiles take longer to start and end).
+bool dx_mid_takes(int64_t M, int64_t K, int64_t Kc) { return dx_mid_cost(M, K, Kc) < dx_split(M, K, Kc).cost + 6.0; }
 }  // namespace
 
 size_t gemm_dx_ext_workspace(int64_t M, int64_t K, int64_t Kc) {
+  if (dx_mid_takes(M, K, Kc)) return dx_mid_workspace(M, K, Kc);
   const DxSplit sp = dx_split(M, K, Kc);
   const int64_t tiles = ((M + TM - 1) / TM) * ((K + TN - 1) / TN);
   return sp.splits > 1 ? static_cast<size_t>(sp.splits) * tiles * TM * TN * sizeof(float) : 0;
@@ -1520,6 +1500,8 @@ hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M
   const int64_t Np = w.n_rows / parts, half = (Np + 7) / 8 * 8, Kc = parts > 1 ? parts * half : half;
   if (w.n_rows % parts != 0 || (parts > 2 && half != Np)) return hipErrorInvalidValue;
   if (!fits_32bit(M, Kc, w.n_cols, r) || M > 0x7fffffff) return hipErrorInvalidValue;
+  if (dx_mid_takes(M, w.n_cols, Kc))
+    return launch_dx_mid(w, dY, M, Kc, half == Np ? Kc : half, half - Np, V, At, r, dX, d, part, stream, fin);
   GemmParams p = make_params(dY, w, V, At, dX, M, w.n_cols, Kc, r);
   if (fin && fin->splits > 0) {
     p.fin = *fin;

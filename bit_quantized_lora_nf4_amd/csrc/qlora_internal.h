@@ -255,4 +255,13 @@ hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M
                               const uint16_t *At, int r, uint16_t *dX, const Dropout &d, float *part,
                               hipStream_t stream, const FinalizeJob *fin);
 
+// The same product on smaller tiles (dx_mid.hip), which launch_gemm_dx_ext takes where its own
+// are estimated to take longer: dY [M, Kc] with the padding described by half and skip (DxExt
+// in gemm.hip); estimated time in us; bytes of partial sums.
+double dx_mid_cost(int64_t M, int64_t K, int64_t Kc);
+size_t dx_mid_workspace(int64_t M, int64_t K, int64_t Kc);
+hipError_t launch_dx_mid(const WeightView &w, const uint16_t *dY, int64_t M, int64_t Kc, int64_t half, int64_t skip,
+                         const uint16_t *V, const uint16_t *At, int r, uint16_t *dX, const Dropout &d, float *part,
+                         hipStream_t stream, const FinalizeJob *fin);
+
 }  // namespace qlora

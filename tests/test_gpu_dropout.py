@@ -106,6 +106,8 @@ CASES = [
     (530, 2048, 776, 64, 1, 0.1),     # several workgroups of every kind
     (20, 64, 1000, 8, 1, 0.1), (40, 704, 130, 40, 1, 0.1), (100, 320, 513, 72, 1, 0.1),
     (50, 448, 512, 72, 3, 0.1),       # parts of stacked ranks that straddle 64-rank tiles
+    # dX on tiles of 128 tokens, whole and split; on the large tiles, split
+    (8200, 512, 520, 16, 1, 0.1), (4000, 320, 2000, 72, 1, 0.2), (520, 64, 8195, 20, 1, 0.1), (300, 64, 2048, 72, 2, 0.1),
 ]
 
 

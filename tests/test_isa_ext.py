@@ -143,6 +143,40 @@ def test_mid_barrier_waits(tmp_path_factory):
     assert len(sizes) == 42 and all(int(n) <= 16 for _, n in sizes), sizes
 
 
+def test_dx_mid_barrier_waits(tmp_path_factory):
+    """dX on smaller tiles: in the main loop of three steps, a step's wait may leave in flight
+    only what was loaded behind its dY tile, one later step's tile and codes; no other wait
+    makes it wait for its own step's loads; no kernel spills."""
+    asm = _asm(tmp_path_factory, "dx_mid")
+    kernels = re.findall(r"^(_Z\S*dx_mid_kernelILi(\d)ELi(\d)ELb\d\S*):", asm, re.M)
+    assert len(kernels) == 18, len(kernels)
+    for name, ct, ni in kernels:
+        per_step = int(ni) + (3 if ct == "2" else 5)
+        body = re.search(r"^" + re.escape(name) + r":.*?^\.Lfunc_end", asm, re.S | re.M).group(0)
+        lines = [ln.strip() for ln in body.splitlines()]
+        labels = {m.group(1): i for i, ln in enumerate(lines) if (m := re.match(r"^(\.LBB\S+):", ln))}
+        loops = [lines[labels[m.group(2)]:i + 1] for i, ln in enumerate(lines)
+                 if (m := _BR.search(ln)) and m.group(2) in labels and labels[m.group(2)] < i]
+        loop = max((x for x in loops if _dma(x) == 3 * int(ni)), key=len)
+        # twice around, counting the loads issued since the last barrier
+        seen, since = 0, 0
+        for i, ln in enumerate(loop + loop):
+            if _VMEM.match(ln):
+                since += 1
+            elif m := re.match(r"s_waitcnt (?:.*\s)?vmcnt\((\d+)\)", ln):
+                n = int(m.group(1))
+                nxt = (loop + loop)[i + 1] if i + 1 < 2 * len(loop) else ""
+                if nxt.startswith("s_barrier"):
+                    # one whole later step in flight: its tile, then its codes
+                    assert n == per_step, (name, n)
+                    seen, since = seen + 1, 0
+                else:
+                    assert n >= since, (name, n, since)
+        assert seen == 6, (name, seen)
+    sizes = re.findall(r"\.name:\s+(\S*dx_mid_\S*kernel\S*)\s.*?\.private_segment_fixed_size:\s+(\d+)", asm, re.S)
+    assert len(sizes) == 21 and all(int(n) == 0 for _, n in sizes), sizes
+
+
 def test_gemv_ext_x_stage_waits(tmp_path_factory):
     asm = _asm(tmp_path_factory, "gemv")
     # gemv_ext_kernel<CT, XLDS = false, MULTI, DIRECT, XDMA = true>
