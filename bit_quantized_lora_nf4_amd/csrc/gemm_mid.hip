@@ -20,7 +20,8 @@
 //     row's operand is zero in the other projection's ranks;
 //   - SPLIT: the contraction is divided over several workgroups that write their fp32
 //     accumulators, and gemm_mid_join adds them in a fixed order and does the epilogue.
-// Bound by the decode's vector instructions (busy 81 % of the kernel's cycles at 16 tokens).
+// Bound by the decode's vector instructions (at 16 tokens they issue in 65 % of the cycles, and
+// two fifths of them are permutes, which take two slots).
 // Measured, whole calls: 16 x 8192 -> 2 x 22016 of rank 64 82 us (2.38 TB/s; the 256 x 256
 // tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 188 us (201), 333 x 1280 ->
 // 2 x 1001 43 us (82).
