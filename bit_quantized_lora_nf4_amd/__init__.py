@@ -541,7 +541,7 @@ _ACTS = {"silu": QLORA_ACT_SILU, "gelu_tanh": QLORA_ACT_GELU_TANH}
 
 
 def _gated_checks(qw, X, A, B, act):
-    """(checker, M, K, P, r, activation value) of a gated call."""
+    """(argument checks, M, K, P, r, activation value) of a gated call."""
     if act not in _ACTS:
         raise ValueError(f"act {act!r}: expected one of {sorted(_ACTS)}")
     K, N = qw.n_cols, qw.n_rows

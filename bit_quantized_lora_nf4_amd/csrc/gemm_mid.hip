@@ -23,7 +23,7 @@
 // Bound by the decode's vector instructions (at 16 tokens they issue in 65 % of the cycles, and
 // two fifths of them are permutes, which take two slots).
 // Measured, whole calls: 16 x 8192 -> 2 x 22016 of rank 64 82 us (2.38 TB/s; the 256 x 256
-// tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 188 us (201), 333 x 1280 ->
+// tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 183 us (201), 333 x 1280 ->
 // 2 x 1001 43 us (82).
 
 #include <type_traits>
@@ -132,18 +132,12 @@ struct Codes {
 constexpr int kCodeLoads = RING + 1;  // vector loads of one Codes
 constexpr int kMaxSteps = 256;
 
-template <int CT, bool GATED, int NI, bool SPLIT>
-__global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
+// One tile of 32 NI tokens from m0 on; SLOT: 32-token blocks of a tile in the partial sums.
+template <int CT, bool GATED, int NI, bool SPLIT, int SLOT>
+__device__ __forceinline__ void mid_body(const MidParams &p, char *sX, int m0, int tni, int split) {
   constexpr int TILE = NI * 32 * 128;  // bytes of an X tile
-  __shared__ __attribute__((aligned(16))) char sX[RING * TILE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = p.tiles_m * p.tiles_n;
-  const int split = SPLIT ? static_cast<int>(blockIdx.x) / tiles : 0;
-  const int tile = static_cast<int>(blockIdx.x) - split * tiles;
-  int tmi, tni;
-  tile_coords(tile, p.tiles_m, p.tiles_n, tmi, tni);
-  const int m0 = tmi * 32 * NI;
   const int c0 = tni * (GATED ? TN / 2 : TN) + wave * (GATED ? 16 : 32);  // this wave's first column
 
   const int K = p.K;
@@ -333,7 +327,7 @@ __global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the kernel ends
 
   if constexpr (SPLIT) {
-    float *const base = p.part + (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (NI * kBlockFloats);
+    float *const base = p.part + (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (SLOT * kBlockFloats);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if (m0 + 32 * i >= p.M) break;
@@ -346,6 +340,26 @@ __global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) store_block<GATED>(p, m0 + 32 * i + (lane & 31), c0, acc[i]);
   }
+}
+
+// TAIL: the 32-token blocks of the last tile, when that many hold its tokens (0: as many as the
+// others'): a step for 32 tokens takes 0.55 of the time of one for 128 (777 x 4096 -> 2 x 11008:
+// 189.6 us with 128 for the last 9 tokens, 183.0 with 32).
+template <int CT, bool GATED, int NI, bool SPLIT, int TAIL>
+__global__ __launch_bounds__(NT, 2) void gemm_mid_kernel(MidParams p) {
+  __shared__ __attribute__((aligned(16))) char sX[RING * NI * 32 * 128];
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int split = SPLIT ? static_cast<int>(blockIdx.x) / tiles : 0;
+  const int tile = static_cast<int>(blockIdx.x) - split * tiles;
+  int tmi, tni;
+  tile_coords(tile, p.tiles_m, p.tiles_n, tmi, tni);
+  if constexpr (TAIL > 0) {
+    if (tmi == p.tiles_m - 1) {
+      mid_body<CT, GATED, TAIL, SPLIT, NI>(p, sX, tmi * 32 * NI, tni, split);
+      return;
+    }
+  }
+  mid_body<CT, GATED, NI, SPLIT, NI>(p, sX, tmi * 32 * NI, tni, split);
 }
 
 // The join of a split forward: a wave adds one block's partial sums in split order, four
@@ -484,23 +498,30 @@ hipError_t launch_gemm_mid(const WeightView &w, const uint16_t *X, int64_t M, co
   const int64_t wgs = int64_t(b.tiles_m) * b.tiles_n * b.splits;
   if (wgs > 0x7fffffff || (b.splits > 1 && !part)) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(wgs)), block(NT);
-  auto go = [&](auto ct, auto g, auto ni) -> hipError_t {
-    constexpr int CT = decltype(ct)::value, NI = decltype(ni)::value;
+  auto go = [&](auto ct, auto g, auto ni, auto tail) -> hipError_t {
+    constexpr int CT = decltype(ct)::value, NI = decltype(ni)::value, TAIL = decltype(tail)::value;
     constexpr bool GATED = decltype(g)::value;
     if (b.splits == 1) {
-      hipLaunchKernelGGL((gemm_mid_kernel<CT, GATED, NI, false>), grid, block, 0, stream, p);
+      hipLaunchKernelGGL((gemm_mid_kernel<CT, GATED, NI, false, TAIL>), grid, block, 0, stream, p);
       return hipGetLastError();
     }
-    hipLaunchKernelGGL((gemm_mid_kernel<CT, GATED, NI, true>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((gemm_mid_kernel<CT, GATED, NI, true, TAIL>), grid, block, 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 jgrid(static_cast<unsigned>(int64_t(b.tiles_m) * b.tiles_n * NI));
     hipLaunchKernelGGL((gemm_mid_join_kernel<GATED, NI>), jgrid, block, 0, stream, p);
     return hipGetLastError();
   };
+  const int64_t last = M - int64_t(b.tiles_m - 1) * 32 * b.ni;  // tokens of the last tile
   auto with_ni = [&](auto ct, auto g) {
-    return b.ni == 1 ? go(ct, g, std::integral_constant<int, 1>{})
-           : b.ni == 2 ? go(ct, g, std::integral_constant<int, 2>{}) : go(ct, g, std::integral_constant<int, 4>{});
+    using std::integral_constant;
+    if (b.ni == 1) return go(ct, g, integral_constant<int, 1>{}, integral_constant<int, 0>{});
+    if (b.ni == 2)
+      return last <= 32 ? go(ct, g, integral_constant<int, 2>{}, integral_constant<int, 1>{})
+                        : go(ct, g, integral_constant<int, 2>{}, integral_constant<int, 0>{});
+    return last <= 32   ? go(ct, g, integral_constant<int, 4>{}, integral_constant<int, 1>{})
+           : last <= 64 ? go(ct, g, integral_constant<int, 4>{}, integral_constant<int, 2>{})
+                        : go(ct, g, integral_constant<int, 4>{}, integral_constant<int, 0>{});
   };
   auto with_g = [&](auto ct) { return gated ? with_ni(ct, std::true_type{}) : with_ni(ct, std::false_type{}); };
   switch (w.const_type) {

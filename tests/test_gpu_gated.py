@@ -102,6 +102,9 @@ CASES = [
     (18, 64, 2200, 8, "silu", 0.0), (31, 320, 70, 32, "silu", 0.0), (40, 448, 65, 40, "gelu_tanh", 0.0),
     (64, 704, 3000, 16, "silu", 0.0), (96, 576, 130, 96, "silu", 0.1), (129, 2112, 40, 8, "silu", 0.0),
     (20, 17408, 33, 8, "silu", 0.0),  # more than 256 steps: always split
+    # forward tiles of 128 and 64 tokens whose last one has up to 32 or 64, whole and split
+    (777, 512, 3000, 16, "silu", 0.1), (820, 640, 3001, 8, "silu", 0.0), (80, 512, 6000, 16, "gelu_tanh", 0.1),
+    (260, 2048, 600, 8, "silu", 0.0), (140, 4096, 1000, 8, "silu", 0.1), (560, 4096, 300, 72, "silu", 0.0),
     # dX on tiles of 64 and 128 tokens, split; on the large tiles, split, with padded blocks
     (1500, 512, 1501, 12, "silu", 0.1), (4000, 320, 1001, 12, "gelu_tanh", 0.1), (300, 64, 4097, 20, "silu", 0.25),
     (100, 256, 4100, 80, "silu", 0.1),
