@@ -430,7 +430,8 @@ constexpr int NBUF = 3;
 // call: 704 us, 1073 TFLOP/s (a bf16 library product of that size: 1239); 2048 x 8192 -> 2 x
 // 22016: 1330 us, 1121.
 template <int CT, bool GATED>
-__device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o, char *sX) {
+__device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o) {
+  __shared__ __attribute__((aligned(16))) char sX[(NBUF + (GATED ? 1 : 0)) * TILE_BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tmi, tni;
@@ -665,14 +666,12 @@ __device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o, char *sX
 template <int CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_fwd_kernel(
     GemmParams p) {
-  __shared__ __attribute__((aligned(16))) char sX[NBUF * TILE_BYTES];
-  gemm_fwd_body<CT, false>(p, GatedOut{}, sX);
+  gemm_fwd_body<CT, false>(p, GatedOut{});
 }
 template <int CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_gated_kernel(
     GemmParams p, GatedOut o) {
-  __shared__ __attribute__((aligned(16))) char sX[(NBUF + 1) * TILE_BYTES];
-  gemm_fwd_body<CT, true>(p, o, sX);
+  gemm_fwd_body<CT, true>(p, o);
 }
 
 // ===================================== backward ====================================
@@ -1040,8 +1039,13 @@ __device__ __forceinline__ void store_dx_part(const GemmParams &p, float *part, 
 // matrix units as the kernel without EXT is.
 // SPLIT: one part of the contraction, see dx_split.
 template <int CT, bool EXT, bool SPLIT = false>
-__device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x, char *sW0, char *sW1, char *sY0,
-                                             char *sY1) {
+__device__ __forceinline__ void dx_pipe_body(GemmParams p, DxExt x) {
+  // two weight tiles and two dY stages, 128 KB; separate objects, so that the
+  // compiler can tell reads of one stage or tile from the loads into the other stage
+  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
+  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
   // the workgroups after the tiles (dispatched last, so in CUs the tiles have left) do
   // the finalize job that rides in this launch
   const int tile_wgs = SPLIT ? p.tiles * x.splits : p.tiles;
@@ -1339,31 +1343,17 @@ __global__ __launch_bounds__(NT) void dx_join_kernel(const float *__restrict__ p
 template <int CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_pipe_kernel(
     GemmParams p) {
-  // two weight tiles and two dY stages, 128 KB; separate objects, so that the
-  // compiler can tell reads of one stage or tile from the loads into the other stage
-  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
-  dx_pipe_body<CT, false>(p, DxExt{}, sW0, sW1, sY0, sY1);
+  dx_pipe_body<CT, false>(p, DxExt{});
 }
 template <int CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_ext_kernel(
     GemmParams p, DxExt x) {
-  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
-  dx_pipe_body<CT, true>(p, x, sW0, sW1, sY0, sY1);
+  dx_pipe_body<CT, true>(p, x);
 }
 template <int CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_dx_split_kernel(
     GemmParams p, DxExt x) {
-  __shared__ __attribute__((aligned(16))) char sW0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sW1[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY0[TILE_BYTES];
-  __shared__ __attribute__((aligned(16))) char sY1[TILE_BYTES];
-  dx_pipe_body<CT, true, true>(p, x, sW0, sW1, sY0, sY1);
+  dx_pipe_body<CT, true, true>(p, x);
 }
 
 bool fits_32bit(int64_t M, int64_t N, int64_t K, int r) {
