@@ -321,8 +321,11 @@ __device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, co
   if constexpr (EXT) dk = drop_key(drop);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
+    if (b_lo + 4 * i >= b_hi) break;  // a slice of one step
     const int b = b_lo + 4 * i + g;
     const bool ok = b < b_hi;
+    // lanes past the slice multiply zeros on both sides (A's zeros times an infinity would be
+    // NaN, and the mask made for block b is not that of the block read in its place)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       u32x4_t keep;
@@ -334,6 +337,7 @@ __device__ void lora_finish(const GemvArgs &a, const char *sx, int KB, int p, co
         // the staged X is permuted per 8-element group: permute A the same way
         u32x4_t x = *reinterpret_cast<const u32x4_t *>(sx + tok * xrow_bytes(KB) + (ok ? b : 0) * 128 + u * 16);
         if constexpr (EXT) x = x & permute8(keep);
+        if (!ok) x = u32x4_t{0u, 0u, 0u, 0u};
         acc = mfma16x16x32(permute8(ll.av[i][u]), x, acc);
       } else {
         u32x4_t x = ll.xv[i][u];

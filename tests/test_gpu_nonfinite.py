@@ -1,0 +1,71 @@
+"""Infinities and NaN where they have to stay apart: what is dropped for the adapter, what lies
+past a lane's own blocks, the other projection's ranks.  A zero that a kernel puts in by
+itself must never meet an infinity (their product is NaN, where the definition has none)."""
+
+import numpy as np
+import pytest
+
+from tests import drop_cases as dc
+from tests import gpu_cases as gc
+
+pytestmark = pytest.mark.gpu
+ALPHA = 16.0
+
+
+@pytest.fixture(scope="module")
+def q():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_quantized_lora_nf4_amd as lib
+    return lib
+
+
+def same_kind(got, want):
+    """Infinities of the same sign and NaN in the same places, finite elsewhere."""
+    for f in (np.isposinf, np.isneginf, np.isnan):
+        bad = np.argwhere(f(got) != f(want))
+        assert bad.size == 0, (f.__name__, bad[:4].tolist(), got[tuple(bad[0])], want[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 40])
+@pytest.mark.parametrize("K", [64, 192, 256, 1024])
+def test_dropped_nan_in_any_block_stays_out_of_u(q, M, K):
+    """Row i has NaN at a dropped element of block i (rows past the last block again from the
+    first): the adapter does not see it, whichever lane holds the block."""
+    import torch
+    N, r = 64, 8
+    h = dc.linear_inputs(M, K, N, r, 1, seed=3)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.5, seed=21)
+    m, _ = dc.mask(M, K, 0.5, 21, 0)
+    X = dev["X"].clone()
+    for i in range(M):
+        b = 64 * (i % (K // 64))
+        X[i, b + int(np.flatnonzero(m[i, b:b + 64] == 0)[0])] = float("nan")
+    _, U = q.linear_fwd(qw, dev["X"], dev["A"], dev["B"], ALPHA, dropout=d)
+    _, U2 = q.linear_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+    assert torch.equal(U, U2)
+
+
+@pytest.mark.parametrize("dropout", [False, True])
+@pytest.mark.parametrize("K", [64, 192, 256, 1024])
+def test_infinite_input_of_the_adapter(q, K, dropout):
+    """One infinite (kept) element in block i of row i: U is infinite with the sign that the
+    definition gives, for one token to 16 and for tiles."""
+    N, r, M = 64, 8, 16
+    h = dc.linear_inputs(40, K, N, r, 1, seed=5)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    d = q.Dropout(0.5, seed=22) if dropout else None
+    m = dc.mask(40, K, 0.5, 22, 0)[0] if dropout else np.ones((40, K))
+    X, col = dev["X"].clone(), []
+    for i in range(40):
+        b = 64 * (i % (K // 64))
+        col.append(b + int(np.flatnonzero(m[i, b:b + 64])[3]))
+        X[i, col[-1]] = float("inf")
+    want = np.inf * gc.f64(h["A"])[:, col].T
+    for rows in (1, 3, M, 40):
+        _, U = q.linear_fwd(qw, X[:rows].contiguous(), dev["A"], dev["B"], ALPHA, dropout=d)
+        same_kind(dc.bits(U), want[:rows])
