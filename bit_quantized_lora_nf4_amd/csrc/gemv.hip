@@ -621,16 +621,22 @@ __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char
       dma16(rx, stage + wave * kXdmaStage + q * 1024, ok ? xq_off[q] + static_cast<uint32_t>(bp + xq_blk[q]) * 128 : kOOB);
     }
   };
+  // staged X: this lane's token row, and 128 bytes of zeros that stand for the blocks past the
+  // wave's range (their weights are zeros, which an infinity must not meet), in the wave's own
+  // slot of the partial sums, which it writes after its last step
+  const int xrow = lp.x + tok * xrow_bytes(KB), xzero = lp.red + wave * 1024;
+  if constexpr (XLDS) *reinterpret_cast<u32x4_t *>(lds + xzero + lane * 16) = u32x4_t{0u, 0u, 0u, 0u};
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
   auto compute = [&](const Loads &s, int t, const char *stage) {
     const int b = kb0 + 4 * t + g;
     const Planes pl = make_planes(constant_of<CT, !XREG>(s, gc, row_blk + b, row_ok && b < kb1), a.lvl);
+    const int xo = b < kb1 ? xrow + b * 128 : xzero;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const uint32_t cw = u < 4 ? s.c0[u] : s.c1[u - 4];
       u32x4_t xv;
       if constexpr (XLDS)
-        xv = *reinterpret_cast<const u32x4_t *>(sx + tok * xrow_bytes(KB) + (b < kb1 ? b : kb0) * 128 + u * 16);
+        xv = *reinterpret_cast<const u32x4_t *>(lds + xo + u * 16);
       else if constexpr (XDMA)
         xv = permute8(*reinterpret_cast<const u32x4_t *>(stage + xr_off[u]));
       else

@@ -69,3 +69,33 @@ def test_infinite_input_of_the_adapter(q, K, dropout):
     for rows in (1, 3, M, 40):
         _, U = q.linear_fwd(qw, X[:rows].contiguous(), dev["A"], dev["B"], ALPHA, dropout=d)
         same_kind(dc.bits(U), want[:rows])
+
+
+@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("K", [64, 192, 256, 320, 448, 1088])
+def test_infinite_input_in_any_block(q, M, K):
+    """Row i has an infinity in its block i (rows past the last block again from the first),
+    dropped for the adapter: the base product is infinite, or NaN where the weight is zero,
+    whichever lane or step holds the block."""
+    N, r = 256, 8
+    h = dc.linear_inputs(M, K, N, r, 1, seed=6)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    Wd = dc.weight64(qw)
+    d = q.Dropout(0.5, seed=23)
+    m, _ = dc.mask(M, K, 0.5, 23, 0)
+    X, col = dev["X"].clone(), []
+    for i in range(M):
+        b = 64 * (i % (K // 64))
+        col.append(b + int(np.flatnonzero(m[i, b:b + 64] == 0)[1]))
+        X[i, col[-1]] = float("inf") if i % 2 else float("-inf")
+    sign = np.where(np.arange(M) % 2, np.inf, -np.inf)
+    with np.errstate(invalid="ignore"):
+        want = sign[:, None] * Wd[:, col].T
+    if m[0].any():
+        Y, _ = q.linear_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+        same_kind(dc.bits(Y), want)
+    Y, _ = q.linear_fwd(qw, X)
+    same_kind(dc.bits(Y), want)
+    _, Y, _ = q.gated_fwd(qw, X)
+    same_kind(dc.bits(Y), want)
