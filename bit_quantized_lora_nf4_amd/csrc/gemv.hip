@@ -714,17 +714,28 @@ __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char
     // U_s of this part is in LDS (the LoRA wave put it there before the barrier)
     const uint16_t *urow = reinterpret_cast<const uint16_t *>(lds + lp.u) + tok * r8;
     const uint16_t *brow = sb + (grp * 16 + ml) * r8;
-    // gated: once per part, the other part's B rows cleared
-    for (int q = 0; q < (gated ? 2 : 1); ++q, urow += a.M * r8)
+    auto up = [&](f32x4_t s) {
       for (int c = 0; c < a.r; c += 32) {
         const int j0 = c + 8 * g;
         const bool in = j0 < a.r;
         u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (in ? j0 : 0));
         u32x4_t uf = *reinterpret_cast<const u32x4_t *>(urow + (in ? j0 : 0));
-        if (!in || (gated && (ml >> 3) != q)) bf = u32x4_t{0u, 0u, 0u, 0u};
+        if (!in) bf = u32x4_t{0u, 0u, 0u, 0u};
         if (!(in && tok_ok)) uf = u32x4_t{0u, 0u, 0u, 0u};
-        y = mfma16x16x32(bf, uf, y);
+        s = mfma16x16x32(bf, uf, s);
       }
+      return s;
+    };
+    // gated: each part's U_s in sums of its own, of which the lanes of its rows take theirs
+    // (in common sums a part's infinities would meet the other's zeros)
+    const f32x4_t y0 = up(y);
+    if (gated) {
+      urow += a.M * r8;
+      const f32x4_t y1 = up(y);
+      y = g < 2 ? y0 : y1;
+    } else {
+      y = y0;
+    }
   } else if (a.R > 0) {
     // U_s from the LoRA waves: poll this workgroup's flag (and clear it for the next
     // call), then read this workgroup's copy of U_s (one row group per workgroup on this
@@ -742,12 +753,12 @@ __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char
     // operand) from the staged Bl tile, tokens (the B operand) from U_s
     const bool aligned = (a.r & 7) == 0;
     const uint16_t *brow = sb + (grp * 16 + ml) * r8;
-    auto up = [&](int q, bool own) {  // own: this lane's B row is of part q
+    auto up = [&](int q, f32x4_t s) {
       const uint32_t ubase = static_cast<uint32_t>((blockIdx.x % a.NC) * a.UCE + tok * RP + q * a.r);
       for (int c = 0; c < a.r; c += 32) {
         const int j0 = c + 8 * g;
         u32x4_t bf = *reinterpret_cast<const u32x4_t *>(brow + (j0 < a.r ? j0 : 0));
-        if (j0 >= a.r || !own) bf = u32x4_t{0u, 0u, 0u, 0u};
+        if (j0 >= a.r) bf = u32x4_t{0u, 0u, 0u, 0u};
         u32x4_t uf = u32x4_t{0u, 0u, 0u, 0u};
         if (tok_ok && j0 < a.r) {
           if (aligned) {
@@ -763,14 +774,15 @@ __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char
             }
           }
         }
-        y = mfma16x16x32(bf, uf, y);
+        s = mfma16x16x32(bf, uf, s);
       }
+      return s;
     };
-    if (gated) {
-      up(0, ml < 8);
-      up(1, ml >= 8);
+    if (gated) {  // (as above)
+      const f32x4_t y0 = up(0, y), y1 = up(1, y);
+      y = g < 2 ? y0 : y1;
     } else {
-      up(a.part_rows > 0 ? n0 / a.part_rows : 0, true);
+      y = up(a.part_rows > 0 ? n0 / a.part_rows : 0, y);
     }
   }
   if (gated) {

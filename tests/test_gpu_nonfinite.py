@@ -99,3 +99,25 @@ def test_infinite_input_in_any_block(q, M, K):
     same_kind(dc.bits(Y), want)
     _, Y, _ = q.gated_fwd(qw, X)
     same_kind(dc.bits(Y), want)
+
+
+@pytest.mark.parametrize("M,K,P,r", [
+    (1, 256, 72, 8), (3, 256, 71, 12), (16, 512, 264, 64), (16, 8192, 136, 8),  # one launch
+    (300, 64, 4097, 20), (700, 64, 5637, 72),
+])
+@pytest.mark.parametrize("part", [0, 1])
+def test_non_finite_ranks_stay_in_their_projection(q, M, K, P, r, part):
+    """Infinite and NaN ranks of one projection's adapter leave the other projection alone."""
+    import torch
+    h = dc.linear_inputs(M, K, P, r, 2, seed=7)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    _, Y, U = q.gated_fwd(qw, dev["X"], dev["A"], dev["B"], ALPHA)
+    A = dev["A"].clone()
+    A[part * r, K // 2] = float("inf")
+    A[part * r + r - 1, 0] = float("nan")
+    _, Y2, U2 = q.gated_fwd(qw, dev["X"], A, dev["B"], ALPHA)
+    own, other = slice(part * P, (part + 1) * P), slice((1 - part) * P, (2 - part) * P)
+    assert torch.equal(U2[:, (1 - part) * r:(2 - part) * r], U[:, (1 - part) * r:(2 - part) * r])
+    assert not bool(torch.isfinite(Y2[:, own]).any())
+    assert torch.equal(Y2[:, other], Y[:, other])
