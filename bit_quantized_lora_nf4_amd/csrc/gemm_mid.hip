@@ -218,37 +218,57 @@ __device__ __forceinline__ void mid_body(const MidParams &p, char *sX, int m0, i
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
 
-  // The LoRA term first, 64 stacked ranks at a time through the ring's last buffer (U rows
-  // past M clamped like X's, ranks past the end read as zero); split 0 adds it.
-  const int R = GATED ? 2 * p.r : p.r;
+  // The LoRA term first, 64 ranks at a time through the ring's last buffer (U rows past M
+  // clamped like X's, ranks past the end read as zero); split 0 adds it.  Gated: both
+  // projections' ranks at a time, the up projection's through the buffer before it and into sums
+  // of their own, of which its rows (elements 8..15 of a block) are taken: in common sums a
+  // projection's infinities would meet the zeros of the other's rows.
   if (p.r > 0 && split == 0) {
-    const int part = GATED ? (lane & 31) >> 4 : 0;
+    constexpr int PARTS = GATED ? 2 : 1;
     const int qc = !GATED && p.part_rows > 0 ? (c0 / p.part_rows) * p.r : 0;
     const __amdgpu_buffer_rsrc_t ru = make_rsrc(p.U, static_cast<uint32_t>(uint64_t(p.M) * p.ldu * 2));
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.Bl, static_cast<uint32_t>(uint64_t(p.N) * p.r * 2));
-    char *const sU = sX + (RING - 1) * TILE;
-    for (int t = 0; t < R; t += TK) {
+    f32x16_t up[GATED ? NI : 1];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int x = (wave * NI + i) * 8 + (lane >> 3);
-        const int j = t + ((lane & 7) ^ swz(x)) * 8;
-        const uint32_t off =
-            j < R ? (static_cast<uint32_t>(min(m0 + x, p.M - 1)) * p.ldu + qc + j) * 2 : kOOB;
-        dma16(ru, sU + (wave * NI + i) * 1024, off, 0);
-      }
+    for (int i = 0; i < (GATED ? NI : 1); ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) up[i][e] = 0.0f;
+    for (int t = 0; t < p.r; t += TK) {
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int x = (wave * NI + i) * 8 + (lane >> 3);
+          const int j = t + ((lane & 7) ^ swz(x)) * 8;
+          const uint32_t off =
+              j < p.r ? (static_cast<uint32_t>(min(m0 + x, p.M - 1)) * p.ldu + (GATED ? q * p.r : qc) + j) * 2 : kOOB;
+          dma16(ru, sX + (RING - 1 - q) * TILE + (wave * NI + i) * 1024, off, 0);
+        }
+      // 8 ranks of this lane's row (every lane's row takes part in one of the two sums)
       u32x4_t wl[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        // 8 ranks of this lane's row, within one part (r is a multiple of 8)
-        const int j = t + 32 * (lane >> 5) + 8 * s - part * p.r;
-        wl[s] = buf_load16(rb, row_ok && j >= 0 && j < p.r ? (static_cast<uint32_t>(n) * p.r + j) * 2 : kOOB);
+        const int j = t + (GATED ? 16 * s + 8 * half : 32 * half + 8 * s);
+        wl[s] = buf_load16(rb, row_ok && j < p.r ? (static_cast<uint32_t>(n) * p.r + j) * 2 : kOOB);
       }
       asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s) {
+        if (GATED && t + 16 * s >= p.r) break;  // (no ranks left for this sub-step)
+        const int c = GATED ? 2 * s + half : 4 * half + s;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) acc[i] = mfma32x32x16(wl[s], frag(sU, 4 * half + s, i), acc[i]);
+        for (int i = 0; i < NI; ++i) {
+          acc[i] = mfma32x32x16(wl[s], frag(sX + (RING - 1) * TILE, c, i), acc[i]);
+          if constexpr (GATED) up[i] = mfma32x32x16(wl[s], frag(sX + (RING - 2) * TILE, c, i), up[i]);
+        }
+      }
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // read before it is loaded again
+    }
+    if constexpr (GATED) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 8; e < 16; ++e) acc[i][e] = up[i][e];
     }
   }
 

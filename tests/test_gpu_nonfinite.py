@@ -103,7 +103,8 @@ def test_infinite_input_in_any_block(q, M, K):
 
 @pytest.mark.parametrize("M,K,P,r", [
     (1, 256, 72, 8), (3, 256, 71, 12), (16, 512, 264, 64), (16, 8192, 136, 8),  # one launch
-    (300, 64, 4097, 20), (700, 64, 5637, 72),
+    (40, 256, 72, 8), (40, 448, 65, 40), (130, 256, 136, 72), (70, 512, 136, 128), (777, 512, 3000, 16),
+    (18, 64, 2200, 8), (300, 64, 4097, 20), (700, 64, 5637, 72),
 ])
 @pytest.mark.parametrize("part", [0, 1])
 def test_non_finite_ranks_stay_in_their_projection(q, M, K, P, r, part):
