@@ -273,10 +273,11 @@ __device__ __forceinline__ void mid_body(const MidParams &p, char *sX, int m0, i
   }
 
   // Two steps, 4 a + 2 jp and the next: lane half h takes the whole block of step h from tile
-  // t + h; with `single` there is no second step, and half 1 adds zeros.  The codes' fragments
-  // are decoded and the X fragments read one sub-step ahead of the MFMAs that use them.
+  // t + h; with `single` there is no second step, and half 1 adds zeros (its tile is cleared
+  // too: zero weights alone would make NaN of an infinity).  The codes' fragments are decoded
+  // and the X fragments read one sub-step ahead of the MFMAs that use them.
   auto compute = [&](const char *tiles2, const Codes<CT> &cs, int jp, int it, bool single) {
-    const char *t = tiles2 + (single ? 0 : half * TILE);  // (zeros times a buffer never written could be NaN)
+    const char *t = tiles2 + half * TILE;
     float c = constant(cs, jp, it + half);
     if (single && half) c = 0.0f;
     const Planes pl = make_planes(c, p.lvl);
@@ -333,11 +334,21 @@ __device__ __forceinline__ void mid_body(const MidParams &p, char *sX, int m0, i
     it += RING;
     ca = cb;
   }
-  // the last nk % 4 steps
+  // the last nk % 4 steps; a wave clears its part of the tile behind an odd last one
+  auto clear_x = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      *reinterpret_cast<u32x4_t *>(sX + slot * TILE + (wave * NI + i) * 1024 + lane * 16) = u32x4_t{0u, 0u, 0u, 0u};
+  };
   const int rem = nk - it;
   if (rem > 0) {
+    if (rem == 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // slot 1 still takes the repeated last tile
+      clear_x(1);
+    }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     issue_x(it + 2);
+    if (rem == 3) clear_x(3);  // (no load into slot 3 is in flight, and no wave reads it any more)
     compute(sX, ca, 0, it, rem == 1);
     if (rem == 3) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");

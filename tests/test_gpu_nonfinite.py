@@ -71,7 +71,7 @@ def test_infinite_input_of_the_adapter(q, K, dropout):
         same_kind(dc.bits(U), want[:rows])
 
 
-@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("M", [1, 7, 16, 40, 300])
 @pytest.mark.parametrize("K", [64, 192, 256, 320, 448, 1088])
 def test_infinite_input_in_any_block(q, M, K):
     """Row i has an infinity in its block i (rows past the last block again from the first),
