@@ -624,9 +624,11 @@ struct FinalizeJobs {
 __device__ __forceinline__ void finalize_v(const FinalizeJob &j, int64_t i, int64_t lo) {
   const f32x4_t v = split_sum(j.P, j.splits, j.count, i) * j.scale;
   const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  // exact differences: hi is within half a step of v (and NaN or infinity leave NaN)
-  const u32x2_t rest = {pack_bf16x2(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
-                        pack_bf16x2(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
+  // exact differences: hi is within half a step of v; none where hi is infinite (v - hi is an
+  // infinity of the other sign, or NaN, and dA's sum with it NaN)
+  auto left = [](float x, float h) { return __builtin_fabsf(h) == __builtin_inff() ? 0.0f : x - h; };
+  const u32x2_t rest = {pack_bf16x2(left(v[0], bf16_lo(hi[0])), left(v[1], bf16_hi(hi[0]))),
+                        pack_bf16x2(left(v[2], bf16_lo(hi[1])), left(v[3], bf16_hi(hi[1])))};
   const int64_t e = 4 * i, row = e / j.cols, col = e % j.cols;
   uint16_t *const out = j.OUT + row * j.ldout + col;
   *reinterpret_cast<u32x2_t *>(out) = hi;

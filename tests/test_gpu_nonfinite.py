@@ -122,3 +122,31 @@ def test_non_finite_ranks_stay_in_their_projection(q, M, K, P, r, part):
     assert torch.equal(U2[:, (1 - part) * r:(2 - part) * r], U[:, (1 - part) * r:(2 - part) * r])
     assert not bool(torch.isfinite(Y2[:, own]).any())
     assert torch.equal(Y2[:, other], Y[:, other])
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_infinite_v_gives_infinite_da(q, M):
+    """V = (alpha / r) dY B past the largest bf16 value: dA's rows are infinite with the signs of
+    the definition (what V's rounding took off is not a number there and must not be added)."""
+    import torch
+    K, P, r = 128, 64, 8
+    h = dc.linear_inputs(M, K, P, r, 2, seed=8)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    g = np.random.default_rng(1)
+    sign = g.choice([-1.0, 1.0], r)
+    i, c = M // 2, 5
+    Y = torch.zeros(M, 2 * P, dtype=torch.bfloat16, device="cuda")
+    Y[:, :P] = 1.0  # act(1) = 0.73
+    dH = torch.zeros(M, P, dtype=torch.bfloat16, device="cuda")
+    dH[i, c] = 1e37
+    B = dev["B"].clone()
+    B[P + c] = torch.tensor(sign * 1e3, device="cuda").bfloat16()
+    X = dev["X"].clone()
+    X[X == 0] = 1.0
+    U = torch.zeros(M, 2 * r, dtype=torch.bfloat16, device="cuda")
+    _, dA, _ = q.gated_bwd(qw, dH, Y, X, dev["A"], B, ALPHA, U)
+    want = np.zeros((2 * r, K))
+    want[r:] = sign[:, None] * np.inf * dc.bits(X)[i][None, :]
+    same_kind(dc.bits(dA), want)
+    assert np.all(dc.bits(dA)[:r] == 0.0)
