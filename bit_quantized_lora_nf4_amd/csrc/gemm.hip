@@ -1489,7 +1489,8 @@ hipError_t launch_gemm_dx_ext(const WeightView &w, const uint16_t *dY, int64_t M
                               hipStream_t stream, const FinalizeJob *fin) {
   const int64_t Np = w.n_rows / parts, half = (Np + 7) / 8 * 8, Kc = parts > 1 ? parts * half : half;
   if (w.n_rows % parts != 0 || (parts > 2 && half != Np)) return hipErrorInvalidValue;
-  if (!fits_32bit(M, Kc, w.n_cols, r) || M > 0x7fffffff) return hipErrorInvalidValue;
+  // the padding is dY's alone: the weight's arrays have n_rows rows (as gemm_supported counts them)
+  if (!gemm_supported(w, M, r) || uint64_t(M) * Kc * 2 > 0xFFFFFFF0ull) return hipErrorInvalidValue;
   if (dx_mid_takes(M, w.n_cols, Kc))
     return launch_dx_mid(w, dY, M, Kc, half == Np ? Kc : half, half - Np, V, At, r, dX, d, part, stream, fin);
   GemmParams p = make_params(dY, w, V, At, dX, M, w.n_cols, Kc, r);
