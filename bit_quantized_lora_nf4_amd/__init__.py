@@ -260,10 +260,19 @@ def workspace(op, M, K, N, r, device):
     return torch.zeros(max(n, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=device)
 
 
+_CLEAR_WHOLE_BYTES = 4 << 20
+
+
 def _scratch(nbytes, device):
-    """A workspace for one call: only its header has to start at zero."""
+    """A workspace for one call.  Only its header has to start at zero; up to 4 MiB it is
+    cleared whole all the same, which is one call less (5.5 us on the host instead of 6.7, the
+    fill itself as fast as that of the header), while clearing 77 MiB of partial sums takes
+    11.7 us."""
     torch = _torch()
-    ws = torch.empty(max(nbytes, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=device)
+    nbytes = max(nbytes, _lib.QLORA_WORKSPACE_HEADER_BYTES)
+    if nbytes <= _CLEAR_WHOLE_BYTES:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     ws[:_lib.QLORA_WORKSPACE_HEADER_BYTES].zero_()
     return ws
 
@@ -369,7 +378,7 @@ def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws, dropout=None
         if dB is None:
             dB = torch.empty((N, r), dtype=torch.bfloat16, device=dev)
         if ws is None:
-            ws = torch.zeros(max(nbytes, _lib.QLORA_WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=dev)
+            ws = _scratch(nbytes, dev)
     if drop is not None:
         with _guard(dev):
             st = qlora_linear_bwd_dropout(qw.descriptor(), parts, dY.data_ptr(), _ptr(X), M, _ptr(A), _ptr(B), r,
@@ -494,7 +503,7 @@ def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=
     if r and save_u and U is None:
         U = torch.empty((M, R), dtype=torch.bfloat16, device=dev)
     if ws is None and nbytes > 0:
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        ws = _scratch(nbytes, dev)
     if drop is not None:
         with _guard(dev):
             st = qlora_linear_fwd_dropout(qw.descriptor(), n_parts, X.data_ptr(), M, _ptr(A), _ptr(B), r,
