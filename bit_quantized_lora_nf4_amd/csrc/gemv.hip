@@ -115,7 +115,8 @@ struct GemvArgs {
   int NC, UCE;
   float scale;
   int M, R, r, part_rows;
-  int W, T;             // weight waves per row group, steps of 4 blocks per weight wave
+  int W;                // weight waves per row group
+  int PW;               // workgroups (the first ones) that compute pieces
   int RG;               // row groups (16-row tiles) per workgroup, sharing the staged X
   int PT, SP, LB, G;    // rank tiles, pieces per rank tile and their 64-blocks, workgroups
   LevelTable lvl;
@@ -517,14 +518,15 @@ __device__ __forceinline__ void gemv_body(GemvArgs a, GemvExt x, char *lds, char
     // weight waves (the staging barrier and the one of the final reduction).
     const int npieces = a.PT * a.SP;
     LoraLoads<XLDS> ll;
-    if (static_cast<int>(blockIdx.x) < npieces) ll = lora_issue<XLDS>(a, KB, blockIdx.x);
+    if (static_cast<int>(blockIdx.x) < (MULTI ? a.PW : npieces)) ll = lora_issue<XLDS>(a, KB, blockIdx.x);
     __syncthreads();
-    if (static_cast<int>(blockIdx.x) < npieces)
+    if (static_cast<int>(blockIdx.x) < (MULTI ? a.PW : npieces))
       lora_finish<XLDS, DIRECT, EXT>(a, lds + lp.x, KB, blockIdx.x, ll, x.drop);
     if constexpr (MULTI) {
-      // more pieces than workgroups (few output rows): the later ones one after another
+      // more pieces than workgroups for them (few output rows): the later ones one after another
       // (a separate instantiation: the loop costs the kernel about 35 registers)
-      for (int p = blockIdx.x + gridDim.x; p < npieces; p += gridDim.x) {
+      const int first = static_cast<int>(blockIdx.x) < a.PW ? static_cast<int>(blockIdx.x) + a.PW : npieces;
+      for (int p = first; p < npieces; p += a.PW) {
         const LoraLoads<XLDS> lp2 = lora_issue<XLDS>(a, KB, p);
         lora_finish<XLDS, DIRECT, EXT>(a, lds + lp.x, KB, p, lp2, x.drop);
       }
@@ -963,6 +965,19 @@ GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int R, bool allow_rg = true)
   return p;
 }
 
+// Workgroups that compute LoRA pieces, of G.  Every workgroup waits for all the pieces, so those
+// that compute them must be on the card together, and the grid's first ones are dispatched first.
+// All of the grid may, unless there are more with pieces than the plan's waves and LDS let the
+// CUs hold at once (thousands of rank x column slices): then those that fit however a workgroup's
+// waves fall on the four SIMDs, with several pieces each.
+int piece_wgs(const GemvPlan &p, int R, int pieces, int G) {
+  const int waves = p.RG * p.sh.W + (R > 0 ? 1 : 0), simd = p.xlds ? 5 : 4;  // waves a SIMD holds
+  const bool per_wave = !p.xlds && p.xdma && p.RG == 1 && p.sh.W <= kXdmaWaves;
+  const int lds = 160 * 1024 / std::max(p.lds_bytes + (per_wave ? 2 * kXdmaWaves * kXdmaStage : 0), 1);
+  if (std::min(pieces, G) <= 256 * std::max(std::min(4 * simd / waves, lds), 1)) return G;
+  return std::min(G, 256 * std::max(std::min(simd / ((waves + 3) / 4), lds), 1));
+}
+
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // Copies of U_s [M][16 PT] bf16 published by the LoRA waves.
@@ -1021,7 +1036,7 @@ hipError_t go_gemv1(const GemvArgs &a, const GemvExt &x, int lds_bytes, hipStrea
 }
 template <bool EXT, int CT, bool XLDS>
 hipError_t go_gemv(const GemvArgs &a, const GemvExt &x, bool direct, bool xdma, int lds_bytes, hipStream_t stream) {
-  const bool multi = a.PT * a.SP > a.G;
+  const bool multi = a.PT * a.SP > a.PW;
   if constexpr (!XLDS) {
     // the XDMA layout with one row group and at most kXdmaWaves weight waves
     if (xdma && a.RG == 1 && a.W <= kXdmaWaves) {
@@ -1063,10 +1078,10 @@ hipError_t run_gemv(const GemvPlan &p, const WeightView &w, const uint16_t *X, i
   a.part_rows = static_cast<int>(part_rows);
   a.W = p.sh.W;
   a.RG = p.RG;
-  a.T = p.sh.T;
   a.LB = p.LB;
   a.SP = R > 0 ? p.SP : 0;
   a.G = static_cast<int>(((N + 15) / 16 + p.RG - 1) / p.RG);
+  a.PW = piece_wgs(p, R, a.PT * a.SP, a.G);
   a.lvl = level_table(w.quant_type);
   switch (w.const_type) {
     case kConstDqInt8:

@@ -74,3 +74,31 @@ def test_code_arrays_near_four_gib(q, parts, N):  # noqa: F811
     dc.check("dB", dc.bits(dB[at_rows]), *want["dB"])
     dB[at_rows] = 0
     assert int(dB.count_nonzero()) == 0
+
+
+def _random_weight(q, N, K, gen):
+    import torch
+    blocks = N * K // 64
+    groups = -(-blocks // 256)
+    return q.NF4Weight(torch.randint(0, 256, (N * K // 2,), dtype=torch.uint8, device="cuda", generator=gen),
+                       torch.randint(-127, 128, (blocks,), dtype=torch.int8, device="cuda", generator=gen),
+                       torch.rand(groups, device="cuda", generator=gen) * 1e-4,
+                       torch.rand(groups, device="cuda", generator=gen) * 0.02 + 0.02, N, K)
+
+
+def test_more_slices_than_workgroups_at_once(q):  # noqa: F811
+    """One token of 65536 columns at rank 256: 4096 rank x column slices, more than the card
+    holds of the workgroups that wait for them."""
+    import torch
+    M, K, N, r = 1, 65536, 65536, 256
+    print(f"small M: {M} x {K} -> {N}, rank {r}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    qw = _random_weight(q, N, K, gen)
+    X = torch.randn(M, K, device="cuda", generator=gen).bfloat16()
+    A = (torch.randn(r, K, device="cuda", generator=gen) / 8).bfloat16()
+    B = (torch.randn(N, r, device="cuda", generator=gen) * 0.1).bfloat16()
+    _, U = q.linear_fwd(qw, X, A, B, ALPHA)
+    torch.cuda.synchronize()
+    f = gc.host_f32_from_bf16
+    want, e = dc.down(f(X), f(A), ALPHA, r, np.ones((M, K)), 1.0)
+    dc.check("U", dc.bits(U), want, e)
