@@ -170,7 +170,7 @@ struct FwdLayout {
 // caller does not keep it) then the fp32 partial sums of lora_down; nothing when r = 0.
 FwdLayout fwd_layout(int64_t M, int64_t K, int64_t N, int r, bool need_u) {
   FwdLayout L;
-  if (qlora::gemv_shape_ok(M, N)) {
+  if (qlora::gemv_shape_ok(M, N, K)) {
     L.total = qlora::gemv_workspace(M, K, N, r);
     return L;
   }
@@ -258,7 +258,7 @@ int fwd_impl(const char *who, const qlora_nf4_weight *w, int parts, const uint16
   if (need_ws && !aligned16(workspace))
     return fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
   const qlora::WeightView wv = view(w);
-  const bool small = qlora::gemv_shape_ok(M, wv.n_rows);
+  const bool small = qlora::gemv_shape_ok(M, wv.n_rows, wv.n_cols);
   if (small ? !qlora::gemv_supported(wv, M, R) : !qlora::gemm_supported(wv, M, R))
     return fail(QLORA_ERR_SHAPE, "%s: a tensor of %lld x %lld x %lld exceeds 32-bit buffer offsets", who,
                 (long long)M, (long long)K, (long long)N);

@@ -488,7 +488,7 @@ bool mid_takes(int64_t M, int64_t K, int64_t N, bool gated) {
 // weights (gated, 1 x 4096 -> 2 x 11008: 24.5; 16: 38; 1 x 8192 -> 2 x 22016: 88; 16: 134),
 // these tiles their plan's time and two launches of about 5 us for U (33, 33, 74, 78).
 bool gemv_takes(int64_t M, int64_t K, int64_t N, int r, bool gated) {
-  if (!gemv_shape_ok(M, N)) return false;
+  if (!gemv_shape_ok(M, N, K)) return false;
   const double gemv = 4.0 + double(N) * K * 1e-6 * (0.23 + 0.008 * M);
   return gemv < mid_plan(M, K, tile_cols(N, gated)).cost + (r > 0 ? 10.0 : 0.0);
 }

@@ -854,17 +854,19 @@ __global__ __launch_bounds__(kMaxWaves * 64) void gemv_ext_kernel(GemvArgs a, Ge
 // weight waves of T = ceil(ceil(KB / W) / 4) steps each, the decode time of the launch.
 // W minimises that product (a lone wave per SIMD counts 30% more: it cannot hide its own
 // dependency chains), within the waves a CU holds at once (`max_cu_waves`, counting the
-// LoRA wave of each workgroup, `extra`), preferring fewer steps.
+// LoRA wave of each workgroup, `extra`), preferring fewer steps.  At least as many that a wave's
+// range is at most 256 blocks, which touch two groups of constants at most (load_groups).
 struct GemvShape {
   int W, T;
 };
+int64_t min_waves(int64_t KB) { return (KB + 255) / 256; }
 GemvShape gemv_shape(int64_t N, int64_t K, int max_cu_waves, int extra) {
-  const int64_t tiles = (N + 15) / 16, KB = K / 64;
+  const int64_t tiles = (N + 15) / 16, KB = K / 64, first = min_waves(KB);
   const int64_t c = (tiles + 255) / 256;
   GemvShape best{1, static_cast<int>((KB + 3) / 4)};
   double best_cost = 1e30;
-  for (int W = 1; W + extra <= kMaxWaves; ++W) {
-    if (W > 1 && (c * (W + extra) > max_cu_waves || W > KB)) break;
+  for (int W = static_cast<int>(first); W + extra <= kMaxWaves; ++W) {
+    if (W > first && (c * (W + extra) > max_cu_waves || W > KB)) break;
     const int64_t T = ((KB + W - 1) / W + 3) / 4;
     const int64_t per_simd = (c * W + 3) / 4;
     const double cost = double(per_simd * T) * (per_simd == 1 ? 1.3 : 1.0);
@@ -877,12 +879,13 @@ GemvShape gemv_shape(int64_t N, int64_t K, int max_cu_waves, int extra) {
 }
 
 // Row groups of W weight waves in workgroups of RG tiles, one workgroup per CU: W
-// minimises the busiest SIMD's wave-steps within the 16 waves of a workgroup.
+// minimises the busiest SIMD's wave-steps within the 16 waves of a workgroup (none for rows of
+// more blocks than they may take).
 GemvShape gemv_shape_rg(int64_t K, int RG, int extra) {
   const int64_t KB = K / 64;
-  GemvShape best{1, static_cast<int>((KB + 3) / 4)};
+  GemvShape best{0, 0};
   double best_cost = 1e30;
-  for (int W = 1; RG * W + extra <= kMaxWaves && W <= KB; ++W) {
+  for (int W = static_cast<int>(min_waves(KB)); RG * W + extra <= kMaxWaves && W <= KB; ++W) {
     const int64_t T = ((KB + W - 1) / W + 3) / 4;
     const int64_t per_simd = (RG * W + 3) / 4;
     const double cost = double(per_simd * T) * (per_simd == 1 ? 1.3 : 1.0);
@@ -950,7 +953,7 @@ GemvPlan gemv_plan(int64_t M, int64_t K, int64_t N, int R, bool allow_rg = true)
     q.sh = gemv_shape_rg(K, rg, extra);
     q.xlds = true;
     lora_slices(q, KB);
-    if (lds_plan(rg * q.sh.W, static_cast<int>(M), R, R, KB, true, true, rg).total <= 160 * 1024 &&
+    if (q.sh.W > 0 && lds_plan(rg * q.sh.W, static_cast<int>(M), R, R, KB, true, true, rg).total <= 160 * 1024 &&
         (R == 0 || gather_ok(M, R, q.SP, kGatherTripsRG)))
       p = q;
   }
@@ -1001,7 +1004,7 @@ size_t gemv_workspace(int64_t M, int64_t K, int64_t N, int r) {
 
 bool gemv_supported(const WeightView &w, int64_t M, int r) {
   const int64_t N = w.n_rows, K = w.n_cols;
-  return gemv_shape_ok(M, N) && M <= GMAXM && r >= 0 && r <= kMaxRank && (N + 15) / 16 <= kMaxFlagWGs &&
+  return gemv_shape_ok(M, N, K) && M <= GMAXM && r >= 0 && r <= kMaxRank && (N + 15) / 16 <= kMaxFlagWGs &&
          uint64_t(N) * K / 2 <= 0xFFFFFFF0ull && uint64_t(M) * K * 2 <= 0xFFFFFFF0ull &&
          uint64_t(r) * K * 2 <= 0xFFFFFFF0ull && uint64_t(N) * (K / 64) <= 0xFFFFFFF0ull &&
          uint64_t(N) * r * 2 + 4 <= 0xFFFFFFF0ull;

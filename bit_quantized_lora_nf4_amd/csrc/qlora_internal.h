@@ -198,9 +198,12 @@ hipError_t launch_gemm_fwd(const WeightView &w, const uint16_t *X, int64_t M, co
 // one linear, R = r).  `ws` holds gemv_workspace bytes: a kGemvSyncBytes header of
 // counters and flags that must be zero when the call starts (every call leaves it
 // zero), then copies of U_s and the partial sums of the down-projection.
-// The small-M forward runs for M <= 16 and up to 4096 tiles of 16 output rows (one flag
-// word per workgroup in the header); other shapes take the fused GEMM.
-inline bool gemv_shape_ok(int64_t M, int64_t N) { return M >= 1 && M <= 16 && (N + 15) / 16 <= 4096; }
+// The small-M forward runs for M <= 16, up to 4096 tiles of 16 output rows (one flag word per
+// workgroup in the header) and rows of up to 15 x 256 blocks (256 for each of a workgroup's weight
+// waves); other shapes take the fused GEMM.
+inline bool gemv_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= 16 && (N + 15) / 16 <= 4096 && K <= 15 * 256 * 64;
+}
 size_t gemv_workspace(int64_t M, int64_t K, int64_t N, int r);
 bool gemv_supported(const WeightView &w, int64_t M, int r);
 hipError_t launch_gemv(const WeightView &w, const uint16_t *X, int64_t M, const uint16_t *A, int R,

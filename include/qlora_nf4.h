@@ -203,9 +203,8 @@ int qlora_dequantize(const qlora_nf4_weight *w, void *out, int out_dtype, void *
  * X bf16 [M, K]; A bf16 [r, K]; B bf16 [N, r]; Y bf16 [M, N].
  * U_saved (nullable) receives U_s for the backward.  The decode of W' happens inside
  * the GEMM; no bf16 copy of the weight is written.  The call needs
- * qlora_workspace_bytes(0, M, K, N, r) bytes of workspace: for M <= 16 and N <= 65536
- * (the small-M path, one launch)
- * the counter header, copies of U_s and the partial sums of the down-projection
+ * qlora_workspace_bytes(0, M, K, N, r) bytes of workspace: for M <= 16, N <= 65536 and
+ * K <= 245760 (the small-M path, one launch) the counter header, copies of U_s and the partial sums of the down-projection
  * (the header alone when r = 0); otherwise the header, the fp32
  * partial sums of the down-projection plus U_s when U_saved is NULL, and none when
  * r = 0.  The kernels use 32-bit buffer offsets: QLORA_ERR_SHAPE, before anything is

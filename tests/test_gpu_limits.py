@@ -102,3 +102,21 @@ def test_more_slices_than_workgroups_at_once(q):  # noqa: F811
     f = gc.host_f32_from_bf16
     want, e = dc.down(f(X), f(A), ALPHA, r, np.ones((M, K)), 1.0)
     dc.check("U", dc.bits(U), want, e)
+
+
+@pytest.mark.parametrize("N,K,r", [(32768, 25600, 8), (28672, 25600, 0), (28672, 40960, 0), (16384, 34816, 8)])
+@pytest.mark.parametrize("M", [1, 4])
+def test_rows_of_many_groups_of_constants(q, N, K, r, M):  # noqa: F811
+    """Rows long enough that a wave's part of them touches three groups of 256 block constants.
+    One element of X a token, so that each output is one weight (and the adapter's zero)."""
+    import torch
+    print(f"small M: {M} x {K} -> {N}, rank {r}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    qw = _random_weight(q, N, K, gen)
+    cols = [int(K // 64 * f) * 64 + 7 for f in (0.3, 0.1, 0.6, 0.9)[:M]]
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    X[torch.arange(M, device="cuda"), torch.tensor(cols, device="cuda")] = 1.0
+    A = torch.zeros(r, K, dtype=torch.bfloat16, device="cuda") if r else None
+    B = torch.ones(N, r, dtype=torch.bfloat16, device="cuda") if r else None
+    Y, _ = q.linear_fwd(qw, X, A, B, ALPHA)
+    assert torch.equal(Y, q.dequantize(qw)[:, cols].t())
