@@ -22,6 +22,9 @@ Gated feed-forward projections (``qw``: gate rows, then up rows; A [2 r, K], B [
 
     H, Y, U = gated_fwd(qw, X, A, B, alpha)            # H = silu(gate) * up in one kernel
     dX, dA, dB = gated_bwd(qw, dH, Y, X, A, B, alpha, U)
+
+Calls run on the current stream.  Forward calls of up to 16 tokens must not run at the same
+time on several streams of one GPU (see Workspaces in the C header); other calls may.
 """
 
 from contextlib import nullcontext
