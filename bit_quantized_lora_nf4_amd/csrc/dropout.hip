@@ -65,7 +65,7 @@ __global__ __launch_bounds__(NT) void dropout_kernel(const void *X, int64_t n, D
 // Row copies with zero padding (CopyJob): a row of the grid per job, a thread per 8 columns
 // (16 bytes) of the destination.  A side whose rows are 16-byte aligned is accessed whole,
 // the other one element by element, all in flight together.  The jobs are adapter operands
-// of unaligned rank (a few MB: the launch is what they take, COPYUS us for A [24, 1280] and B
+// of unaligned rank (a few MB: the launch is what they take, 3.4 us for A [24, 1280] and B
 // [2002, 12]) or a gradient of odd width.
 struct CopyJobs {
   CopyJob j[kMaxCopyJobs];

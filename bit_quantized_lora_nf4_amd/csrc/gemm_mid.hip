@@ -16,15 +16,15 @@
 //     constants of four steps (a row's 128-byte line) together, a group ahead;
 //   - gated: the 32 rows of a wave are 16 gate rows and the same 16 up rows, which the
 //     accumulator layout puts in one lane (elements e and e + 8 of a block);
-//   - the LoRA term runs over 64 stacked ranks at a time staged like an X tile; gated, a
-//     row's operand is zero in the other projection's ranks;
+//   - the LoRA term runs over 64 ranks at a time staged like an X tile; gated, the two
+//     projections' ranks are staged side by side and summed apart;
 //   - SPLIT: the contraction is divided over several workgroups that write their fp32
 //     accumulators, and gemm_mid_join adds them in a fixed order and does the epilogue.
 // Bound by the decode's vector instructions (at 16 tokens they issue in 65 % of the cycles, and
 // two fifths of them are permutes, which take two slots).
-// Measured, whole calls: 16 x 8192 -> 2 x 22016 of rank 64 82 us (2.38 TB/s; the 256 x 256
-// tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 183 us (201), 333 x 1280 ->
-// 2 x 1001 43 us (82).
+// Measured, whole calls: 16 x 8192 -> 2 x 22016 of rank 64 83 us (2.35 TB/s; the 256 x 256
+// tiles and the small-M kernel take 150), 777 x 4096 -> 2 x 11008 184 us (201), 333 x 1280 ->
+// 2 x 1001 of rank 12, copies of its operands included, 28 us (82).
 
 #include <type_traits>
 
