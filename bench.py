@@ -621,7 +621,8 @@ def cpu_baseline(synth, sample_m=4096, min_seconds=10.0, max_passes=20):
                       "(quantization untimed)"}
 
 
-GEMM_SOURCES = ("bit_quantized_lora_nf4_amd/csrc/gemm.hip", "bit_quantized_lora_nf4_amd/csrc/device_common.h")
+GEMM_SOURCES = ("bit_quantized_lora_nf4_amd/csrc/gemm.hip", "bit_quantized_lora_nf4_amd/csrc/gemm_tile.h",
+                "bit_quantized_lora_nf4_amd/csrc/device_common.h")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm_nf4_workload2_traffic.md")
 
 

@@ -303,7 +303,8 @@ __device__ __forceinline__ u32x4_t drop_mask(u32x4_t w, uint32_t thr) {
 // act(x) = x s and act'(x) = s + x s (1 - s) dz, s = 1 / (1 + exp(-z)):
 //   kActSilu      z = x
 //   kActGeluTanh  z = 2 sqrt(2 / pi) (x + 0.044715 x^3)  (0.5 (1 + tanh(z / 2)) = s)
-// The exponential overflows to infinity for z below -88, where s is 0 as it should be.
+// For z below -88 the exponential overflows to infinity and s, which would be less than the
+// smallest normal number, becomes 0.
 // The hardware exponential and reciprocal are good to a few 2^-24 (times |z| for the
 // exponent's product), far below the bf16 rounding of the results.
 constexpr float kGelu2K = 1.5957691216057308f, kGeluC = 0.044715f;
