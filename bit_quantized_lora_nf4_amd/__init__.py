@@ -120,6 +120,17 @@ class Dropout:
         return _lib.qlora_drop(self.p, self.seed, self.offset, _ptr(self.counter))
 
 
+def _drop(dropout, used, device):
+    """The descriptor of a call's ``dropout``, checked also where it is not used (no adapter);
+    None: nothing is dropped."""
+    if dropout is None:
+        return None
+    if not isinstance(dropout, Dropout):
+        raise TypeError(f"dropout must be a Dropout or None, got {type(dropout).__name__}")
+    d = dropout.descriptor(device)
+    return d if used else None
+
+
 def _stream(t):
     """Handle of the current stream of t's device (torch's own lookup; a Stream object takes
     4 us more to make, a third of a small call's time on the host)."""
@@ -283,7 +294,7 @@ def _scratch(nbytes, device):
 def linear_fwd(qw, X, A=None, B=None, alpha=16.0, save_u=True, Y=None, U=None, ws=None, dropout=None):
     """Y = bf16(X W'^T + U_s B^T) with U_s = bf16((alpha/r) X A^T).  Returns (Y, U_s or None).
     With ``dropout`` the adapter reads the dropped X (see Dropout)."""
-    if dropout is not None and A is not None:
+    if dropout is not None:
         return linear_fwd_fused(qw, 1, X, A, B, alpha, save_u, Y, U, ws, dropout)
     torch = _torch()
     chk = _Args(qw.codes.device)
@@ -362,7 +373,7 @@ def _bwd(qw, parts, dY, X, A, B, alpha, U, need_dx, dX, dA, dB, ws, dropout=None
         chk.need(U, torch.bfloat16, "U", (M, R))
     if need_dx and dX is not None:
         chk.need(dX, torch.bfloat16, "dX", (M, K))
-    drop = None if dropout is None or not R else dropout.descriptor(dY.device)
+    drop = _drop(dropout, R, dY.device)
     need = qlora_workspace_bytes_fused if drop is None else qlora_workspace_bytes_dropout
     nbytes = need(1, M, K, N, r, parts) if R else 0
     if R:
@@ -495,7 +506,7 @@ def linear_fwd_fused(qw, n_parts, X, A=None, B=None, alpha=16.0, save_u=True, Y=
         chk.need(Y, torch.bfloat16, "Y", (M, N))
     if r and save_u and U is not None:
         chk.need(U, torch.bfloat16, "U", (M, R))
-    drop = None if dropout is None or not R else dropout.descriptor(X.device)
+    drop = _drop(dropout, R, X.device)
     need = qlora_workspace_bytes_fused if drop is None else qlora_workspace_bytes_dropout
     nbytes = need(0, M, K, N, r, n_parts)
     chk.workspace(ws, nbytes)
@@ -534,6 +545,9 @@ def dropout(X, drop, out=None):
     torch = _torch()
     if not isinstance(X, torch.Tensor) or X.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("X must be a float32 or bfloat16 tensor")
+    if drop is None:
+        raise TypeError("drop must be a Dropout")
+    d = _drop(drop, True, X.device)
     _need(X, X.dtype, "X")
     if out is None:
         out = torch.empty_like(X)
@@ -542,7 +556,7 @@ def dropout(X, drop, out=None):
         return out
     with _guard(X.device):
         st = qlora_dropout(X.data_ptr(), QLORA_BF16 if X.dtype == torch.bfloat16 else QLORA_F32, X.numel(),
-                           drop.descriptor(X.device), out.data_ptr(), _stream(X))
+                           d, out.data_ptr(), _stream(X))
     _lib.check(st, "qlora_dropout")
     return out
 
@@ -587,7 +601,7 @@ def gated_fwd(qw, X, A=None, B=None, alpha=16.0, act="silu", save=True, H=None, 
         chk.need(Y, bf, "Y", (M, 2 * P))
     if save and r and U is not None:
         chk.need(U, bf, "U", (M, 2 * r))
-    drop = None if dropout is None or not r else dropout.descriptor(X.device)
+    drop = _drop(dropout, r, X.device)
     nbytes = qlora_workspace_bytes_gated(0, M, K, P, r)
     chk.workspace(ws, nbytes)
     chk.devices()
@@ -636,7 +650,7 @@ def gated_bwd(qw, dH, Y, X=None, A=None, B=None, alpha=16.0, U=None, act="silu",
         chk.need(dA, bf, "dA", (2 * r, K))
     if r and dB is not None:
         chk.need(dB, bf, "dB", (2 * P, r))
-    drop = None if dropout is None or not r else dropout.descriptor(dH.device)
+    drop = _drop(dropout, r, dH.device)
     nbytes = qlora_workspace_bytes_gated(1, M, K, P, r)
     chk.workspace(ws, nbytes)
     chk.devices()
