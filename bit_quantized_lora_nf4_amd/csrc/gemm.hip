@@ -427,8 +427,8 @@ constexpr int NBUF = 3;
 // neither projection is read back; H, and G and L where they are kept, leave through LDS in
 // whole rows.  Bound like the plain forward by the matrix units at the clock that the card's
 // power leaves them: 4096 x 4096 -> 2 x 11008 with rank 64, dropout and [G | L] kept, whole
-// call: 704 us, 1073 TFLOP/s (a bf16 library product of that size: 1239); 2048 x 8192 -> 2 x
-// 22016: 1330 us, 1121.
+// call: 695 us, 1086 TFLOP/s (a bf16 library product of that size: 1186); 2048 x 8192 -> 2 x
+// 22016: 1314 us, 1137 (1356).
 template <int CT, bool GATED>
 __device__ __forceinline__ void gemm_fwd_body(GemmParams p, GatedOut o) {
   __shared__ __attribute__((aligned(16))) char sX[(NBUF + (GATED ? 1 : 0)) * TILE_BYTES];
