@@ -526,8 +526,9 @@ int drop_down(const uint16_t *X, int64_t M, int64_t K, int64_t N, const uint16_t
   }
   if (!U8) return QLORA_OK;
   float *P = reinterpret_cast<float *>(ws + part);
-  return launched(d.thr ? qlora::launch_lora_down_drop(X, M, K, *A8, R8, scale, U8, P, d, st)
-                        : qlora::launch_lora_down(X, M, K, K, *A8, K, R8, scale, U8, R8, P, st),
+  const qlora::RankPad rank{round8(r), r};
+  return launched(d.thr ? qlora::launch_lora_down_drop(X, M, K, *A8, R8, scale, U8, P, d, st, rank)
+                        : qlora::launch_lora_down(X, M, K, K, *A8, K, R8, scale, U8, R8, P, st, rank),
                   "lora_down(U)");
 }
 
@@ -627,7 +628,7 @@ int bwd_blocks(const qlora_nf4_weight *w, int parts, const uint16_t *dY, int64_t
     }
     // V, dB and A^T (for the dX GEMM's rank steps) of all parts
     s = launched(qlora::launch_vdb_parts(parts, dY, M, Np, ldp, ldy, B8, U, r8, scale, V, L.lo(), dB8, part, part2,
-                                         dX ? A8 : nullptr, K, dX ? At : nullptr, st),
+                                         dX ? A8 : nullptr, K, dX ? At : nullptr, r, st),
                  "lora(V, dB)");
     if (s == QLORA_OK)
       s = launched(qlora::launch_reduce_pair(X, M, K, V, L.lo(), R8, part, dA8, d, st, dX ? &fin : nullptr), "reduce(dA)");

@@ -619,17 +619,26 @@ __global__ __launch_bounds__(NT) void vdb_parts_kernel(DownArgs d, ReduceArgs q,
 struct FinalizeJobs {
   FinalizeJob j[2 * kMaxVdbParts];
   int n;
+  int live;  // V's columns from `live` on pad the rank: zeros
   int64_t lo;
 };
-__device__ __forceinline__ void finalize_v(const FinalizeJob &j, int64_t i, int64_t lo) {
-  const f32x4_t v = split_sum(j.P, j.splits, j.count, i) * j.scale;
+// Four values of a row whose column is col: those from column `live` on become zero.  (The
+// sums of a padded rank are zero times what was multiplied, so NaN where that was infinite.)
+__device__ __forceinline__ f32x4_t live_ranks(f32x4_t v, int col, int live) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = col + e < live ? v[e] : 0.0f;
+  return v;
+}
+__device__ __forceinline__ void finalize_v(const FinalizeJob &j, int64_t i, int64_t lo, int live) {
+  f32x4_t v = split_sum(j.P, j.splits, j.count, i) * j.scale;
+  const int64_t e = 4 * i, row = e / j.cols, col = e % j.cols;
+  if (live < j.cols) v = live_ranks(v, static_cast<int>(col), live);
   const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   // exact differences: hi is within half a step of v; none where hi is infinite (v - hi is an
   // infinity of the other sign, or NaN, and dA's sum with it NaN)
   auto left = [](float x, float h) { return __builtin_fabsf(h) == __builtin_inff() ? 0.0f : x - h; };
   const u32x2_t rest = {pack_bf16x2(left(v[0], bf16_lo(hi[0])), left(v[1], bf16_hi(hi[0]))),
                         pack_bf16x2(left(v[2], bf16_lo(hi[1])), left(v[3], bf16_hi(hi[1])))};
-  const int64_t e = 4 * i, row = e / j.cols, col = e % j.cols;
   uint16_t *const out = j.OUT + row * j.ldout + col;
   *reinterpret_cast<u32x2_t *>(out) = hi;
   *reinterpret_cast<u32x2_t *>(out + lo) = rest;
@@ -641,7 +650,7 @@ __global__ __launch_bounds__(NT) void finalize_parts_kernel(FinalizeJobs jobs, i
     int k = 0;
     while (k + 1 < jobs.n && at >= jobs.j[k].count / 4) at -= jobs.j[k++].count / 4;
     if (k % 2 == 0)
-      finalize_v(jobs.j[k], at, jobs.lo);
+      finalize_v(jobs.j[k], at, jobs.lo, jobs.live);
     else
       finalize_one(jobs.j[k], at);
   }
@@ -660,6 +669,18 @@ __global__ __launch_bounds__(NT) void finalize_kernel(const float *__restrict__ 
     u32x2_t o = {pack_bf16x2(s[0] * scale, s[1] * scale), pack_bf16x2(s[2] * scale, s[3] * scale)};
     const int64_t e = 4 * i, row = e / cols, col = e % cols;
     *reinterpret_cast<u32x2_t *>(OUT + row * ldout + col) = o;
+  }
+}
+
+// The same for U of padded ranks: rows of parts of `width` columns, of which `live` are kept.
+__global__ __launch_bounds__(NT) void finalize_ranks_kernel(FinalizeJob j, int width, int live) {
+  const int64_t n4 = j.count / 4;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x; i < n4;
+       i += static_cast<int64_t>(gridDim.x) * NT) {
+    const int64_t e = 4 * i, row = e / j.cols, col = e % j.cols;
+    const f32x4_t s =
+        live_ranks(split_sum(j.P, j.splits, j.count, i) * j.scale, static_cast<int>(col) % width, live);
+    *reinterpret_cast<u32x2_t *>(j.OUT + row * j.ldout + col) = u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
   }
 }
 
@@ -842,10 +863,15 @@ bool reduce_fast(int64_t M, int64_t No, int64_t ldin, int64_t lds, int r) {
 }
 
 hipError_t launch_finalize(const float *P, int splits, int64_t count, int64_t cols, int64_t ldout,
-                           float scale, uint16_t *OUT, hipStream_t stream) {
+                           float scale, uint16_t *OUT, hipStream_t stream, RankPad pad = {}) {
   int64_t blocks = (count / 4 + NT - 1) / NT;
   if (blocks > 4096) blocks = 4096;
   if (blocks < 1) blocks = 1;
+  if (pad.live < pad.width) {
+    hipLaunchKernelGGL(finalize_ranks_kernel, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream,
+                       FinalizeJob{P, splits, count, cols, ldout, scale, OUT}, pad.width, pad.live);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(finalize_kernel, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream, P,
                      splits, count, cols, ldout, scale, OUT);
   return hipGetLastError();
@@ -862,7 +888,7 @@ size_t lora_down_workspace(int64_t M, int64_t Kc, int r) {
 
 hipError_t launch_lora_down(const uint16_t *IN, int64_t M, int64_t Kc, int64_t ldin, const uint16_t *WT,
                             int64_t ldwt, int r, float scale, uint16_t *OUT, int64_t ldout, float *ws,
-                            hipStream_t stream) {
+                            hipStream_t stream, RankPad pad) {
   const int rt = (r + 31) / 32;
   if (rt < 1 || rt > 8) return hipErrorInvalidValue;
   if (down_fast(M, Kc, ldin, ldwt, r, ldout)) {
@@ -881,8 +907,9 @@ hipError_t launch_lora_down(const uint16_t *IN, int64_t M, int64_t Kc, int64_t l
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_finalize(ws, sp.ksplit, M * r, r, ldout, scale, OUT, stream);
+    return launch_finalize(ws, sp.ksplit, M * r, r, ldout, scale, OUT, stream, pad);
   }
+  if (pad.live < pad.width) return hipErrorInvalidValue;
   dim3 grid(static_cast<unsigned>((M + 127) / 128)), block(NT);
   switch (rt) {
 #define QLORA_CASE(T)                                                                         \
@@ -902,7 +929,7 @@ bool drop_shape_ok(int64_t M, int64_t Kc, int r) {
 }
 
 hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *WT, int r, float scale,
-                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream) {
+                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream, RankPad pad) {
   if (!drop_shape_ok(M, Kc, r) || d.thr == 0) return hipErrorInvalidValue;
   const DownSplit sp = down_split(M, Kc);
   dim3 grid(static_cast<unsigned>((M + 63) / 64), static_cast<unsigned>(sp.ksplit)), block(NT);
@@ -918,7 +945,7 @@ hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, cons
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_finalize(ws, sp.ksplit, M * r, r, r, scale, OUT, stream);
+  return launch_finalize(ws, sp.ksplit, M * r, r, r, scale, OUT, stream, pad);
 }
 
 // Row splits of the paired reduction: as many workgroups as are on the card at once (two a
@@ -1101,7 +1128,7 @@ hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, co
 hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
                             const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, int64_t lo,
                             uint16_t *dB, float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
-                            hipStream_t stream) {
+                            int live, hipStream_t stream) {
   const int rt = (r + 31) / 32, R = parts * r;
   if (rt < 1 || rt > 8 || parts < 1 || parts > kMaxVdbParts || !vdb_fast(M, Np, ldy, R, r, true))
     return hipErrorInvalidValue;
@@ -1131,6 +1158,7 @@ hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np
   if (e != hipSuccess) return e;
   FinalizeJobs jobs;
   jobs.n = 2 * parts;
+  jobs.live = live;
   jobs.lo = lo;
   int64_t total = 0;
   for (int p = 0; p < parts; ++p) {

@@ -92,13 +92,18 @@ hipError_t launch_dequantize(const WeightView &w, void *out, bool out_bf16, hipS
 // have pitch ldin, WT rows pitch ldwt (column slices of wider matrices are allowed).
 // `ws` holds lora_down_workspace(M, Kc, r) bytes of fp32 partial sums.
 size_t lora_down_workspace(int64_t M, int64_t Kc, int r);
+// A rank padded with zeros: parts of `width` columns, of which the first `live` are the rank's
+// own and the others of OUT are set to zero (live = width: none padded).
+struct RankPad {
+  int width = 0, live = 0;
+};
 hipError_t launch_lora_down(const uint16_t *IN, int64_t M, int64_t Kc, int64_t ldin, const uint16_t *WT,
                             int64_t ldwt, int r, float scale, uint16_t *OUT, int64_t ldout, float *ws,
-                            hipStream_t stream);
+                            hipStream_t stream, RankPad pad = {});
 // The same with the dropout mask on IN, a dense [M, Kc] tensor: OUT = bf16(scale (m IN) WT^T).
 // Needs r % 8 == 0 and the fast-path shapes (drop_shape_ok).
 hipError_t launch_lora_down_drop(const uint16_t *IN, int64_t M, int64_t Kc, const uint16_t *WT, int r, float scale,
-                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream);
+                                 uint16_t *OUT, float *ws, const Dropout &d, hipStream_t stream, RankPad pad = {});
 bool drop_shape_ok(int64_t M, int64_t Kc, int r);
 // OUT_q[C_q, R_q] = IN_q[R_q, C_q]^T for two bf16 matrices (dense row-major) in one
 // launch; IN1 may be NULL (one transpose).
@@ -162,11 +167,12 @@ hipError_t launch_vdb(const uint16_t *dY, int64_t M, int64_t Np, int64_t ldy, co
 // columns are [q ldp, q ldp + Np) of rows of pitch ldy (zeros up to the next multiple of 8),
 // B [parts Np, r], U and V [M, parts r], dB [parts Np, r]; the partial regions are `parts`
 // times vdb_workspace_v / vdb_workspace_db; At[KA, parts r] = A^T if both are given.  What
-// V's rounding took off goes, rounded in its turn, to the matrix `lo` elements behind V.
+// V's rounding took off goes, rounded in its turn, to the matrix `lo` elements behind V.  V's
+// columns from `live` on pad the rank and are set to zero (live = r: none).
 hipError_t launch_vdb_parts(int parts, const uint16_t *dY, int64_t M, int64_t Np, int64_t ldp, int64_t ldy,
                             const uint16_t *B, const uint16_t *U, int r, float scale, uint16_t *V, int64_t lo,
                             uint16_t *dB, float *ws_v, float *ws_db, const uint16_t *A, int64_t KA, uint16_t *At,
-                            hipStream_t stream);
+                            int live, hipStream_t stream);
 
 // AdamW step (fp32 parameter and moments, bf16 gradient, optional bf16 parameter copy).
 struct AdamConsts {

@@ -150,3 +150,41 @@ def test_infinite_v_gives_infinite_da(q, M):
     want[r:] = sign[:, None] * np.inf * dc.bits(X)[i][None, :]
     same_kind(dc.bits(dA), want)
     assert np.all(dc.bits(dA)[:r] == 0.0)
+
+
+def ieee(a, b):
+    """a b with every product and sum of the contraction carried out (a library's may not)."""
+    out = a @ b
+    for i in np.flatnonzero(~np.isfinite(a).all(1)):
+        out[i] = (a[i][:, None] * b).sum(0)
+    return out
+
+
+@pytest.mark.parametrize("r", [1, 4, 8, 12, 20])
+@pytest.mark.parametrize("M,K,N", [(7, 256, 64), (40, 192, 130), (300, 64, 4100), (700, 320, 72)])
+def test_infinities_with_ranks_of_any_size(q, M, K, N, r):
+    """An infinity in X (kept) and one in dY: U, Y, V's part of dX, dA and dB are infinite, NaN and
+    finite where the definition is, also where the rank is padded to a multiple of 8."""
+    h = dc.linear_inputs(M, K, N, r, 1, seed=9)
+    dev = {k: gc.dev_bf16(v) for k, v in h.items()}
+    qw = q.quantize(dev["W"])
+    Wd = dc.weight64(qw)
+    d = q.Dropout(0.5, seed=24)
+    m, c = dc.mask(M, K, 0.5, 24, 0)
+    A, B = dc.f64(h, "A", "B")
+    X, dY = dev["X"].clone(), dev["dY"].clone()
+    i, j = M // 2, M - 1
+    X[i, int(np.flatnonzero(m[i])[-1])] = float("inf")
+    dY[j, N // 3] = float("-inf")
+    Xf, dYf = dc.bits(X), dc.bits(dY)
+    with np.errstate(invalid="ignore"):
+        Y, U = q.linear_fwd(qw, X, dev["A"], dev["B"], ALPHA, dropout=d)
+        Uf = dc.bits(U)
+        same_kind(Uf, ieee(np.where(m != 0, Xf, 0.0), A.T))
+        same_kind(dc.bits(Y), ieee(Xf, Wd.T) + ieee(Uf, B.T))
+        U = dev["X"][:, :r].contiguous()  # any finite U
+        dX, dA, dB = q.linear_bwd(qw, dY, dev["X"], dev["A"], dev["B"], ALPHA, U, dropout=d)
+        V = ieee(dYf, B)
+        same_kind(dc.bits(dX), ieee(dYf, Wd) + np.where(m != 0, ieee(V, A), 0.0))
+        same_kind(dc.bits(dA), ieee(V.T, np.where(m != 0, dc.bits(dev["X"]), 0.0)))
+        same_kind(dc.bits(dB), ieee(dYf.T, dc.bits(U)))
