@@ -23,6 +23,14 @@ Gated feed-forward projections (``qw``: gate rows, then up rows; A [2 r, K], B [
     H, Y, U = gated_fwd(qw, X, A, B, alpha)            # H = silu(gate) * up in one kernel
     dX, dA, dB = gated_bwd(qw, dH, Y, X, A, B, alpha, U)
 
+Serving a merged weight in 4-bit integers with group scales, and what follows the query, key
+and value projections (also in training; the backward's dY goes to ``linear_bwd_fused``):
+
+    gw = group_quantize(lora_merge(qw, A, B, alpha), 128)
+    Y = group_linear_fwd(gw, X)                        # few tokens: a decode step's batch
+    Q, K = qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight, k_weight)
+    dY, dqw, dkw = qk_norm_rope_bwd(dQ, dK, dV, positions, inv_freq, Y, q_weight, k_weight)
+
 Calls run on the current stream.  Forward calls of up to 16 tokens must not run at the same
 time on several streams of one GPU (see Workspaces in the C header); other calls may.
 """
@@ -40,7 +48,8 @@ from ._lib import (QLORA_BF16, QLORA_CONST_DQ_FP8, QLORA_CONST_DQ_INT8, QLORA_CO
                    qlora_quantize_nf4, qlora_workspace_bytes, qlora_workspace_bytes_fused,
                    qlora_dropout, qlora_linear_bwd_dropout, qlora_linear_fwd_dropout,
                    qlora_workspace_bytes_dropout, QLORA_ACT_GELU_TANH, QLORA_ACT_SILU, qlora_gated_bwd,
-                   qlora_gated_fwd, qlora_workspace_bytes_gated)
+                   qlora_gated_fwd, qlora_workspace_bytes_gated, qlora_group_dequantize, qlora_group_linear_fwd,
+                   qlora_group_quantize, qlora_qk_bwd, qlora_qk_fwd, qlora_workspace_bytes_qk)
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "workspace",
            "adamw_step", "lora_merge", "lora_unmerge", "concat_rows", "linear_fwd_fused",
@@ -52,7 +61,9 @@ __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "w
            "QLORA_CONST_DQ_FP8", "QLORA_CONST_FP32", "Dropout", "dropout", "qlora_dropout",
            "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_workspace_bytes_dropout", "gated_fwd", "gated_bwd",
            "qlora_gated_fwd", "qlora_gated_bwd", "qlora_workspace_bytes_gated", "QLORA_ACT_SILU",
-           "QLORA_ACT_GELU_TANH"]
+           "QLORA_ACT_GELU_TANH", "GroupWeight", "group_quantize", "group_dequantize", "group_linear_fwd",
+           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qlora_group_quantize", "qlora_group_dequantize",
+           "qlora_group_linear_fwd", "qlora_qk_fwd", "qlora_qk_bwd", "qlora_workspace_bytes_qk"]
 
 
 _torch_module = None
@@ -672,3 +683,246 @@ def gated_bwd(qw, dH, Y, X=None, A=None, B=None, alpha=16.0, U=None, act="silu",
                              _ptr(ws), ws.numel(), _stream(dH))
     _lib.check(st, "qlora_gated_bwd")
     return (dX if need_dx else None), dA, dB
+
+
+# ---- weights with group scales -----------------------------------------------------------
+
+@dataclass
+class GroupWeight:
+    """Device arrays of a weight W[n_rows, n_cols] in 4-bit integers: each ``group``
+    consecutive elements of a row (a multiple of 32 that divides n_cols) share a scale, and
+    W[n, k] = (code - zero) * scale.  ``zeros`` None: the zero is 8 everywhere.  The arrays of
+    a checkpoint in this layout can be given as they are."""
+    codes: "object"           # uint8 [n_rows * n_cols / 2], byte i = code(2i) | code(2i+1) << 4
+    scales: "object"          # bfloat16 or float32 [n_rows, n_cols / group]
+    zeros: "object"           # uint8 [n_rows, n_cols / group] or None
+    n_rows: int
+    n_cols: int
+    group: int
+
+    @property
+    def shape(self):
+        return (self.n_rows, self.n_cols)
+
+    def descriptor(self):
+        return _lib.qlora_group_weight(self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.zeros), self.n_rows,
+                                       self.n_cols, self.group, _type_of(self.scales, "scales"))
+
+    def checked(self):
+        """The argument checks of a call with this weight (see _Args), its arrays among them."""
+        torch = _torch()
+        N, K, g = self.n_rows, self.n_cols, self.group
+        _check_groups(N, K, g)
+        chk = _Args(self.codes.device)
+        chk.need(self.codes, torch.uint8, "codes")
+        if self.codes.numel() != N * K // 2:
+            raise ValueError(f"codes has {self.codes.numel()} bytes, expected {N * K // 2}")
+        _type_of(self.scales, "scales")
+        chk.need(self.scales, self.scales.dtype, "scales", (N, K // g))
+        if self.zeros is not None:
+            chk.need(self.zeros, torch.uint8, "zeros", (N, K // g))
+        return chk
+
+
+def _check_groups(N, K, g):
+    if N < 1 or K < 1 or g < 1 or g % 32 or K % g:
+        raise ValueError(f"weight [{N}, {K}] in groups of {g}: need rows, groups a multiple of 32 and columns a multiple "
+                         "of the group")
+
+
+def _type_of(t, name):
+    """QLORA_BF16 or QLORA_F32 of a tensor or dtype."""
+    torch = _torch()
+    dtype = getattr(t, "dtype", t)
+    if dtype == torch.bfloat16:
+        return QLORA_BF16
+    if dtype == torch.float32:
+        return QLORA_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+
+
+def group_quantize(W, group=128, zeros=False, scale_dtype=None):
+    """W [n_rows, n_cols] (fp32 or bf16, on the GPU) in 4-bit integers with a scale (bf16, or
+    ``scale_dtype`` float32) for each ``group`` consecutive elements of a row: symmetric about
+    zero (codes 1 to 15 about 8), or with ``zeros`` over the group's own range."""
+    torch = _torch()
+    if not isinstance(W, torch.Tensor):
+        raise TypeError("W must be a torch tensor")
+    wt = _type_of(W, "W")
+    st = _type_of(torch.bfloat16 if scale_dtype is None else scale_dtype, "scale_dtype")
+    if W.dim() != 2:
+        raise ValueError(f"W must be 2-D, got shape {tuple(W.shape)}")
+    _meta(W, W.dtype, "W")
+    N, K = W.shape
+    _check_groups(N, K, group)
+    _on(W, "W")
+    dev = W.device
+    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty((N, K // group), dtype=torch.bfloat16 if st == QLORA_BF16 else torch.float32, device=dev)
+    z = torch.empty((N, K // group), dtype=torch.uint8, device=dev) if zeros else None
+    with _guard(dev):
+        status = qlora_group_quantize(W.data_ptr(), wt, N, K, group, st, codes.data_ptr(), scales.data_ptr(), _ptr(z),
+                                      _stream(W))
+    _lib.check(status, "qlora_group_quantize")
+    return GroupWeight(codes, scales, z, N, K, group)
+
+
+def group_dequantize(gw, dtype=None, out=None):
+    """The weight that ``gw`` stands for, [n_rows, n_cols] bf16 (default) or fp32."""
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    ot = _type_of(dtype, "dtype")
+    chk = gw.checked()
+    if out is not None:
+        chk.need(out, dtype, "out", gw.shape)
+    chk.devices()
+    dev = chk.device
+    if out is None:
+        out = torch.empty(gw.shape, dtype=dtype, device=dev)
+    with _guard(dev):
+        status = qlora_group_dequantize(gw.descriptor(), out.data_ptr(), ot, _stream(out))
+    _lib.check(status, "qlora_group_dequantize")
+    return out
+
+
+def group_linear_fwd(gw, X, Y=None):
+    """Y [M, n_rows] = bf16(X W^T) for X [M, n_cols] bf16 and a GroupWeight: made for few
+    tokens (the weight is read once for up to 64 of them, and again for every 64 more)."""
+    torch = _torch()
+    chk = gw.checked()
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError(f"X must be 2-D [M, {gw.n_cols}]")
+    M = X.shape[0]
+    chk.need(X, torch.bfloat16, "X", (M, gw.n_cols))
+    if Y is not None:
+        chk.need(Y, torch.bfloat16, "Y", (M, gw.n_rows))
+    chk.devices()
+    dev = chk.device
+    if Y is None:
+        Y = torch.empty((M, gw.n_rows), dtype=torch.bfloat16, device=dev)
+    if M == 0:
+        return Y
+    with _guard(dev):
+        status = qlora_group_linear_fwd(gw.descriptor(), X.data_ptr(), M, Y.data_ptr(), _stream(X))
+    _lib.check(status, "qlora_group_linear_fwd")
+    return Y
+
+
+# ---- norms of queries and keys with the position rotation ---------------------------------
+
+def _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight):
+    """Checks what both directions share; returns the number of rotated elements."""
+    torch = _torch()
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight must both be given or both be None")
+    chk.need(positions, torch.int64, "positions", (M,))
+    chk.need(inv_freq, torch.float32, "inv_freq")
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be 1-D, got shape {tuple(inv_freq.shape)}")
+    if q_weight is not None:
+        chk.need(q_weight, dtype, "q_weight", (d,))
+        chk.need(k_weight, dtype, "k_weight", (d,))
+    rot = 2 * inv_freq.numel()
+    if d < 4 or d > 256 or d % 4 or rot > d or rot % 4:
+        raise ValueError(f"heads of {d} elements, {rot} of them rotated: need multiples of 4, at most 256 and the head")
+    return rot
+
+
+def qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, Q=None, K=None):
+    """Queries and keys from the rows Y [M, (n_heads + 2 n_kv_heads) d] of a fused projection
+    (q heads, k heads, v heads): each head divided by its root mean square (eps inside the
+    root) and multiplied by q_weight or k_weight [d] (both None: no norm), then its first
+    2 len(inv_freq) elements turned by positions [M] (int64) times inv_freq (fp32): element i
+    with i + len(inv_freq), or ``interleaved`` 2 i with 2 i + 1.  bf16 or fp32.  Returns Q [M,
+    n_heads, d] and K [M, n_kv_heads, d]; the value heads are Y's last n_kv_heads * d columns."""
+    torch = _torch()
+    if not isinstance(Y, torch.Tensor):
+        raise TypeError("Y must be a torch tensor")
+    t = _type_of(Y, "Y")
+    if n_heads < 1 or n_kv_heads < 1:
+        raise ValueError(f"{n_heads} query and {n_kv_heads} key heads")
+    if Y.dim() != 2 or Y.shape[1] % (n_heads + 2 * n_kv_heads):
+        raise ValueError(f"Y has shape {tuple(Y.shape)}, expected [M, ({n_heads} + 2 * {n_kv_heads}) d]")
+    dtype, dev = Y.dtype, Y.device
+    chk = _Args(dev)
+    chk.need(Y, dtype, "Y")
+    M = Y.shape[0]
+    d = Y.shape[1] // (n_heads + 2 * n_kv_heads)
+    rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
+    if Q is not None:
+        chk.need(Q, dtype, "Q", (M, n_heads, d))
+    if K is not None:
+        chk.need(K, dtype, "K", (M, n_kv_heads, d))
+    chk.devices()
+    if Q is None:
+        Q = torch.empty((M, n_heads, d), dtype=dtype, device=dev)
+    if K is None:
+        K = torch.empty((M, n_kv_heads, d), dtype=dtype, device=dev)
+    if M == 0:
+        return Q, K
+    shape = _lib.qlora_qk_shape(M, n_heads, n_kv_heads, d, rot, t, 1 if interleaved else 0, eps)
+    with _guard(dev):
+        status = qlora_qk_fwd(shape, Y.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
+                              _ptr(k_weight), Q.data_ptr(), K.data_ptr(), _stream(Y))
+    _lib.check(status, "qlora_qk_fwd")
+    return Q, K
+
+
+def qk_norm_rope_bwd(dQ, dK, dV, positions, inv_freq, Y=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, dY=None, dqw=None, dkw=None, ws=None):
+    """(dY, dqw, dkw) of qk_norm_rope_fwd from the gradients dQ [M, n_heads, d] and dK [M,
+    n_kv_heads, d] and that of the value heads, dV [M, n_kv_heads, d], which dY [M, (n_heads +
+    2 n_kv_heads) d] takes over.  Y is the forward's (needed with weights, whose gradients are
+    dqw and dkw; None without)."""
+    torch = _torch()
+    if not isinstance(dQ, torch.Tensor) or not isinstance(dK, torch.Tensor):
+        raise TypeError("dQ and dK must be torch tensors")
+    t = _type_of(dQ, "dQ")
+    if dQ.dim() != 3 or dK.dim() != 3:
+        raise ValueError("dQ and dK must be 3-D [M, heads, d]")
+    dtype, dev = dQ.dtype, dQ.device
+    M, nq, d = dQ.shape
+    nk = dK.shape[1]
+    if nq < 1 or nk < 1:
+        raise ValueError(f"{nq} query and {nk} key heads")
+    chk = _Args(dev)
+    chk.need(dQ, dtype, "dQ")
+    chk.need(dK, dtype, "dK", (M, nk, d))
+    chk.need(dV, dtype, "dV", (M, nk, d))
+    rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
+    N = (nq + 2 * nk) * d
+    if dY is not None:
+        chk.need(dY, dtype, "dY", (M, N))
+    shape = _lib.qlora_qk_shape(M, nq, nk, d, rot, t, 1 if interleaved else 0, eps)
+    norm = q_weight is not None
+    nbytes = 0
+    if norm:
+        if Y is None:
+            raise ValueError("Y is required with weights")
+        chk.need(Y, dtype, "Y", (M, N))
+        for g, name in ((dqw, "dqw"), (dkw, "dkw")):
+            if g is not None:
+                chk.need(g, dtype, name, (d,))
+        nbytes = qlora_workspace_bytes_qk(shape, 1) if M else 0
+        chk.workspace(ws, nbytes)
+    else:
+        Y = dqw = dkw = ws = None
+    chk.devices()
+    if dY is None:
+        dY = torch.empty((M, N), dtype=dtype, device=dev)
+    if norm:
+        dqw = torch.empty(d, dtype=dtype, device=dev) if dqw is None else dqw
+        dkw = torch.empty(d, dtype=dtype, device=dev) if dkw is None else dkw
+        if M == 0:
+            return dY, dqw.zero_(), dkw.zero_()
+        if ws is None:
+            ws = _scratch(nbytes, dev)
+    if M == 0:
+        return dY, None, None
+    with _guard(dev):
+        status = qlora_qk_bwd(shape, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), _ptr(Y), positions.data_ptr(),
+                              inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight), dY.data_ptr(), _ptr(dqw), _ptr(dkw),
+                              _ptr(ws), 0 if ws is None else ws.numel(), _stream(dQ))
+    _lib.check(status, "qlora_qk_bwd")
+    return dY, dqw, dkw

@@ -40,8 +40,10 @@ EXPORTED = (
     "qlora_linear_bwd_fused", "qlora_nf4_concat_rows", "qlora_quantize", "qlora_codebook",
     "qlora_linear_fwd_noalloc", "qlora_workspace_bytes_dropout", "qlora_linear_fwd_dropout",
     "qlora_linear_bwd_dropout", "qlora_dropout", "qlora_workspace_bytes_gated", "qlora_gated_fwd",
-    "qlora_gated_bwd",
+    "qlora_gated_bwd", "qlora_group_quantize", "qlora_group_dequantize", "qlora_group_linear_fwd", "qlora_qk_fwd",
+    "qlora_qk_bwd", "qlora_workspace_bytes_qk",
 )
+QLORA_GROUP_MAX_COLS = 262144
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 QLORA_WORKSPACE_HEADER_BYTES = 65792  # leading workspace bytes that must be zero at first use
 
@@ -63,6 +65,18 @@ class qlora_nf4_weight(ctypes.Structure):
 class qlora_drop(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
                 ("counter", ctypes.c_void_p)]
+
+
+class qlora_group_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int64), ("n_cols", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("scale_type", ctypes.c_int32)]
+
+
+class qlora_qk_shape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("nq", ctypes.c_int32), ("nk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -140,6 +154,20 @@ def load(path=LIB_PATH):
     lib.qlora_gated_fwd.restype = I32
     lib.qlora_gated_bwd.argtypes = [W, P, P, P, I64, P, P, I32, F32, I32, D, P, P, P, P, P, SZ, P]
     lib.qlora_gated_bwd.restype = I32
+    G = ctypes.POINTER(qlora_group_weight)
+    lib.qlora_group_quantize.argtypes = [P, I32, I64, I64, I64, I32, P, P, P, P]
+    lib.qlora_group_quantize.restype = I32
+    lib.qlora_group_dequantize.argtypes = [G, P, I32, P]
+    lib.qlora_group_dequantize.restype = I32
+    lib.qlora_group_linear_fwd.argtypes = [G, P, I64, P, P]
+    lib.qlora_group_linear_fwd.restype = I32
+    S = ctypes.POINTER(qlora_qk_shape)
+    lib.qlora_qk_fwd.argtypes = [S, P, P, P, P, P, P, P, P]
+    lib.qlora_qk_fwd.restype = I32
+    lib.qlora_workspace_bytes_qk.argtypes = [S, I32]
+    lib.qlora_workspace_bytes_qk.restype = SZ
+    lib.qlora_qk_bwd.argtypes = [S, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.qlora_qk_bwd.restype = I32
     _lib = lib
     return lib
 
@@ -295,3 +323,29 @@ def qlora_gated_bwd(w, dH, Y_saved, X, M, A, B, r, alpha, act, drop, U_saved, dX
 
 def _drop(drop):
     return None if drop is None else ctypes.byref(drop)
+
+
+def qlora_group_quantize(W, w_dtype, n_rows, n_cols, group, scale_type, codes, scales, zeros, stream):
+    return load().qlora_group_quantize(W, w_dtype, n_rows, n_cols, group, scale_type, codes, scales, zeros, stream)
+
+
+def qlora_group_dequantize(w, out, out_dtype, stream):
+    return load().qlora_group_dequantize(ctypes.byref(w), out, out_dtype, stream)
+
+
+def qlora_group_linear_fwd(w, X, M, Y, stream):
+    return load().qlora_group_linear_fwd(ctypes.byref(w), X, M, Y, stream)
+
+
+def qlora_qk_fwd(shape, Y, positions, inv_freq, q_weight, k_weight, Q, K, stream):
+    return load().qlora_qk_fwd(ctypes.byref(shape), Y, positions, inv_freq, q_weight, k_weight, Q, K, stream)
+
+
+def qlora_workspace_bytes_qk(shape, norm):
+    return load().qlora_workspace_bytes_qk(ctypes.byref(shape), norm)
+
+
+def qlora_qk_bwd(shape, dQ, dK, dV, Y, positions, inv_freq, q_weight, k_weight, dY, dqw, dkw, workspace,
+                 workspace_bytes, stream):
+    return load().qlora_qk_bwd(ctypes.byref(shape), dQ, dK, dV, Y, positions, inv_freq, q_weight, k_weight, dY, dqw,
+                               dkw, workspace, workspace_bytes, stream)

@@ -31,7 +31,8 @@ FLAGS = [
 ]
 
 SOURCES = ["codebook.cpp", "api.cpp", "quantize.hip", "dequant.hip", "lora.hip", "gemm.hip", "gemm_mid.hip", "dx_mid.hip",
-           "adamw.hip", "merge.hip", "dropout.hip", "gated.hip", "gemv.hip"]
+           "adamw.hip", "merge.hip", "dropout.hip", "gated.hip", "gemv.hip", "group_quant.hip", "group_linear.hip",
+           "qk.hip"]
 
 
 def _compile(src, obj_dir, verbose):

@@ -809,6 +809,74 @@ int gated_bwd_impl(const char *who, const qlora_nf4_weight *w, const uint16_t *d
   return bwd_blocks(w, 2, dY, ldp, 2 * ldp, X, M, A, B, r, scale, d, U_saved, dX, dA, dB, ws, L, st);
 }
 
+// ---- group-scaled weights, query / key norms with rotation -----------------------------
+int check_group_shape(const char *who, int64_t n_rows, int64_t n_cols, int64_t group, int scale_type) {
+  if (n_rows < 1 || n_cols < 1 || group < 1 || group % 32 != 0 || n_cols % group != 0)
+    return fail(QLORA_ERR_SHAPE,
+                "%s: weight [%lld, %lld] in groups of %lld: need n_rows >= 1, groups a multiple of 32 and n_cols a "
+                "multiple of the group",
+                who, (long long)n_rows, (long long)n_cols, (long long)group);
+  if (n_cols > QLORA_GROUP_MAX_COLS || n_rows > kMaxDim / n_cols)
+    return fail(QLORA_ERR_SHAPE, "%s: weight [%lld, %lld] too large", who, (long long)n_rows, (long long)n_cols);
+  if (scale_type != QLORA_F32 && scale_type != QLORA_BF16)
+    return fail(QLORA_ERR_DTYPE, "%s: scale_type %d: expected QLORA_F32 or QLORA_BF16", who, scale_type);
+  return QLORA_OK;
+}
+
+bool aligned_as(const void *p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == QLORA_BF16 ? 1u : 3u)) == 0;
+}
+
+int check_group_weight(const char *who, const qlora_group_weight *w) {
+  if (!w) return fail(QLORA_ERR_NULL, "%s: weight descriptor is NULL", who);
+  int s = check_group_shape(who, w->n_rows, w->n_cols, w->group, w->scale_type);
+  if (s != QLORA_OK) return s;
+  if (!w->codes || !w->scales) return fail(QLORA_ERR_NULL, "%s: weight descriptor has a NULL array", who);
+  if (!aligned16(w->codes) || !aligned_as(w->scales, w->scale_type))
+    return fail(QLORA_ERR_ALIGN, "%s: codes must be 16-byte aligned and scales aligned to their type", who);
+  return QLORA_OK;
+}
+
+qlora::GroupView view(const qlora_group_weight *w) {
+  return qlora::GroupView{w->codes,  w->scales, w->zeros, w->n_rows, w->n_cols,
+                          w->group,  w->scale_type == QLORA_BF16};
+}
+
+int check_qk_shape(const char *who, const qlora_qk_shape *s, bool norm, qlora::QkShape *out) {
+  if (!s) return fail(QLORA_ERR_NULL, "%s: shape is NULL", who);
+  if (s->dtype != QLORA_F32 && s->dtype != QLORA_BF16)
+    return fail(QLORA_ERR_DTYPE, "%s: dtype %d: expected QLORA_F32 or QLORA_BF16", who, s->dtype);
+  if (s->M < 1 || s->nq < 1 || s->nk < 1 || s->d < 4 || s->d > qlora::kQkMaxDim || s->d % 4 != 0 || s->rot < 0 ||
+      s->rot > s->d || s->rot % 4 != 0)
+    return fail(QLORA_ERR_SHAPE,
+                "%s: M = %lld, heads %d and %d of %d elements, %d rotated: need M, heads >= 1, elements a multiple of "
+                "4 up to %d, rotated ones a multiple of 4 among them",
+                who, (long long)s->M, s->nq, s->nk, s->d, s->rot, qlora::kQkMaxDim);
+  constexpr int kMaxHeads = 1 << 20;
+  if (s->nq > kMaxHeads || s->nk > kMaxHeads ||
+      s->M > kMaxDim / (static_cast<int64_t>(s->d) * (static_cast<int64_t>(s->nq) + 2 * s->nk)))
+    return fail(QLORA_ERR_SHAPE, "%s: [%lld, %d + 2 * %d heads of %d] too large", who, (long long)s->M, s->nq, s->nk,
+                s->d);
+  if (s->interleaved != 0 && s->interleaved != 1)
+    return fail(QLORA_ERR_VALUE, "%s: interleaved = %d: expected 0 or 1", who, s->interleaved);
+  if (norm && !(std::isfinite(s->eps) && s->eps >= 0.0f))
+    return fail(QLORA_ERR_VALUE, "%s: eps must be finite and >= 0", who);
+  *out = qlora::QkShape{s->M, s->nq, s->nk, s->d, s->rot, norm ? s->eps : 0.0f, 0, 0, 0, 0, 0.0f};
+  return QLORA_OK;
+}
+
+int check_qk_operands(const char *who, const qlora_qk_shape *s, const int64_t *positions, const float *inv_freq,
+                      const void *q_weight, const void *k_weight) {
+  if (!positions || (s->rot > 0 && !inv_freq))
+    return fail(QLORA_ERR_NULL, "%s: positions and inv_freq are required", who);
+  if ((q_weight == nullptr) != (k_weight == nullptr))
+    return fail(QLORA_ERR_NULL, "%s: q_weight and k_weight must both be given or both be NULL", who);
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || !aligned4(inv_freq) || !aligned16(q_weight) ||
+      !aligned16(k_weight))
+    return fail(QLORA_ERR_ALIGN, "%s: positions must be 8-byte, inv_freq 4-byte, weights 16-byte aligned", who);
+  return QLORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1116,6 +1184,106 @@ int qlora_lora_unmerge(const uint16_t *W_merged, int64_t n_rows, int64_t n_cols,
   return launched(qlora::launch_lora_unmerge(W_merged, n_rows, n_cols, A, B, r, scale, out,
                                              static_cast<hipStream_t>(stream)),
                   "lora_unmerge");
+}
+
+int qlora_group_quantize(const void *W, int w_dtype, int64_t n_rows, int64_t n_cols, int64_t group, int scale_type,
+                         uint8_t *codes, void *scales, uint8_t *zeros, void *stream) {
+  int s = check_group_shape("group_quantize", n_rows, n_cols, group, scale_type);
+  if (s != QLORA_OK) return s;
+  if (w_dtype != QLORA_F32 && w_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_DTYPE, "group_quantize: w_dtype %d: expected QLORA_F32 or QLORA_BF16", w_dtype);
+  if (!W || !codes || !scales) return fail(QLORA_ERR_NULL, "group_quantize: W, codes and scales are required");
+  if (!aligned16(W) || !aligned16(codes) || !aligned_as(scales, scale_type))
+    return fail(QLORA_ERR_ALIGN, "group_quantize: W and codes must be 16-byte aligned, scales aligned to their type");
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  return launched(qlora::launch_group_quantize(W, w_dtype == QLORA_BF16, n_rows, n_cols, group,
+                                               scale_type == QLORA_BF16, codes, scales, zeros,
+                                               static_cast<hipStream_t>(stream)),
+                  "group_quantize");
+}
+
+int qlora_group_dequantize(const qlora_group_weight *w, void *out, int out_dtype, void *stream) {
+  int s = check_group_weight("group_dequantize", w);
+  if (s != QLORA_OK) return s;
+  if (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_DTYPE, "group_dequantize: out_dtype %d: expected QLORA_F32 or QLORA_BF16", out_dtype);
+  if (!out) return fail(QLORA_ERR_NULL, "group_dequantize: out is NULL");
+  if (!aligned16(out)) return fail(QLORA_ERR_ALIGN, "group_dequantize: out must be 16-byte aligned");
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  return launched(qlora::launch_group_dequantize(view(w), out, out_dtype == QLORA_BF16,
+                                                 static_cast<hipStream_t>(stream)),
+                  "group_dequantize");
+}
+
+int qlora_group_linear_fwd(const qlora_group_weight *w, const uint16_t *X, int64_t M, uint16_t *Y, void *stream) {
+  int s = check_group_weight("group_linear_fwd", w);
+  if (s != QLORA_OK) return s;
+  if (M < 1 || M > qlora::kGroupMaxTokens)
+    return fail(QLORA_ERR_SHAPE, "group_linear_fwd: M = %lld outside [1, %lld]", (long long)M,
+                (long long)qlora::kGroupMaxTokens);
+  if (w->n_rows > int64_t(1) << 31)
+    return fail(QLORA_ERR_SHAPE, "group_linear_fwd: %lld rows are more than 2^31", (long long)w->n_rows);
+  if (!X || !Y) return fail(QLORA_ERR_NULL, "group_linear_fwd: X and Y are required");
+  if (!aligned16(X) || !aligned16(Y))
+    return fail(QLORA_ERR_ALIGN, "group_linear_fwd: X and Y must be 16-byte aligned");
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  return launched(qlora::launch_group_linear(view(w), X, M, Y, static_cast<hipStream_t>(stream)), "group_linear_fwd");
+}
+
+int qlora_qk_fwd(const qlora_qk_shape *shape, const void *Y, const int64_t *positions, const float *inv_freq,
+                 const void *q_weight, const void *k_weight, void *Q, void *K, void *stream) {
+  qlora::QkShape s;
+  int e = check_qk_shape("qk_fwd", shape, q_weight != nullptr, &s);
+  if (e == QLORA_OK) e = check_qk_operands("qk_fwd", shape, positions, inv_freq, q_weight, k_weight);
+  if (e != QLORA_OK) return e;
+  if (!Y || !Q || !K) return fail(QLORA_ERR_NULL, "qk_fwd: Y, Q and K are required");
+  if (!aligned16(Y) || !aligned16(Q) || !aligned16(K))
+    return fail(QLORA_ERR_ALIGN, "qk_fwd: Y, Q and K must be 16-byte aligned");
+  e = check_device();
+  if (e != QLORA_OK) return e;
+  return launched(qlora::launch_qk_fwd(Y, s, shape->dtype == QLORA_BF16, shape->interleaved != 0, positions, inv_freq,
+                                       q_weight, k_weight, Q, K, static_cast<hipStream_t>(stream)),
+                  "qk_fwd");
+}
+
+size_t qlora_workspace_bytes_qk(const qlora_qk_shape *shape, int norm) {
+  qlora::QkShape s;
+  if (check_qk_shape("workspace_bytes_qk", shape, norm != 0, &s) != QLORA_OK || !norm) return 0;
+  return qlora::kGemvSyncBytes + qlora::qk_bwd_workspace(s, shape->dtype == QLORA_BF16, true);
+}
+
+int qlora_qk_bwd(const qlora_qk_shape *shape, const void *dQ, const void *dK, const void *dV, const void *Y,
+                 const int64_t *positions, const float *inv_freq, const void *q_weight, const void *k_weight, void *dY,
+                 void *dqw, void *dkw, void *workspace, size_t workspace_bytes, void *stream) {
+  const bool norm = q_weight != nullptr;
+  qlora::QkShape s;
+  int e = check_qk_shape("qk_bwd", shape, norm, &s);
+  if (e == QLORA_OK) e = check_qk_operands("qk_bwd", shape, positions, inv_freq, q_weight, k_weight);
+  if (e != QLORA_OK) return e;
+  if (!dQ || !dK || !dV || !dY) return fail(QLORA_ERR_NULL, "qk_bwd: dQ, dK, dV and dY are required");
+  if (norm && (!Y || !dqw || !dkw))
+    return fail(QLORA_ERR_NULL, "qk_bwd: Y, dqw and dkw are required with weights");
+  if (!aligned16(dQ) || !aligned16(dK) || !aligned16(dV) || !aligned16(dY) ||
+      (norm && (!aligned16(Y) || !aligned16(dqw) || !aligned16(dkw))))
+    return fail(QLORA_ERR_ALIGN, "qk_bwd: tensors must be 16-byte aligned");
+  float *part = nullptr;
+  if (norm) {
+    const size_t need = qlora_workspace_bytes_qk(shape, 1);
+    if (!workspace || workspace_bytes < need)
+      return fail(QLORA_ERR_WORKSPACE, "qk_bwd: workspace has %zu bytes, %zu needed", workspace ? workspace_bytes : 0,
+                  need);
+    if (!aligned16(workspace)) return fail(QLORA_ERR_ALIGN, "qk_bwd: workspace must be 16-byte aligned");
+    part = reinterpret_cast<float *>(static_cast<char *>(workspace) + qlora::kGemvSyncBytes);
+  }
+  e = check_device();
+  if (e != QLORA_OK) return e;
+  return launched(qlora::launch_qk_bwd(dQ, dK, dV, Y, s, shape->dtype == QLORA_BF16, shape->interleaved != 0,
+                                       positions, inv_freq, q_weight, k_weight, dY, dqw, dkw, part,
+                                       static_cast<hipStream_t>(stream)),
+                  "qk_bwd");
 }
 
 }  // extern "C"

@@ -1,0 +1,249 @@
+// 4-bit weights with one scale (and zero) for each group of consecutive elements of a row
+// (gfx950): quantization and its inverse.
+//
+//   without zeros  s = ST(RN(max |w| RN(1 / 7))),  z = 8
+//   with zeros     lo = min(w, 0), hi = max(w, 0), s = ST(RN(RN(hi - lo) RN(1 / 15))),
+//                  z = clamp(rint(RN(-lo RN(1 / s))), 0, 15)
+//   code = clamp(rint(RN(w RN(1 / s))) + z, 0, 15),   w' = RN((code - z) s)
+//
+// RN rounds to fp32, ST to the scales' type (bf16 or fp32); s below 2^-126 counts as 0 and
+// 1 / s as 0 then, so that a group of zeros (or of subnormal numbers) stands for zeros.  The
+// reciprocal is taken once a group, the weights are multiplied by it.  Both kernels are bound
+// by memory: 2 or 4 bytes a weight on one side, 0.5 and the scales on the other.
+
+#include "device_common.h"
+#include "qlora_internal.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct GroupStep {
+  float s, inv, z;
+};
+// Scale, its reciprocal and the zero of a group from its extremes (lo <= 0 <= hi with zeros,
+// else hi = max |w|).
+template <bool S16, bool ZP>
+__device__ __forceinline__ GroupStep group_step(float lo, float hi) {
+  constexpr float kPer7 = 1.0f / 7.0f, kPer15 = 1.0f / 15.0f;
+  float s = ZP ? (hi - lo) * kPer15 : hi * kPer7;
+  if constexpr (S16) s = bf16_to_f32(to_bf16(s));
+  if (s < 0x1p-126f) return {0.0f, 0.0f, ZP ? 0.0f : 8.0f};
+  const float inv = 1.0f / s;
+  const float z = ZP ? fminf(fmaxf(__builtin_rintf(-lo * inv), 0.0f), 15.0f) : 8.0f;
+  return {s, inv, z};
+}
+__device__ __forceinline__ uint32_t group_code(float w, const GroupStep &g) {
+  return static_cast<uint32_t>(fminf(fmaxf(__builtin_rintf(w * g.inv) + g.z, 0.0f), 15.0f));
+}
+template <bool S16, bool ZP>
+__device__ __forceinline__ void store_step(const GroupStep &g, int64_t i, void *scales, uint8_t *zeros) {
+  if constexpr (S16)
+    static_cast<uint16_t *>(scales)[i] = to_bf16(g.s);
+  else
+    static_cast<float *>(scales)[i] = g.s;
+  if constexpr (ZP) zeros[i] = static_cast<uint8_t>(g.z);
+}
+
+// V consecutive weights as fp32: eight of bf16 or four of fp32, 16 bytes.
+template <bool W16>
+struct Chunk {
+  static constexpr int V = W16 ? 8 : 4;
+  float v[V];
+};
+template <bool W16>
+__device__ __forceinline__ Chunk<W16> load_chunk(const void *W, int64_t c) {
+  Chunk<W16> x;
+  const u32x4_t u = reinterpret_cast<const u32x4_t *>(W)[c];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = u[i];
+    if constexpr (W16) {
+      x.v[2 * i] = bf16_lo(b);
+      x.v[2 * i + 1] = bf16_hi(b);
+    } else {
+      x.v[i] = __uint_as_float(b);
+    }
+  }
+  return x;
+}
+template <bool W16, bool ZP>
+__device__ __forceinline__ void extremes(const Chunk<W16> &x, float &lo, float &hi) {
+#pragma unroll
+  for (int i = 0; i < Chunk<W16>::V; ++i) {
+    if constexpr (ZP) lo = fminf(lo, x.v[i]);
+    hi = fmaxf(hi, ZP ? x.v[i] : fabsf(x.v[i]));
+  }
+}
+template <bool W16>
+__device__ __forceinline__ void store_codes(const Chunk<W16> &x, const GroupStep &g, int64_t c, void *codes) {
+  uint32_t p = 0;
+#pragma unroll
+  for (int i = 0; i < Chunk<W16>::V; ++i) p |= group_code(x.v[i], g) << (4 * i);
+  if constexpr (W16)
+    static_cast<uint32_t *>(codes)[c] = p;
+  else
+    static_cast<uint16_t *>(codes)[c] = static_cast<uint16_t>(p);
+}
+
+// Groups of a power of two of chunks, at most a wave's 64: `lanes` neighbouring lanes hold a
+// group, a thread takes U chunks a stride of the whole launch apart, all loaded before the
+// first is used.  Whole groups fall out together at the end, so no lane misses a partner.
+constexpr int kUnroll = 4;
+template <bool W16, bool S16, bool ZP>
+__global__ __launch_bounds__(kThreads) void group_quantize_kernel(const void *__restrict__ W, int64_t chunks,
+                                                                  int lanes, int shift, void *__restrict__ codes,
+                                                                  void *__restrict__ scales,
+                                                                  uint8_t *__restrict__ zeros) {
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kUnroll) * kThreads + threadIdx.x;
+  Chunk<W16> x[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t c = first + u * kThreads;
+    if (c < chunks) x[u] = load_chunk<W16>(W, c);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t c = first + u * kThreads;
+    if (c >= chunks) return;
+    float lo = 0.0f, hi = 0.0f;
+    extremes<W16, ZP>(x[u], lo, hi);
+    for (int m = 1; m < lanes; m <<= 1) {
+      hi = fmaxf(hi, __shfl_xor(hi, m, 64));
+      if constexpr (ZP) lo = fminf(lo, __shfl_xor(lo, m, 64));
+    }
+    const GroupStep g = group_step<S16, ZP>(lo, hi);
+    store_codes<W16>(x[u], g, c, codes);
+    if ((threadIdx.x & (lanes - 1)) == 0) store_step<S16, ZP>(g, c >> shift, scales, zeros);
+  }
+}
+
+// Any other group size: a wave to a group, which it reads twice (the second time from the
+// caches).
+template <bool W16, bool S16, bool ZP>
+__global__ __launch_bounds__(kThreads) void group_quantize_any_kernel(const void *__restrict__ W, int64_t groups,
+                                                                      int64_t per_group, void *__restrict__ codes,
+                                                                      void *__restrict__ scales,
+                                                                      uint8_t *__restrict__ zeros) {
+  const int lane = threadIdx.x & 63;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 64);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6); i < groups; i += step) {
+    const int64_t base = i * per_group;
+    float lo = 0.0f, hi = 0.0f;
+    for (int64_t c = lane; c < per_group; c += 64) extremes<W16, ZP>(load_chunk<W16>(W, base + c), lo, hi);
+    hi = wave_max(hi);
+    if constexpr (ZP) lo = wave_min(lo);
+    const GroupStep g = group_step<S16, ZP>(lo, hi);
+    for (int64_t c = lane; c < per_group; c += 64) store_codes<W16>(load_chunk<W16>(W, base + c), g, base + c, codes);
+    if (lane == 0) store_step<S16, ZP>(g, i, scales, zeros);
+  }
+}
+
+// A wave takes spans of kUnroll x 64 chunks of one row (V codes and 16 bytes of output a
+// lane), so the group of a chunk is a 32-bit division by the group's chunks, done by a
+// multiplication (exact for the row lengths that the caller allows).
+template <bool O16>
+__global__ __launch_bounds__(kThreads) void group_dequantize_kernel(GroupView w, uint32_t row_chunks, uint32_t spans,
+                                                                    uint32_t per_group, uint32_t magic,
+                                                                    void *__restrict__ out) {
+  constexpr int V = O16 ? 8 : 4;
+  const uint32_t lane = threadIdx.x & 63;
+  const int64_t total = w.n_rows * spans, step = static_cast<int64_t>(gridDim.x) * (kThreads / 64);
+  const uint32_t row_groups = row_chunks / per_group;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6); i < total; i += step) {
+    const int64_t row = i / spans;
+    const uint32_t c0 = static_cast<uint32_t>(i - row * spans) * (kUnroll * 64) + lane;
+    const int64_t chunk0 = row * row_chunks, group0 = row * row_groups;
+    uint32_t code[kUnroll];
+    float s[kUnroll], z[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t c = c0 + 64 * u;
+      if (c >= row_chunks) continue;
+      if constexpr (O16)
+        code[u] = reinterpret_cast<const uint32_t *>(w.codes)[chunk0 + c];
+      else
+        code[u] = reinterpret_cast<const uint16_t *>(w.codes)[chunk0 + c];
+      const int64_t g = group0 + (per_group == 1 ? c : __umulhi(c, magic));
+      s[u] = w.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t *>(w.scales)[g])
+                          : static_cast<const float *>(w.scales)[g];
+      z[u] = w.zeros ? static_cast<float>(w.zeros[g]) : 8.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t c = c0 + 64 * u;
+      if (c >= row_chunks) continue;
+      float v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = (static_cast<float>((code[u] >> (4 * e)) & 15u) - z[u]) * s[u];
+      u32x4_t o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (O16)
+          o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        else
+          o[e] = __float_as_uint(v[e]);
+      }
+      reinterpret_cast<u32x4_t *>(out)[chunk0 + c] = o;
+    }
+  }
+}
+
+template <bool W16, bool S16, bool ZP>
+hipError_t quantize_go(const void *W, int64_t n, int64_t group, void *codes, void *scales, uint8_t *zeros,
+                       hipStream_t stream) {
+  constexpr int V = Chunk<W16>::V;
+  const int64_t chunks = n / V, per_group = group / V;
+  if (per_group <= 64 && (per_group & (per_group - 1)) == 0) {
+    const int64_t blocks = (chunks + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    int shift = 0;
+    while ((int64_t(1) << shift) < per_group) ++shift;
+    hipLaunchKernelGGL((group_quantize_kernel<W16, S16, ZP>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                       stream, W, chunks, static_cast<int>(per_group), shift, codes, scales, zeros);
+  } else {
+    const int64_t groups = n / group;
+    int64_t blocks = (groups + kThreads / 64 - 1) / (kThreads / 64);
+    if (blocks > 256 * 16) blocks = 256 * 16;
+    hipLaunchKernelGGL((group_quantize_any_kernel<W16, S16, ZP>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                       0, stream, W, groups, per_group, codes, scales, zeros);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_group_quantize(const void *W, bool w_bf16, int64_t n_rows, int64_t n_cols, int64_t group,
+                                 bool scale_bf16, uint8_t *codes, void *scales, uint8_t *zeros, hipStream_t stream) {
+  const int64_t n = n_rows * n_cols;
+  switch ((w_bf16 ? 4 : 0) + (scale_bf16 ? 2 : 0) + (zeros ? 1 : 0)) {
+    case 0: return quantize_go<false, false, false>(W, n, group, codes, scales, zeros, stream);
+    case 1: return quantize_go<false, false, true>(W, n, group, codes, scales, zeros, stream);
+    case 2: return quantize_go<false, true, false>(W, n, group, codes, scales, zeros, stream);
+    case 3: return quantize_go<false, true, true>(W, n, group, codes, scales, zeros, stream);
+    case 4: return quantize_go<true, false, false>(W, n, group, codes, scales, zeros, stream);
+    case 5: return quantize_go<true, false, true>(W, n, group, codes, scales, zeros, stream);
+    case 6: return quantize_go<true, true, false>(W, n, group, codes, scales, zeros, stream);
+    default: return quantize_go<true, true, true>(W, n, group, codes, scales, zeros, stream);
+  }
+}
+
+hipError_t launch_group_dequantize(const GroupView &w, void *out, bool out_bf16, hipStream_t stream) {
+  const int V = out_bf16 ? 8 : 4;
+  const uint32_t row_chunks = static_cast<uint32_t>(w.n_cols / V), per_group = static_cast<uint32_t>(w.group / V);
+  const uint32_t spans = (row_chunks + kUnroll * 64 - 1) / (kUnroll * 64);
+  int64_t blocks = (w.n_rows * spans + kThreads / 64 - 1) / (kThreads / 64);
+  if (blocks > 256 * 16) blocks = 256 * 16;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  const uint32_t magic = group_magic(per_group);
+  if (out_bf16)
+    hipLaunchKernelGGL(group_dequantize_kernel<true>, grid, block, 0, stream, w, row_chunks, spans, per_group, magic,
+                       out);
+  else
+    hipLaunchKernelGGL(group_dequantize_kernel<false>, grid, block, 0, stream, w, row_chunks, spans, per_group, magic,
+                       out);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

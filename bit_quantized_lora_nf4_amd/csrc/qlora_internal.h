@@ -273,4 +273,49 @@ hipError_t launch_dx_mid(const WeightView &w, const uint16_t *dY, int64_t M, int
                          const uint16_t *V, const uint16_t *At, int r, uint16_t *dX, const Dropout &d, float *part,
                          hipStream_t stream, const FinalizeJob *fin);
 
+// ---- weights with one scale for each group of a row's elements -----------------------
+// Element k of row n has the value (code - zero) scale of group k / group of that row; zeros
+// NULL: 8 everywhere.  n_cols is a multiple of group, group of 32, and n_cols <= kGroupMaxCols.
+struct GroupView {
+  const uint8_t *codes;
+  const void *scales;
+  const uint8_t *zeros;
+  int64_t n_rows, n_cols, group;
+  bool scale_bf16;
+};
+// group_magic(d): u / d = the high 32 bits of u group_magic(d), for 2 <= d <= u's largest value
+// below 2^16 (the rounded-up 2^32 / d is less than d / 2^32 too large, times u less than one);
+// rows of at most kGroupMaxCols columns hold that many units of 4 columns or more.
+constexpr int64_t kGroupMaxCols = int64_t(1) << 18;
+inline uint32_t group_magic(uint32_t d) {
+  return d < 2 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d);
+}
+hipError_t launch_group_quantize(const void *W, bool w_bf16, int64_t n_rows, int64_t n_cols, int64_t group,
+                                 bool scale_bf16, uint8_t *codes, void *scales, uint8_t *zeros, hipStream_t stream);
+hipError_t launch_group_dequantize(const GroupView &w, void *out, bool out_bf16, hipStream_t stream);
+// Y[M, N] = bf16(X . W^T), fp32 sums; M <= kGroupMaxTokens.
+constexpr int64_t kGroupMaxTokens = int64_t(1) << 20;
+hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream);
+
+// ---- norms of query and key heads with the position rotation --------------------------
+constexpr int kQkMaxDim = 256;
+// M rows of nq + 2 nk heads of d elements, rot of them rotated; the other members are the
+// launchers' own (the distribution of the heads over lanes and waves).
+struct QkShape {
+  int64_t M;
+  int nq, nk, d, rot;
+  float eps;
+  int lanes, per, split;
+  int64_t row;
+  float inv_d;
+};
+// t16: bf16 tensors, else fp32; qw, kw NULL: no norm (Y is not read then by the backward).
+hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
+                         const float *inv_freq, const void *qw, const void *kw, void *Q, void *K, hipStream_t stream);
+// `part`: qk_bwd_workspace bytes of partial sums of dqw and dkw (norm only).
+size_t qk_bwd_workspace(QkShape s, bool t16, bool norm);
+hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const void *Y, QkShape s, bool t16,
+                         bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
+                         const void *kw, void *dY, void *dqw, void *dkw, float *part, hipStream_t stream);
+
 }  // namespace qlora

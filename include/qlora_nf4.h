@@ -394,6 +394,80 @@ int qlora_lora_merge(const qlora_nf4_weight *w, const uint16_t *A, const uint16_
 int qlora_lora_unmerge(const uint16_t *W_merged, int64_t n_rows, int64_t n_cols, const uint16_t *A,
                        const uint16_t *B, int r, float alpha, uint16_t *out, void *stream);
 
+/* ---- weights with group scales ----------------------------------------------------
+ * A weight W[n_rows, n_cols] in 4-bit integers with one scale (and, asymmetric, one zero) for
+ * each `group` consecutive elements of a row: the form a merged weight (qlora_lora_merge) is
+ * served in.  With G = n_cols / group groups in a row:
+ *   codes    [n_rows * n_cols / 2]  byte i = code(2i) | code(2i+1) << 4, row-major elements
+ *   scales   [n_rows, G]            bf16 (scale_type = QLORA_BF16) or fp32 (QLORA_F32)
+ *   zeros    [n_rows, G]            a byte each; NULL: 8 everywhere
+ * W[n, k] = (code - zeros[n, k / group]) * scales[n, k / group].
+ * n_cols is a multiple of group, group a multiple of 32, n_cols <= QLORA_GROUP_MAX_COLS.
+ * codes must be 16-byte aligned, scales aligned to their type. */
+enum { QLORA_GROUP_MAX_COLS = 262144 };
+typedef struct {
+  const uint8_t *codes;
+  const void *scales;
+  const uint8_t *zeros;
+  int64_t n_rows;
+  int64_t n_cols;
+  int64_t group;
+  int32_t scale_type;
+} qlora_group_weight;
+
+/* Quantization of W [n_rows, n_cols] fp32 or bf16 (16-byte aligned).  RN rounds to fp32, ST to
+ * the scales' type:
+ *   zeros NULL:  s = ST(RN(max |w| RN(1 / 7))), z = 8
+ *   else         lo = min(w, 0), hi = max(w, 0), s = ST(RN(RN(hi - lo) RN(1 / 15))),
+ *                z = clamp(rint(RN(-lo RN(1 / s))), 0, 15)
+ *   code = clamp(rint(RN(w RN(1 / s))) + z, 0, 15)   (rint: ties to even)
+ * s below 2^-126 is stored as 0 and 1 / s counts as 0 then: such a group stands for zeros. */
+int qlora_group_quantize(const void *W, int w_dtype, int64_t n_rows, int64_t n_cols, int64_t group, int scale_type,
+                         uint8_t *codes, void *scales, uint8_t *zeros, void *stream);
+
+/* out[n_rows, n_cols] = RN((code - zero) * scale) as fp32 or its bf16 rounding. */
+int qlora_group_dequantize(const qlora_group_weight *w, void *out, int out_dtype, void *stream);
+
+/* Y[M, N] = bf16(X . W^T): X bf16 [M, K], fp32 sums, the weight's values never rounded.  Made
+ * for few tokens (a decode step's batch): up to 64 tokens the weight is read once, more run in
+ * tiles of 64 tokens that each read it again.  M <= 2^20.  The sums of a group are formed as
+ * sum (16 + code) x - (16 + zero) sum x, so a value's error is that of fp32 sums of terms of up
+ * to 31 |x| s.  Infinite and NaN inputs give what the definition gives.  No workspace; calls may
+ * overlap on any streams. */
+int qlora_group_linear_fwd(const qlora_group_weight *w, const uint16_t *X, int64_t M, uint16_t *Y, void *stream);
+
+/* ---- norms of queries and keys with the position rotation --------------------------
+ * Rows Y [M, (nq + 2 nk) d] as a fused projection writes them: nq query heads, nk key heads,
+ * nk value heads of d elements.  For every query and key head x of the token at position p:
+ *   n = x / sqrt(mean x^2 + eps) * w        (w = q_weight or k_weight [d]; both NULL: n = x)
+ *   pair i < rot / 2 of its first rot elements, (a, b), turns by t = p * inv_freq[i]:
+ *     (a cos t - b sin t, b cos t + a sin t)
+ *   interleaved = 0: pair i is (i, i + rot / 2); 1: (2 i, 2 i + 1).  Elements past rot are n.
+ * dtype QLORA_BF16 or QLORA_F32 is that of all tensors but positions (int64 [M], any sign) and
+ * inv_freq (fp32 [rot / 2]).  The angle is formed and reduced in 64 bits, the rest in fp32 with
+ * one rounding at the end.  1 <= nq, nk; d a multiple of 4, at most 256; rot a multiple of 4,
+ * 0 <= rot <= d (0: the norm alone).
+ *   Q [M, nq, d], K [M, nk, d]; the value heads stay where they are. */
+typedef struct {
+  int64_t M;
+  int32_t nq, nk, d, rot;
+  int32_t dtype;
+  int32_t interleaved;
+  float eps; /* finite, >= 0; used with weights */
+} qlora_qk_shape;
+int qlora_qk_fwd(const qlora_qk_shape *shape, const void *Y, const int64_t *positions, const float *inv_freq,
+                 const void *q_weight, const void *k_weight, void *Q, void *K, void *stream);
+
+/* Backward of qlora_qk_fwd: dY [M, (nq + 2 nk) d] from dQ, dK, and dV [M, nk, d] (copied into
+ * the value heads' place), so that dY is whole for the projections' backward.  With weights
+ * also dqw, dkw [d], summed in fp32 in a fixed order, Y (the forward's rows) is required and
+ * qlora_workspace_bytes_qk bytes of workspace (its header as for every workspace); without them
+ * Y, dqw, dkw and the workspace are not used and may be NULL. */
+size_t qlora_workspace_bytes_qk(const qlora_qk_shape *shape, int norm);
+int qlora_qk_bwd(const qlora_qk_shape *shape, const void *dQ, const void *dK, const void *dV, const void *Y,
+                 const int64_t *positions, const float *inv_freq, const void *q_weight, const void *k_weight, void *dY,
+                 void *dqw, void *dkw, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,8 @@ Module map:
 * ``oracle.merge``      LoRA merge / unmerge into a bf16 copy of the base.
 * ``oracle.fusion``     horizontally fused linears (stacked weights and adapters).
 * ``oracle.variants``   FP4 levels, FP8-coded and fp32 block constants.
+* ``oracle.groups``     4-bit integers with group scales, products with them.
+* ``oracle.rotation``   norms of query / key heads and the position rotation.
 
 Every function is pinned by ``tests/test_oracle_*.py`` to facts the pages or
 mathematics fix; none is "parity unpinned".
