@@ -12,11 +12,17 @@
 // or so large that a sum overflows; a wave whose result is not finite computes its part again
 // from the integers q - z themselves (never taken on ordinary data).
 //
-// A wave owns 16 NT rows and, of K, every W-th block of 128 columns (W waves in the
-// workgroup); the waves' fp32 sums are added in wave order through LDS.  A lane (row l % 16,
-// l / 16) loads 16 bytes, 32 consecutive codes; four swaps between the lane groups turn four
-// such dwords into the fragments of four matrix instructions of 32 consecutive columns each.
-// One instruction then never spans two groups, and X is read in whole 64-byte pieces.
+// A workgroup owns 16 NT rows.  Its waves split K: each takes every W-th round of 512 columns
+// (four blocks of 128), and their fp32 sums are added in wave order through LDS.  A lane
+// (row l % 16, l / 16) loads 16 bytes of a block, 32 consecutive codes; four swaps between
+// the lane groups turn four such dwords into the fragments of four matrix instructions of 32
+// consecutive columns each, so that one instruction never spans two groups.  A row's scales
+// (and zeros) of a round are one load, lane group g holding those of block g.  X is loaded in
+// whole contiguous pieces and passed through LDS of the wave's own (no barrier), in the order of
+// the codes, the 16-byte chunk c of a token's block at slot c ^ token, so that the sixteen
+// token lanes of a fragment read fall in distinct banks.
+
+#include <type_traits>
 
 #include "device_common.h"
 #include "qlora_internal.h"
@@ -51,91 +57,212 @@ __device__ __forceinline__ u32x4_t code_order(u32x4_t x) {
   return u32x4_t{pack_lo(x[0], x[2]), pack_hi(x[0], x[2]), pack_lo(x[1], x[3]), pack_hi(x[1], x[3])};
 }
 
-// FS: columns between two uses of a scale, the largest of 32, 64 and 128 that divides the group.
-template <int MT, int NT, int FS>
-struct Tile {
-  static constexpr int kScales = 128 / FS;  // scales of a row in a block of 128 columns
-  struct Block {
-    u32x4_t codes[NT], x[MT][4];
-    float s[NT][kScales], z[NT][kScales];
+// The value of lane group q (of four) made known to all lanes.
+__device__ __forceinline__ uint32_t from_lane_group(uint32_t v, int q) {
+  const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // lane groups (0 1 0 1), (2 3 2 3)
+  const uint32_t u = h[q >> 1];
+  const auto o = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return o[q & 1];
+}
+
+// What a wave holds.  XR: tokens kept in LDS (a power of two; MT tiles of 16 of them).  FS:
+// columns between two uses of a scale, the largest of 32, 64 and 128 that divides the group.
+// VS: a block's scales of a row are one aligned load.
+template <int XR, int NT, int FS, bool S16, bool VS>
+struct Product {
+  static constexpr int MT = (XR + 15) / 16;
+  static constexpr int kScales = 128 / FS;  // scales of a row in a block
+  static constexpr int kFlush = XR >= 16 && FS == 128 ? 64 : FS;
+  static constexpr int kSRegs = S16 && VS ? kScales / 2 : kScales;
+  static constexpr int kZRegs = VS ? 1 : kScales;
+  static constexpr int kXLoads = XR < 16 ? XR : XR / 8;  // of a round (few tokens) or half a block
+  // Scales and zeros of a round, those of block g held by lane group g.
+  struct Scales {
+    uint32_t s[NT][kSRegs], z[NT][kZRegs];
+  };
+  struct Codes {
+    u32x4_t c[NT];
+  };
+  struct Xs {
+    u32x4_t x[kXLoads];
   };
 
   __amdgpu_buffer_rsrc_t codes, scales, zeros, X;
-  bool s16, zp;
+  bool zp;  // zeros are given (else 8 everywhere)
   uint32_t lane, row_bytes, row_groups, x_bytes, per, magic, n_steps;
+  char *xs;  // the wave's LDS: [4][XR][256] bytes (few tokens) or [XR][128]
   f32x4_t y[MT][NT];
 
-  __device__ __forceinline__ uint32_t group_of(uint32_t step32) const {
-    return per == 1 ? step32 : __umulhi(step32, magic);
+  __device__ __forceinline__ void init(const GroupView &w, int64_t n0, const uint16_t *x, uint32_t tokens,
+                                       uint32_t magic_) {
+    lane = threadIdx.x & 63;
+    row_bytes = static_cast<uint32_t>(w.n_cols / 2);
+    x_bytes = static_cast<uint32_t>(2 * w.n_cols);
+    per = static_cast<uint32_t>(w.group / 32);
+    magic = magic_;
+    n_steps = static_cast<uint32_t>(w.n_cols / 32);
+    row_groups = group_of(n_steps);
+    // Reads past the tile's own rows, and past the last one of the tensor, give zeros.
+    const uint32_t rows = static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT)));
+    const uint32_t n_groups = rows * row_groups;
+    constexpr uint32_t kBytes = S16 ? 2 : 4;
+    const int64_t g0 = n0 * row_groups;
+    codes = make_rsrc(w.codes + n0 * row_bytes, rows * row_bytes);
+    scales = make_rsrc(static_cast<const char *>(w.scales) + g0 * kBytes, n_groups * kBytes);
+    zp = w.zeros != nullptr;
+    zeros = make_rsrc(zp ? w.zeros + g0 : nullptr, zp ? n_groups : 0u);
+    X = make_rsrc(x, tokens * x_bytes);
   }
+  __device__ __forceinline__ uint32_t group_of(uint32_t step) const { return per == 1 ? step : __umulhi(step, magic); }
 
-  __device__ __forceinline__ void load(Block &b, uint32_t block) const {
+  __device__ __forceinline__ void load_scales(Scales &b, uint32_t round) const {
+    const uint32_t r = lane % 16, block = 4 * round + lane / 16;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      b.codes[t] = buf_load16(codes, (16 * t + lane % 16) * row_bytes + block * 64 + 16 * (lane / 16));
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t row = (16 * t + r) * row_groups;
+      if constexpr (VS) {
+        const bool in = 4 * block < n_steps;
+        const uint32_t i = row + block * kScales;
+        if constexpr (S16 && kScales == 2) {
+          b.s[t][0] = buf_load4(scales, in ? 2 * i : kOOB);
+        } else if constexpr (S16 || kScales == 2) {
+          const u32x2_t v = buf_load8(scales, in ? (S16 ? 2 : 4) * i : kOOB);
+          b.s[t][0] = v[0], b.s[t][1] = v[1];
+        } else {
+          const u32x4_t v = buf_load16(scales, in ? 4 * i : kOOB);
+          b.s[t][0] = v[0], b.s[t][1] = v[1], b.s[t][2] = v[2], b.s[t][3] = v[3];
+        }
+        b.z[t][0] = 0x08080808u;
+        if (zp)
+          b.z[t][0] = kScales == 2 ? __builtin_amdgcn_raw_buffer_load_b16(zeros, in ? i : kOOB, 0, 0)
+                                   : buf_load4(zeros, in ? i : kOOB);
+      } else {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        b.x[m][j] = buf_load16(X, (16 * m + lane % 16) * x_bytes + block * 256 + 64 * j + 16 * (lane / 16));
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int g = 0; g < kScales; ++g) {
-        const uint32_t i = (16 * t + lane % 16) * row_groups + group_of(4 * block + g * (FS / 32));
-        b.s[t][g] = s16 ? __uint_as_float(uint32_t(__builtin_amdgcn_raw_buffer_load_b16(scales, 2 * i, 0, 0)) << 16)
-                        : __uint_as_float(buf_load4(scales, 4 * i));
-        b.z[t][g] = zp ? static_cast<float>(__builtin_amdgcn_raw_buffer_load_b8(zeros, i, 0, 0)) : 8.0f;
-      }
-  }
-
-  template <bool EXACT>
-  __device__ __forceinline__ void multiply(const Block &b, uint32_t block) {
-    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    u32x4_t c[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) c[t] = transpose_lane_groups(b.codes[t]);
-#pragma unroll
-    for (int g = 0; g < kScales; ++g) {
-      f32x4_t acc[MT][NT], sum[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        sum[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-#pragma unroll
-      for (int jj = 0; jj < FS / 32; ++jj) {
-        const int j = g * (FS / 32) + jj;
-        if (4 * block + j < n_steps) {
-          u32x4_t w[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint32_t cj = c[t][j];
-            w[t] = EXACT ? plain_codes(cj, b.z[t][g]) : offset_codes(cj);
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const u32x4_t x = code_order(b.x[m][j]);
-            if constexpr (!EXACT) sum[m] = mfma16x16x32(x, ones, sum[m]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[m][t] = mfma16x16x32(x, w[t], acc[m][t]);
-          }
+        for (int k = 0; k < kScales; ++k) {
+          const uint32_t step = 4 * block + k * (FS / 32), i = row + group_of(step);
+          const bool in = step < n_steps;
+          b.s[t][k] = S16 ? __builtin_amdgcn_raw_buffer_load_b16(scales, in ? 2 * i : kOOB, 0, 0)
+                          : buf_load4(scales, in ? 4 * i : kOOB);
+          b.z[t][k] = 8u;
+          if (zp) b.z[t][k] = __builtin_amdgcn_raw_buffer_load_b8(zeros, in ? i : kOOB, 0, 0);
         }
       }
-      if (4 * block + g * (FS / 32) >= n_steps) continue;
+    }
+  }
+  // Blocks past the last read as zeros, without a memory access.
+  __device__ __forceinline__ void load_codes(Codes &b, uint32_t block) const {
+    const uint32_t o = (lane % 16) * row_bytes + block * 64 + 16 * (lane / 16);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) b.c[t] = buf_load16(codes, 4 * block < n_steps ? o + 16 * t * row_bytes : kOOB);
+  }
+  // Few tokens: a round of X, a token a load.  More: half a block, eight tokens a load.
+  __device__ __forceinline__ void load_round(Xs &b, uint32_t round) const {
+    const uint32_t o = round * 1024 + 16 * lane;
+#pragma unroll
+    for (int m = 0; m < kXLoads; ++m) b.x[m] = buf_load16(X, o < x_bytes ? m * x_bytes + o : kOOB);
+  }
+  __device__ __forceinline__ void load_half(Xs &b, uint32_t half) const {
+    const uint32_t o = half * 128 + 16 * (lane % 8);
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      b.x[i] = buf_load16(X, o < x_bytes ? (8 * i + lane / 8) * x_bytes + o : kOOB);
+  }
+  __device__ __forceinline__ void stage_round(const Xs &b) const {
+#pragma unroll
+    for (int m = 0; m < kXLoads; ++m)
+      *reinterpret_cast<u32x4_t *>(xs + ((lane / 16) * XR + m) * 256 + 16 * ((lane % 16) ^ m)) = code_order(b.x[m]);
+  }
+  __device__ __forceinline__ void stage_half(const Xs &b) const {
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+      const uint32_t m = 8 * i + lane / 8;
+      *reinterpret_cast<u32x4_t *>(xs + m * 128 + 16 * ((lane % 8) ^ (m % 8))) = code_order(b.x[i]);
+    }
+  }
+  // Fragments of a round's block q (few tokens) and of the half block in LDS.
+  __device__ __forceinline__ u32x4_t frag_round(int q, int j) const {
+    const uint32_t m = (lane % 16) % XR;
+    return *reinterpret_cast<const u32x4_t *>(xs + (q * XR + m) * 256 + 16 * ((4 * j + lane / 16) ^ m));
+  }
+  __device__ __forceinline__ u32x4_t frag_half(int m, int j) const {
+    const uint32_t r = lane % 16;
+    return *reinterpret_cast<const u32x4_t *>(xs + (16 * m + r) * 128 + 16 * ((4 * (j & 1) + lane / 16) ^ (r % 8)));
+  }
+
+  // Scales and zeros of a block as every lane knows them.
+  struct Known {
+    uint32_t s[NT][kSRegs], z[NT][kZRegs];
+    __device__ __forceinline__ float scale(int t, int k) const {
+      if constexpr (S16 && VS) return (k & 1) ? bf16_hi(s[t][k / 2]) : bf16_lo(s[t][k / 2]);
+      return __uint_as_float(S16 ? s[t][k] << 16 : s[t][k]);
+    }
+    __device__ __forceinline__ float zero(int t, int k) const {
+      return static_cast<float>(VS ? (z[t][0] >> (8 * k)) & 255u : z[t][VS ? 0 : k]);
+    }
+  };
+  __device__ __forceinline__ Known known(const Scales &b, int q) const {
+    Known v;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int k = 0; k < kSRegs; ++k) v.s[t][k] = from_lane_group(b.s[t][k], q);
+#pragma unroll
+      for (int k = 0; k < kZRegs; ++k) v.z[t][k] = from_lane_group(b.z[t][k], q);
+    }
+    return v;
+  }
+
+  struct Sums {
+    f32x4_t acc[MT][NT], sum[MT];
+  };
+  // Steps j0 .. j1 - 1 (of 32 columns) of a block: X's fragment of step j and token tile m is
+  // frag(m, j).  A group that ends inside goes to y; what is left stays in `a`.
+  template <bool EXACT, int J0, int J1, typename FRAG>
+  __device__ __forceinline__ void multiply(Sums &a, const Codes &c, const Known &v, uint32_t block, FRAG frag) {
+    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+    for (int j = J0; j < J1; ++j) {
+      if (4 * block + j >= n_steps) break;
+      const int k = j / (FS / 32);
+      if (j % (kFlush / 32) == 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          a.sum[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) a.acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
+      u32x4_t w[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float off = -16.0f - b.z[t][g];
+        const uint32_t cj = c.c[t][j];
+        w[t] = EXACT ? plain_codes(cj, v.zero(t, k)) : offset_codes(cj);
+      }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        const u32x4_t x = frag(m, j);
+        if constexpr (!EXACT) a.sum[m] = mfma16x16x32(x, ones, a.sum[m]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = EXACT ? acc[m][t][i] : __builtin_fmaf(off, sum[m][i], acc[m][t][i]);
-            y[m][t][i] = __builtin_fmaf(b.s[t][g], a, y[m][t][i]);
-          }
+        for (int t = 0; t < NT; ++t) a.acc[m][t] = mfma16x16x32(x, w[t], a.acc[m][t]);
+      }
+      if ((j + 1) % (kFlush / 32) == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float off = -16.0f - v.zero(t, k), s = v.scale(t, k);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float u = EXACT ? a.acc[m][t][i] : __builtin_fmaf(off, a.sum[m][i], a.acc[m][t][i]);
+              y[m][t][i] = __builtin_fmaf(s, u, y[m][t][i]);
+            }
+        }
       }
     }
+  }
+  __device__ __forceinline__ static void transpose(Codes &c) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) c.c[t] = transpose_lane_groups(c.c[t]);
   }
 
   __device__ __forceinline__ void clear() {
@@ -154,95 +281,201 @@ struct Tile {
         for (int i = 0; i < 4; ++i) v = __builtin_fmaf(0.0f, y[m][t][i], v);
     return v == 0.0f;
   }
-};
 
-template <int MT, int NT, int FS>
-__global__ __launch_bounds__(512) void group_linear_kernel(GroupView w, const uint16_t *__restrict__ X, int64_t M,
-                                                           uint32_t magic, uint16_t *__restrict__ Y) {
-  extern __shared__ __attribute__((aligned(16))) float part[];
-  constexpr int kRows = 16 * NT, kTokens = 16 * MT;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kRows, m0 = static_cast<int64_t>(blockIdx.y) * kTokens;
-  const uint32_t rows = static_cast<uint32_t>(min(w.n_rows - n0, int64_t(kRows)));
-  const uint32_t tokens = static_cast<uint32_t>(min(M - m0, int64_t(kTokens)));
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-
-  Tile<MT, NT, FS> T;
-  T.lane = threadIdx.x & 63;
-  T.row_bytes = static_cast<uint32_t>(w.n_cols / 2);
-  T.x_bytes = static_cast<uint32_t>(2 * w.n_cols);
-  T.per = static_cast<uint32_t>(w.group / 32);
-  T.magic = magic;
-  T.n_steps = static_cast<uint32_t>(w.n_cols / 32);
-  T.row_groups = T.n_steps / T.per;
-  T.s16 = w.scale_bf16;
-  T.zp = w.zeros != nullptr;
-  // Reads past the tile's own rows, and past the last one of the tensor, give zeros.
-  const int64_t g0 = n0 * T.row_groups;
-  const uint32_t n_groups = rows * T.row_groups, s_size = T.s16 ? 2 : 4;
-  T.codes = make_rsrc(w.codes + n0 * T.row_bytes, rows * T.row_bytes);
-  T.scales = make_rsrc(static_cast<const char *>(w.scales) + g0 * s_size, n_groups * s_size);
-  T.zeros = make_rsrc(T.zp ? w.zeros + g0 : nullptr, T.zp ? n_groups : 0u);
-  T.X = make_rsrc(X + m0 * w.n_cols, tokens * T.x_bytes);
-
-  const uint32_t blocks = (T.n_steps + 3) / 4;
-  T.clear();
-  typename Tile<MT, NT, FS>::Block b;
-  for (uint32_t k = wave; k < blocks; k += waves) {
-    T.load(b, k);
-    T.template multiply<false>(b, k);
-  }
-  if (__any(!T.finite())) {
-    T.clear();
-#pragma nounroll
-    for (uint32_t k = wave; k < blocks; k += waves) {
-      T.load(b, k);
-      T.template multiply<true>(b, k);
+  // The waves' sums added in wave order through `part`, [wave][m tile][t][token][row], and stored.
+  __device__ __forceinline__ void finish(float *part, uint32_t wave, uint32_t waves, uint32_t tokens, uint32_t rows,
+                                         uint16_t *Y, int64_t ldy) const {
+    constexpr uint32_t kTok = XR < 16 ? XR : 16, kPart = MT * NT * kTok * 16;
+    __syncthreads();  // the waves' X pieces are read
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t tok = 4 * (lane / 16) + i;
+          if (tok < kTok) part[wave * kPart + ((m * NT + t) * kTok + tok) * 16 + lane % 16] = y[m][t][i];
+        }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < kPart; e += blockDim.x) {
+      const uint32_t mt = e / (16 * kTok), m = 16 * (mt / NT) + (e / 16) % kTok, n = 16 * (mt % NT) + e % 16;
+      if (m >= tokens || n >= rows) continue;
+      float v = part[e];
+      for (uint32_t k = 1; k < waves; ++k) v += part[k * kPart + e];
+      Y[m * ldy + n] = to_bf16(v);
     }
   }
+};
 
-  // part[wave][m][t][i][lane]
-  constexpr uint32_t kPart = MT * NT * 4 * 64;
+// Up to 8 tokens: a round of everything in flight at once.  W: the most waves of a workgroup.
+template <int XR, int NT, int W, int FS, bool S16, bool VS>
+__global__ __launch_bounds__(64 * W) void group_few_kernel(GroupView w, const uint16_t *__restrict__ X, uint32_t M,
+                                                           uint32_t magic, uint16_t *__restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  using P = Product<XR, NT, FS, S16, VS>;
+  P T;
+  T.init(w, n0, X, M, magic);
+  T.xs = lds + wave * (XR * 1024);
+  T.clear();
+  auto rounds = [&](auto exact) {
+#pragma nounroll
+    for (uint32_t k = wave; 16 * k < T.n_steps; k += waves) {
+      typename P::Xs x;
+      typename P::Scales s;
+      typename P::Codes c[4];
+      typename P::Sums a;
+      T.load_round(x, k);
+      T.load_scales(s, k);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+      for (int q = 0; q < 4; ++q) T.load_codes(c[q], 4 * k + q);
+      __builtin_amdgcn_sched_barrier(0);
+      T.stage_round(x);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave * kPart + ((m * NT + t) * 4 + i) * 64 + T.lane] = T.y[m][t][i];
-  __syncthreads();
-  for (uint32_t e = threadIdx.x; e < kPart; e += blockDim.x) {
-    const uint32_t l = e & 63, i = (e >> 6) & 3, mt = e >> 8;
-    const uint32_t m = 16 * (mt / NT) + 4 * (l / 16) + i, n = 16 * (mt % NT) + l % 16;
-    if (m >= tokens || n >= rows) continue;
-    float v = part[e];
-    for (uint32_t k = 1; k < waves; ++k) v += part[k * kPart + e];
-    Y[(m0 + m) * w.n_rows + n0 + n] = to_bf16(v);
+      for (int q = 0; q < 4; ++q) {
+        if (4 * (4 * k + q) >= T.n_steps) break;
+        T.transpose(c[q]);
+        T.template multiply<decltype(exact)::value, 0, 4>(a, c[q], T.known(s, q), 4 * k + q,
+                                                          [&](int, int j) { return T.frag_round(q, j); });
+      }
+    }
+  };
+  rounds(std::false_type());
+  if (__any(!T.finite())) {
+    T.clear();
+    rounds(std::true_type());
   }
+  T.finish(reinterpret_cast<float *>(lds), wave, waves, M, static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT))),
+           Y + n0, w.n_rows);
 }
 
-template <int MT, int NT>
-hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, int waves, uint16_t *Y, hipStream_t stream) {
-  const int64_t gx = (w.n_rows + 16 * NT - 1) / (16 * NT), gy = (M + 16 * MT - 1) / (16 * MT);
+// More tokens, XR of them a workgroup: half a block of X and a block of codes in flight while the
+// one before is multiplied.
+template <int XR, int NT, int W, int FS, bool S16, bool VS>
+__global__ __launch_bounds__(64 * W) void group_many_kernel(GroupView w, const uint16_t *__restrict__ X, int64_t M,
+                                                            uint32_t magic, uint16_t *__restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT), m0 = static_cast<int64_t>(blockIdx.y) * XR;
+  const uint32_t tokens = static_cast<uint32_t>(min(M - m0, int64_t(XR)));
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  using P = Product<XR, NT, FS, S16, VS>;
+  P T;
+  T.init(w, n0, X + m0 * w.n_cols, tokens, magic);
+  T.xs = lds + wave * (XR * 128);
+  T.clear();
+  auto rounds = [&](auto exact) {
+    typename P::Xs x;
+    typename P::Scales s, s2;
+    typename P::Codes c, c2;
+    typename P::Sums a;
+    auto frag = [&](int m, int j) { return T.frag_half(m, j); };
+    T.load_scales(s, wave);
+    T.load_half(x, 8 * wave);
+    T.load_codes(c, 4 * wave);
+#pragma nounroll
+    for (uint32_t k = wave; 16 * k < T.n_steps; k += waves) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t block = 4 * k + q, next = q < 3 ? block + 1 : 4 * (k + waves);
+        T.stage_half(x);
+        __builtin_amdgcn_sched_barrier(0);
+        T.load_half(x, 2 * block + 1);
+        T.load_codes(c2, next);
+        if (q == 3) T.load_scales(s2, k + waves);
+        __builtin_amdgcn_sched_barrier(0);
+        const typename P::Known v = T.known(s, q);
+        T.transpose(c);
+        T.template multiply<decltype(exact)::value, 0, 2>(a, c, v, block, frag);
+        __builtin_amdgcn_sched_barrier(0);
+        T.stage_half(x);
+        __builtin_amdgcn_sched_barrier(0);
+        T.load_half(x, 2 * next);
+        __builtin_amdgcn_sched_barrier(0);
+        T.template multiply<decltype(exact)::value, 2, 4>(a, c, v, block, frag);
+        __builtin_amdgcn_sched_barrier(0);
+        c = c2;
+      }
+      s = s2;
+    }
+  };
+  rounds(std::false_type());
+  if (__any(!T.finite())) {
+    T.clear();
+    rounds(std::true_type());
+  }
+  T.finish(reinterpret_cast<float *>(lds), wave, waves, tokens,
+           static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT))), Y + m0 * w.n_rows + n0, w.n_rows);
+}
+
+template <bool FEW, int XR, int NT, int W>
+hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
+  const int64_t gx = (w.n_rows + 16 * NT - 1) / (16 * NT), gy = (M + XR - 1) / XR;
   if (gx > 0x7fffffff || gy > 0xffff) return hipErrorInvalidValue;
+  // as many waves as share the rounds evenly
+  const int64_t rounds = (w.n_cols + 511) / 512, each = (rounds + W - 1) / W;
+  const int waves = static_cast<int>((rounds + each - 1) / each);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * waves);
-  const size_t lds = static_cast<size_t>(waves) * MT * NT * 1024;
+  const size_t xs = FEW ? XR * 1024 : XR * 128, part = ((XR + 15) / 16) * NT * (XR < 16 ? XR : 16) * 64;
+  const size_t lds = static_cast<size_t>(waves) * (xs > part ? xs : part);
   const uint32_t magic = group_magic(static_cast<uint32_t>(w.group / 32));
-  if (w.group % 128 == 0)
-    hipLaunchKernelGGL((group_linear_kernel<MT, NT, 128>), grid, block, lds, stream, w, X, M, magic, Y);
-  else if (w.group % 64 == 0)
-    hipLaunchKernelGGL((group_linear_kernel<MT, NT, 64>), grid, block, lds, stream, w, X, M, magic, Y);
-  else
-    hipLaunchKernelGGL((group_linear_kernel<MT, NT, 32>), grid, block, lds, stream, w, X, M, magic, Y);
-  return hipGetLastError();
+  auto launch = [&](auto kernel) {
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, grid, block, lds, stream, w, X, M, magic, Y);
+    return hipGetLastError();
+  };
+  // Groups of whole blocks take one scale a block; groups of 64 and 32 theirs by one aligned load;
+  // any other group (and unaligned arrays) a load for each 32 columns.
+  const int64_t per_block = 128 / w.group;
+  const bool aligned = (w.group == 64 || w.group == 32) && w.n_cols % 128 == 0 &&
+                       reinterpret_cast<uintptr_t>(w.scales) % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(w.zeros) % per_block == 0;
+  const int kind = w.group % 128 == 0 ? 0 : !aligned ? 3 : w.group == 64 ? 1 : 2;
+  switch (2 * kind + (w.scale_bf16 ? 1 : 0)) {
+#define QLORA_ONE(n, fs, s16, vs)                                           \
+  case n:                                                                   \
+    if constexpr (FEW)                                                      \
+      return launch(group_few_kernel<XR, NT, W, fs, s16, vs>);              \
+    else                                                                    \
+      return launch(group_many_kernel<XR, NT, W, fs, s16, vs>);
+    QLORA_ONE(0, 128, false, false)
+    QLORA_ONE(1, 128, true, false)
+    QLORA_ONE(2, 64, false, true)
+    QLORA_ONE(3, 64, true, true)
+    QLORA_ONE(4, 32, false, true)
+    QLORA_ONE(5, 32, true, true)
+    QLORA_ONE(6, 32, false, false)
+    QLORA_ONE(7, 32, true, false)
+#undef QLORA_ONE
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
+// Up to 8 tokens the whole of a wave's round is in flight (1024-column rows: 1 token 7.8 us, 4
+// tokens of 12288 rows 9.0 us); more are multiplied by tiles of 16, 32 or 64 tokens.  The height of
+// a workgroup's tile is the one that leaves the fewest rows to the busiest CU.
 hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
-  const int64_t blocks = (w.n_cols + 127) / 128;
-  const int waves = static_cast<int>(blocks < 8 ? blocks : 8);
-  if (M <= 16) return go<1, 2>(w, X, M, waves, Y, stream);
-  if (M <= 32) return go<2, 2>(w, X, M, waves, Y, stream);
-  return go<4, 2>(w, X, M, waves, Y, stream);
+  if (M == 1) return go<true, 1, 1, 16>(w, X, M, Y, stream);
+  if (M <= 4) return go<true, 4, 1, 16>(w, X, M, Y, stream);
+  if (M <= 8) return go<true, 8, 1, 16>(w, X, M, Y, stream);
+  const int64_t tiles = (w.n_rows + 15) / 16;
+  if (M <= 16) {
+    if (tiles <= 256) return go<false, 16, 1, 16>(w, X, M, Y, stream);
+    if (tiles <= 512) return go<false, 16, 2, 16>(w, X, M, Y, stream);
+    return go<false, 16, 3, 8>(w, X, M, Y, stream);
+  }
+  if (M <= 32) {
+    if (tiles <= 512) return go<false, 32, 2, 8>(w, X, M, Y, stream);
+    return go<false, 32, 3, 8>(w, X, M, Y, stream);
+  }
+  if (tiles <= 512) return go<false, 64, 2, 8>(w, X, M, Y, stream);
+  return go<false, 64, 3, 8>(w, X, M, Y, stream);
 }
 
 }  // namespace qlora
