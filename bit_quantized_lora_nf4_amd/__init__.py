@@ -156,6 +156,19 @@ def _guard(device):
     return torch.cuda.device(device)
 
 
+def _run(name, fn, device, *args):
+    """The library call fn(*args, stream) on the device of this index and its current stream,
+    its status checked."""
+    c = _torch()._C
+    if c._cuda_getDevice() == device:
+        status = fn(*args, c._cuda_getCurrentRawStream(device))
+    else:
+        with _torch().cuda.device(device):
+            status = fn(*args, c._cuda_getCurrentRawStream(device))
+    if status:
+        _lib.check(status, name)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -184,6 +197,17 @@ def _on(t, name, device=None):
 def _need(t, dtype, name, shape=None, device=None):
     _meta(t, dtype, name, shape)
     _on(t, name, device)
+
+
+def _fits(t, dtype, shape, device):
+    """Whether t is a contiguous GPU tensor of this dtype and shape on the device of this index:
+    the checks of ``_need`` as one test, for the calls that are short enough for their time on
+    the host to count (a product of one token: 10.8 us a call with _Args alone, 7.5 with
+    this).  Where it fails, the caller goes through _Args, which says why."""
+    try:
+        return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device >= 0
+    except AttributeError:
+        return False
 
 
 class _Args:
@@ -705,8 +729,20 @@ class GroupWeight:
         return (self.n_rows, self.n_cols)
 
     def descriptor(self):
-        return _lib.qlora_group_weight(self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.zeros), self.n_rows,
-                                       self.n_cols, self.group, _type_of(self.scales, "scales"))
+        z = self.zeros
+        return _lib.qlora_group_weight(self.codes.data_ptr(), self.scales.data_ptr(), None if z is None else z.data_ptr(),
+                                       self.n_rows, self.n_cols, self.group, _type_of(self.scales, "scales"))
+
+    def fits(self, device):
+        """Whether the arrays are what a call on the device of this index takes (see _fits)."""
+        N, K, g = self.n_rows, self.n_cols, self.group
+        if N < 1 or K < 1 or g < 1 or g % 32 or K % g:
+            return False
+        torch, s, z = _torch(), self.scales, self.zeros
+        shape = (N, K // g)
+        return (_fits(self.codes, torch.uint8, (N * K // 2,), device) and
+                (_fits(s, torch.bfloat16, shape, device) or _fits(s, torch.float32, shape, device)) and
+                (z is None or _fits(z, torch.uint8, shape, device)))
 
     def checked(self):
         """The argument checks of a call with this weight (see _Args), its arrays among them."""
@@ -734,9 +770,9 @@ def _type_of(t, name):
     """QLORA_BF16 or QLORA_F32 of a tensor or dtype."""
     torch = _torch()
     dtype = getattr(t, "dtype", t)
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return QLORA_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return QLORA_F32
     raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
 
@@ -760,10 +796,8 @@ def group_quantize(W, group=128, zeros=False, scale_dtype=None):
     codes = torch.empty(N * K // 2, dtype=torch.uint8, device=dev)
     scales = torch.empty((N, K // group), dtype=torch.bfloat16 if st == QLORA_BF16 else torch.float32, device=dev)
     z = torch.empty((N, K // group), dtype=torch.uint8, device=dev) if zeros else None
-    with _guard(dev):
-        status = qlora_group_quantize(W.data_ptr(), wt, N, K, group, st, codes.data_ptr(), scales.data_ptr(), _ptr(z),
-                                      _stream(W))
-    _lib.check(status, "qlora_group_quantize")
+    _run("qlora_group_quantize", qlora_group_quantize, W.get_device(), W.data_ptr(), wt, N, K, group, st,
+         codes.data_ptr(), scales.data_ptr(), _ptr(z))
     return GroupWeight(codes, scales, z, N, K, group)
 
 
@@ -779,9 +813,7 @@ def group_dequantize(gw, dtype=None, out=None):
     dev = chk.device
     if out is None:
         out = torch.empty(gw.shape, dtype=dtype, device=dev)
-    with _guard(dev):
-        status = qlora_group_dequantize(gw.descriptor(), out.data_ptr(), ot, _stream(out))
-    _lib.check(status, "qlora_group_dequantize")
+    _run("qlora_group_dequantize", qlora_group_dequantize, out.get_device(), gw.descriptor(), out.data_ptr(), ot)
     return out
 
 
@@ -789,22 +821,20 @@ def group_linear_fwd(gw, X, Y=None):
     """Y [M, n_rows] = bf16(X W^T) for X [M, n_cols] bf16 and a GroupWeight: made for few
     tokens (the weight is read once for up to 64 of them, and again for every 64 more)."""
     torch = _torch()
-    chk = gw.checked()
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError(f"X must be 2-D [M, {gw.n_cols}]")
-    M = X.shape[0]
-    chk.need(X, torch.bfloat16, "X", (M, gw.n_cols))
-    if Y is not None:
-        chk.need(Y, torch.bfloat16, "Y", (M, gw.n_rows))
-    chk.devices()
-    dev = chk.device
+    M, N, bf, i = X.shape[0], gw.n_rows, torch.bfloat16, X.get_device()
+    if not (gw.fits(i) and _fits(X, bf, (M, gw.n_cols), i) and (Y is None or _fits(Y, bf, (M, N), i))):
+        chk = gw.checked()
+        chk.need(X, bf, "X", (M, gw.n_cols))
+        if Y is not None:
+            chk.need(Y, bf, "Y", (M, N))
+        chk.devices()
     if Y is None:
-        Y = torch.empty((M, gw.n_rows), dtype=torch.bfloat16, device=dev)
+        Y = X.new_empty((M, N))
     if M == 0:
         return Y
-    with _guard(dev):
-        status = qlora_group_linear_fwd(gw.descriptor(), X.data_ptr(), M, Y.data_ptr(), _stream(X))
-    _lib.check(status, "qlora_group_linear_fwd")
+    _run("qlora_group_linear_fwd", qlora_group_linear_fwd, i, gw.descriptor(), X.data_ptr(), M, Y.data_ptr())
     return Y
 
 
@@ -828,6 +858,20 @@ def _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight):
     return rot
 
 
+def _qk_fits(dtype, device, M, d, positions, inv_freq, q_weight, k_weight):
+    """_qk_operands as one test (see _fits): the number of rotated elements, or None."""
+    torch = _torch()
+    if not (_fits(positions, torch.int64, (M,), device) and isinstance(inv_freq, torch.Tensor)):
+        return None
+    half = inv_freq.numel()
+    if d < 4 or d > 256 or d % 4 or 2 * half > d or half % 2 or not _fits(inv_freq, torch.float32, (half,), device):
+        return None
+    if not (q_weight is None and k_weight is None or
+            _fits(q_weight, dtype, (d,), device) and _fits(k_weight, dtype, (d,), device)):
+        return None
+    return 2 * half
+
+
 def qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, Q=None, K=None):
     """Queries and keys from the rows Y [M, (n_heads + 2 n_kv_heads) d] of a fused projection
@@ -844,28 +888,29 @@ def qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight=None,
         raise ValueError(f"{n_heads} query and {n_kv_heads} key heads")
     if Y.dim() != 2 or Y.shape[1] % (n_heads + 2 * n_kv_heads):
         raise ValueError(f"Y has shape {tuple(Y.shape)}, expected [M, ({n_heads} + 2 * {n_kv_heads}) d]")
-    dtype, dev = Y.dtype, Y.device
-    chk = _Args(dev)
-    chk.need(Y, dtype, "Y")
+    dtype, i = Y.dtype, Y.get_device()
     M = Y.shape[0]
     d = Y.shape[1] // (n_heads + 2 * n_kv_heads)
-    rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
-    if Q is not None:
-        chk.need(Q, dtype, "Q", (M, n_heads, d))
-    if K is not None:
-        chk.need(K, dtype, "K", (M, n_kv_heads, d))
-    chk.devices()
+    rot = _qk_fits(dtype, i, M, d, positions, inv_freq, q_weight, k_weight)
+    if (rot is None or i < 0 or not Y.is_contiguous() or not (Q is None or _fits(Q, dtype, (M, n_heads, d), i)) or
+            not (K is None or _fits(K, dtype, (M, n_kv_heads, d), i))):
+        chk = _Args(Y.device)
+        chk.need(Y, dtype, "Y")
+        rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
+        if Q is not None:
+            chk.need(Q, dtype, "Q", (M, n_heads, d))
+        if K is not None:
+            chk.need(K, dtype, "K", (M, n_kv_heads, d))
+        chk.devices()
     if Q is None:
-        Q = torch.empty((M, n_heads, d), dtype=dtype, device=dev)
+        Q = Y.new_empty((M, n_heads, d))
     if K is None:
-        K = torch.empty((M, n_kv_heads, d), dtype=dtype, device=dev)
+        K = Y.new_empty((M, n_kv_heads, d))
     if M == 0:
         return Q, K
     shape = _lib.qlora_qk_shape(M, n_heads, n_kv_heads, d, rot, t, 1 if interleaved else 0, eps)
-    with _guard(dev):
-        status = qlora_qk_fwd(shape, Y.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
-                              _ptr(k_weight), Q.data_ptr(), K.data_ptr(), _stream(Y))
-    _lib.check(status, "qlora_qk_fwd")
+    _run("qlora_qk_fwd", qlora_qk_fwd, i, shape, Y.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+         _ptr(q_weight), _ptr(k_weight), Q.data_ptr(), K.data_ptr())
     return Q, K
 
 
@@ -886,43 +931,51 @@ def qk_norm_rope_bwd(dQ, dK, dV, positions, inv_freq, Y=None, q_weight=None, k_w
     nk = dK.shape[1]
     if nq < 1 or nk < 1:
         raise ValueError(f"{nq} query and {nk} key heads")
-    chk = _Args(dev)
-    chk.need(dQ, dtype, "dQ")
-    chk.need(dK, dtype, "dK", (M, nk, d))
-    chk.need(dV, dtype, "dV", (M, nk, d))
-    rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
+    i = dQ.get_device()
     N = (nq + 2 * nk) * d
-    if dY is not None:
-        chk.need(dY, dtype, "dY", (M, N))
-    shape = _lib.qlora_qk_shape(M, nq, nk, d, rot, t, 1 if interleaved else 0, eps)
     norm = q_weight is not None
-    nbytes = 0
-    if norm:
-        if Y is None:
-            raise ValueError("Y is required with weights")
-        chk.need(Y, dtype, "Y", (M, N))
-        for g, name in ((dqw, "dqw"), (dkw, "dkw")):
-            if g is not None:
-                chk.need(g, dtype, name, (d,))
-        nbytes = qlora_workspace_bytes_qk(shape, 1) if M else 0
-        chk.workspace(ws, nbytes)
-    else:
+    if norm and Y is None:
+        raise ValueError("Y is required with weights")
+    rot = _qk_fits(dtype, i, M, d, positions, inv_freq, q_weight, k_weight)
+    if not (rot is not None and dQ.is_contiguous() and _fits(dK, dtype, (M, nk, d), i) and
+            _fits(dV, dtype, (M, nk, d), i) and (dY is None or _fits(dY, dtype, (M, N), i)) and
+            (not norm or _fits(Y, dtype, (M, N), i) and all(g is None or _fits(g, dtype, (d,), i) for g in (dqw, dkw)))):
+        chk = _Args(dev)
+        chk.need(dQ, dtype, "dQ")
+        chk.need(dK, dtype, "dK", (M, nk, d))
+        chk.need(dV, dtype, "dV", (M, nk, d))
+        rot = _qk_operands(chk, dtype, M, d, positions, inv_freq, q_weight, k_weight)
+        if dY is not None:
+            chk.need(dY, dtype, "dY", (M, N))
+        if norm:
+            chk.need(Y, dtype, "Y", (M, N))
+            for g, name in ((dqw, "dqw"), (dkw, "dkw")):
+                if g is not None:
+                    chk.need(g, dtype, name, (d,))
+            shape = _lib.qlora_qk_shape(M, nq, nk, d, rot, t, 1 if interleaved else 0, eps)
+            chk.workspace(ws, qlora_workspace_bytes_qk(shape, 1))
+        chk.devices()
+    shape = _lib.qlora_qk_shape(M, nq, nk, d, rot, t, 1 if interleaved else 0, eps)
+    if not norm:
         Y = dqw = dkw = ws = None
-    chk.devices()
-    if dY is None:
-        dY = torch.empty((M, N), dtype=dtype, device=dev)
-    if norm:
-        dqw = torch.empty(d, dtype=dtype, device=dev) if dqw is None else dqw
-        dkw = torch.empty(d, dtype=dtype, device=dev) if dkw is None else dkw
-        if M == 0:
-            return dY, dqw.zero_(), dkw.zero_()
+    elif M:
+        nbytes = qlora_workspace_bytes_qk(shape, 1)
         if ws is None:
             ws = _scratch(nbytes, dev)
-    if M == 0:
+        else:
+            chk = _Args(dev)
+            chk.workspace(ws, nbytes)
+            chk.devices()
+    if dY is None:
+        dY = dQ.new_empty((M, N))
+    if norm:
+        dqw = dQ.new_empty((d,)) if dqw is None else dqw
+        dkw = dQ.new_empty((d,)) if dkw is None else dkw
+        if M == 0:
+            return dY, dqw.zero_(), dkw.zero_()
+    elif M == 0:
         return dY, None, None
-    with _guard(dev):
-        status = qlora_qk_bwd(shape, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), _ptr(Y), positions.data_ptr(),
-                              inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight), dY.data_ptr(), _ptr(dqw), _ptr(dkw),
-                              _ptr(ws), 0 if ws is None else ws.numel(), _stream(dQ))
-    _lib.check(status, "qlora_qk_bwd")
+    _run("qlora_qk_bwd", qlora_qk_bwd, i, shape, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), _ptr(Y),
+         positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight), dY.data_ptr(), _ptr(dqw), _ptr(dkw),
+         _ptr(ws), 0 if ws is None else ws.numel())
     return dY, dqw, dkw

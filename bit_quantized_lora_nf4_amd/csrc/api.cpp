@@ -1282,7 +1282,7 @@ int qlora_qk_bwd(const qlora_qk_shape *shape, const void *dQ, const void *dK, co
   if (e != QLORA_OK) return e;
   return launched(qlora::launch_qk_bwd(dQ, dK, dV, Y, s, shape->dtype == QLORA_BF16, shape->interleaved != 0,
                                        positions, inv_freq, q_weight, k_weight, dY, dqw, dkw, part,
-                                       static_cast<hipStream_t>(stream)),
+                                       static_cast<uint32_t *>(workspace), static_cast<hipStream_t>(stream)),
                   "qk_bwd");
 }
 

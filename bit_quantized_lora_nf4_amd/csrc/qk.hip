@@ -27,57 +27,55 @@
 namespace qlora {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kThreads = 256, kWaves = kThreads / 64;           // forward
+constexpr int kBwdThreads = 1024, kBwdWaves = kBwdThreads / 64;  // backward: few partial sums
 constexpr int kMaxPairs = kQkMaxDim / 2;
 
-// V values as fp32 from / to memory of T16 ? bf16 : fp32; the access is V * size bytes wide.
+// V values of a tensor (T16: bf16, else fp32) as loaded: one access of 16, 8 or 4 bytes.
 template <bool T16, int V>
-__device__ __forceinline__ void load_values(const void *p, int64_t i, float *v) {
-  if constexpr (T16) {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-    uint32_t u[V / 2];
-    if constexpr (V == 8) {
-      const u32x4_t t = *reinterpret_cast<const u32x4_t *>(q);
-      u[0] = t[0], u[1] = t[1], u[2] = t[2], u[3] = t[3];
-    } else if constexpr (V == 4) {
-      const u32x2_t t = *reinterpret_cast<const u32x2_t *>(q);
-      u[0] = t[0], u[1] = t[1];
-    } else {
-      u[0] = *reinterpret_cast<const uint32_t *>(q);
-    }
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) v[2 * e] = bf16_lo(u[e]), v[2 * e + 1] = bf16_hi(u[e]);
+struct Raw {
+  static constexpr int kWords = T16 ? V / 2 : V;
+  uint32_t w[kWords];
+};
+template <bool T16, int V>
+__device__ __forceinline__ void load_raw(Raw<T16, V> &r, const void *p, int64_t i) {
+  const char *q = static_cast<const char *>(p) + i * (T16 ? 2 : 4);
+  if constexpr (Raw<T16, V>::kWords == 4) {
+    const u32x4_t t = *reinterpret_cast<const u32x4_t *>(q);
+    r.w[0] = t[0], r.w[1] = t[1], r.w[2] = t[2], r.w[3] = t[3];
+  } else if constexpr (Raw<T16, V>::kWords == 2) {
+    const u32x2_t t = *reinterpret_cast<const u32x2_t *>(q);
+    r.w[0] = t[0], r.w[1] = t[1];
   } else {
-    const float *q = static_cast<const float *>(p) + i;
-    if constexpr (V == 4) {
-      const f32x4_t t = *reinterpret_cast<const f32x4_t *>(q);
-      v[0] = t[0], v[1] = t[1], v[2] = t[2], v[3] = t[3];
-    } else {
-      const u32x2_t t = *reinterpret_cast<const u32x2_t *>(q);
-      v[0] = __uint_as_float(t[0]), v[1] = __uint_as_float(t[1]);
-    }
+    r.w[0] = *reinterpret_cast<const uint32_t *>(q);
   }
 }
 template <bool T16, int V>
-__device__ __forceinline__ void store_values(void *p, int64_t i, const float *v) {
-  if constexpr (T16) {
-    uint16_t *q = static_cast<uint16_t *>(p) + i;
-    uint32_t u[V / 2];
+__device__ __forceinline__ void store_raw(const Raw<T16, V> &r, void *p, int64_t i) {
+  char *q = static_cast<char *>(p) + i * (T16 ? 2 : 4);
+  if constexpr (Raw<T16, V>::kWords == 4)
+    *reinterpret_cast<u32x4_t *>(q) = u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]};
+  else if constexpr (Raw<T16, V>::kWords == 2)
+    *reinterpret_cast<u32x2_t *>(q) = u32x2_t{r.w[0], r.w[1]};
+  else
+    *reinterpret_cast<uint32_t *>(q) = r.w[0];
+}
+template <bool T16, int V>
+__device__ __forceinline__ void to_values(const Raw<T16, V> &r, float *v) {
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) u[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-    if constexpr (V == 8)
-      *reinterpret_cast<u32x4_t *>(q) = u32x4_t{u[0], u[1], u[2], u[3]};
-    else if constexpr (V == 4)
-      *reinterpret_cast<u32x2_t *>(q) = u32x2_t{u[0], u[1]};
+  for (int e = 0; e < Raw<T16, V>::kWords; ++e) {
+    if constexpr (T16)
+      v[2 * e] = bf16_lo(r.w[e]), v[2 * e + 1] = bf16_hi(r.w[e]);
     else
-      *reinterpret_cast<uint32_t *>(q) = u[0];
-  } else {
-    float *q = static_cast<float *>(p) + i;
-    if constexpr (V == 4)
-      *reinterpret_cast<f32x4_t *>(q) = f32x4_t{v[0], v[1], v[2], v[3]};
-    else
-      *reinterpret_cast<u32x2_t *>(q) = u32x2_t{__float_as_uint(v[0]), __float_as_uint(v[1])};
+      v[e] = __uint_as_float(r.w[e]);
   }
+}
+template <bool T16, int V>
+__device__ __forceinline__ Raw<T16, V> from_values(const float *v) {
+  Raw<T16, V> r;
+#pragma unroll
+  for (int e = 0; e < Raw<T16, V>::kWords; ++e) r.w[e] = T16 ? pack_bf16x2(v[2 * e], v[2 * e + 1]) : __float_as_uint(v[e]);
+  return r;
 }
 
 // What a lane holds of every head: chunks at elements o0 and o1 (has0, has1: within the
@@ -88,9 +86,8 @@ struct Unit {
 };
 template <int V, bool INTER>
 __device__ __forceinline__ Unit unit_of(int u, const QkShape &s) {
-  const int turning = s.rot / (2 * V);
   Unit x;
-  x.turns = u < turning;
+  x.turns = u < s.rot / (2 * V);
   if (!x.turns || INTER) {
     x.o0 = 2 * u * V;
     x.o1 = x.o0 + V;
@@ -102,6 +99,29 @@ __device__ __forceinline__ Unit unit_of(int u, const QkShape &s) {
   x.has1 = x.o1 < s.d;
   return x;
 }
+// A lane's two chunks of a head at element i of a tensor (zeros where there is none).
+template <bool T16, int V>
+struct Both {
+  Raw<T16, V> c[2];
+  __device__ __forceinline__ void load(const void *p, int64_t i, const Unit &u, bool on) {
+#pragma unroll
+    for (int e = 0; e < Raw<T16, V>::kWords; ++e) c[0].w[e] = c[1].w[e] = 0u;
+    if (on && u.has0) load_raw(c[0], p, i + u.o0);
+    if (on && u.has1) load_raw(c[1], p, i + u.o1);
+  }
+  __device__ __forceinline__ void store(void *p, int64_t i, const Unit &u) const {
+    if (u.has0) store_raw(c[0], p, i + u.o0);
+    if (u.has1) store_raw(c[1], p, i + u.o1);
+  }
+  __device__ __forceinline__ void values(float *v) const {
+    to_values(c[0], v);
+    to_values(c[1], v + V);
+  }
+  __device__ __forceinline__ void set(const float *v) {
+    c[0] = from_values<T16, V>(v);
+    c[1] = from_values<T16, V>(v + V);
+  }
+};
 
 // Sines and cosines of a token's pairs into the wave's own LDS, then the V pairs of this
 // lane's unit.  LDS accesses of one wave stay in order, so no barrier is needed.
@@ -138,10 +158,74 @@ __device__ __forceinline__ void turn(float *x, const float *co, const float *si,
   }
 }
 
+constexpr int kInFlight = 16;  // partial sums a thread asks for before it adds them
+constexpr int kSC1 = 16;       // buffer cache policy: agent-coherent access
+
+// Sum over the `lanes` lanes of a head (a power of two, the same for the whole launch), known
+// to all of them: neighbours within 16 lanes by data-parallel moves, then rows of 16.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+// The sum of each lane with its partner 16 (32) lanes away.
+template <int STEP>
+__device__ __forceinline__ float rows_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  uint32_t a, b;
+  if constexpr (STEP == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    a = r[0], b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    a = r[0], b = r[1];
+  }
+  return __uint_as_float(a) + __uint_as_float(b);
+}
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) v += __shfl_xor(v, m, 64);
+  if (lanes > 1) v += moved<0xB1>(v);   // lanes 1 0 3 2
+  if (lanes > 2) v += moved<0x4E>(v);   // lanes 2 3 0 1
+  if (lanes > 4) v += moved<0x141>(v);  // mirrored within 8
+  if (lanes > 8) v += moved<0x140>(v);  // mirrored within 16
+  if (lanes > 16) v = rows_sum<16>(v);
+  if (lanes > 32) v = rows_sum<32>(v);
   return v;
 }
+// Sum over the lanes of a wave that are a multiple of `lanes` apart, known to the first `lanes`.
+__device__ __forceinline__ float heads_sum(float v, int lanes) {
+  if (lanes <= 1) v += moved<0x121>(v);  // a row of 16 turned by 1, 2, 4, 8
+  if (lanes <= 2) v += moved<0x122>(v);
+  if (lanes <= 4) v += moved<0x124>(v);
+  if (lanes <= 8) v += moved<0x128>(v);
+  if (lanes <= 16) v = rows_sum<16>(v);
+  if (lanes <= 32) v = rows_sum<32>(v);
+  return v;
+}
+// 1 / sqrt(mean + eps): the hardware's reciprocal root is within a unit in the last place; its
+// argument may not be subnormal, which only a zero eps allows (scaled by 2^48 then).
+__device__ __forceinline__ float inverse_rms(float sum, const QkShape &s) {
+  const float m = sum * s.inv_d + s.eps;
+  return m < 0x1p-100f ? __builtin_amdgcn_rsqf(m * 0x1p48f) * 0x1p24f : __builtin_amdgcn_rsqf(m);
+}
+
+// A choice of values: the operator's own is one of places where both sides are variables, which
+// keeps what a lambda captures in memory.
+template <typename T>
+__device__ __forceinline__ T pick(bool first, T a, T b) {
+  return first ? a : b;
+}
+
+// A wave's work: rounds of 64 / lanes heads of one token.  The q heads' rounds come first, then
+// the k heads' (then, backward, the v heads'); a round never holds heads of two kinds, so what a
+// head is is the same for the whole wave.
+struct Rounds {
+  int heads_per, q, k, total;
+  __device__ __forceinline__ Rounds(const QkShape &s, bool with_v) {
+    heads_per = 64 / s.lanes;
+    q = (s.nq + heads_per - 1) / heads_per;
+    k = (s.nk + heads_per - 1) / heads_per;
+    total = q + (with_v ? 2 * k : k);
+  }
+};
 
 template <bool T16, int V, bool INTER>
 __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict__ Y, QkShape s,
@@ -151,203 +235,240 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict
                                                           void *__restrict__ Q, void *__restrict__ K) {
   __shared__ float lds[kWaves][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int u = lane & (s.lanes - 1), heads_per = 64 / s.lanes, sub = lane / s.lanes, heads = s.nq + s.nk;
+  const int u = lane & (s.lanes - 1), sub = lane / s.lanes;
   const Unit un = unit_of<V, INTER>(u, s);
+  const Rounds R(s, false);
   const bool norm = qw != nullptr;
-  float wq[2 * V], wk[2 * V];
-#pragma unroll
-  for (int e = 0; e < 2 * V; ++e) wq[e] = wk[e] = 1.0f;
-  if (norm) {
-    if (un.has0) load_values<T16, V>(qw, un.o0, wq), load_values<T16, V>(kw, un.o0, wk);
-    if (un.has1) load_values<T16, V>(qw, un.o1, wq + V), load_values<T16, V>(kw, un.o1, wk + V);
-  }
+  using B = Both<T16, V>;
+  B wq, wk;
+  wq.load(qw, 0, un, norm);
+  wk.load(kw, 0, un, norm);
   const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + wave; task < tasks; task += step) {
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(wave); task < tasks;
+       task += step) {
     const int64_t m = task / s.split;
-    const int part = static_cast<int>(task - m * s.split);
+    const int first = static_cast<int>(task - m * s.split) * s.per, last = min(first + s.per, R.total);
+    // head of this lane in a round: of q or k, and among the row's
+    auto load = [&](B &x, int r) {
+      const bool is_q = r < R.q;
+      const int h = (is_q ? r : r - R.q) * R.heads_per + sub;
+      x.load(Y, m * s.row + static_cast<int64_t>(is_q ? h : s.nq + h) * s.d, un, h < pick(is_q, s.nq, s.nk));
+    };
+    B next;
+    load(next, first);
     float co[V], si[V];
     angles<V>(positions[m], inv_freq, s, lane, u, un.turns, lds[wave], co, si);
-    const int h1 = min(heads, (part + 1) * s.per * heads_per);
-    for (int h = part * s.per * heads_per + sub; h < h1; h += heads_per) {
-      float x[2 * V];
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) x[e] = 0.0f;
-      const int64_t at = m * s.row + static_cast<int64_t>(h) * s.d;
-      if (un.has0) load_values<T16, V>(Y, at + un.o0, x);
-      if (un.has1) load_values<T16, V>(Y, at + un.o1, x + V);
+    for (int r = first; r < last; ++r) {
+      B x = next;
+      if (r + 1 < last) load(next, r + 1);
+      const bool is_q = r < R.q;
+      const int h = (is_q ? r : r - R.q) * R.heads_per + sub, heads = pick(is_q, s.nq, s.nk);
+      float v[2 * V];
+      x.values(v);
       if (norm) {
-        float sq = 0.0f;
+        float sq = 0.0f, w[2 * V];
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
-        sq = lanes_sum(sq, s.lanes);
-        const float r = 1.0f / sqrtf(sq * s.inv_d + s.eps);
+        for (int e = 0; e < 2 * V; ++e) sq = __builtin_fmaf(v[e], v[e], sq);
+        const float rms = inverse_rms(lanes_sum(sq, s.lanes), s);
+        if (is_q)
+          wq.values(w);
+        else
+          wk.values(w);
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) x[e] = x[e] * r * (h < s.nq ? wq[e] : wk[e]);
+        for (int e = 0; e < 2 * V; ++e) v[e] = v[e] * rms * w[e];
       }
-      turn<V, INTER>(x, co, si, 1.0f);
-      void *out = h < s.nq ? Q : K;
-      const int64_t to = h < s.nq ? (m * s.nq + h) * s.d : (m * s.nk + h - s.nq) * s.d;
-      if (un.has0) store_values<T16, V>(out, to + un.o0, x);
-      if (un.has1) store_values<T16, V>(out, to + un.o1, x + V);
+      turn<V, INTER>(v, co, si, 1.0f);
+      x.set(v);
+      if (h < heads) x.store(pick(is_q, Q, K), (m * heads + h) * s.d, un);
     }
   }
 }
 
 template <bool T16, int V, bool INTER>
-__global__ __launch_bounds__(kThreads) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
+__global__ __launch_bounds__(kBwdThreads) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
                                                           const void *__restrict__ dV, const void *__restrict__ Y,
                                                           QkShape s, const int64_t *__restrict__ positions,
                                                           const float *__restrict__ inv_freq,
                                                           const void *__restrict__ qw, const void *__restrict__ kw,
-                                                          void *__restrict__ dY, float *__restrict__ part_dw) {
-  __shared__ float lds[kWaves][2 * kMaxPairs];
+                                                          void *__restrict__ dY, void *__restrict__ dqw, void *__restrict__ dkw,
+                                                          float *__restrict__ part, uint32_t *__restrict__ ticket) {
+  __shared__ float lds[kBwdWaves][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int u = lane & (s.lanes - 1), heads_per = 64 / s.lanes, sub = lane / s.lanes, heads = s.nq + 2 * s.nk;
+  const int u = lane & (s.lanes - 1), sub = lane / s.lanes;
   const Unit un = unit_of<V, INTER>(u, s);
+  const Rounds R(s, true);
   const bool norm = qw != nullptr;
-  float wq[2 * V], wk[2 * V], dwq[2 * V], dwk[2 * V];
+  using B = Both<T16, V>;
+  B wq, wk;
+  wq.load(qw, 0, un, norm);
+  wk.load(kw, 0, un, norm);
+  float dwq[2 * V], dwk[2 * V];
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) wq[e] = wk[e] = 1.0f, dwq[e] = dwk[e] = 0.0f;
-  if (norm) {
-    if (un.has0) load_values<T16, V>(qw, un.o0, wq), load_values<T16, V>(kw, un.o0, wk);
-    if (un.has1) load_values<T16, V>(qw, un.o1, wq + V), load_values<T16, V>(kw, un.o1, wk + V);
-  }
-  const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWaves + wave; task < tasks; task += step) {
+  for (int e = 0; e < 2 * V; ++e) dwq[e] = dwk[e] = 0.0f;
+  const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kBwdWaves;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kBwdWaves + __builtin_amdgcn_readfirstlane(wave); task < tasks;
+       task += step) {
     const int64_t m = task / s.split;
-    const int part = static_cast<int>(task - m * s.split);
+    const int first = static_cast<int>(task - m * s.split) * s.per, last = min(first + s.per, R.total);
+    auto head = [&](int r) __attribute__((always_inline)) { return (r < R.q ? r : r < R.q + R.k ? r - R.q : r - R.q - R.k) * R.heads_per + sub; };
+    auto row_at = [&](int r, int h) __attribute__((always_inline)) {
+      return m * s.row + static_cast<int64_t>(r < R.q ? h : r < R.q + R.k ? s.nq + h : s.nq + s.nk + h) * s.d;
+    };
+    auto load = [&](B &g, B &x, int r) __attribute__((always_inline)) {
+      const int h = head(r), heads = pick(r < R.q, s.nq, s.nk);
+      g.load(pick(r < R.q, dQ, pick(r < R.q + R.k, dK, dV)), (m * heads + h) * s.d, un, h < heads);
+      x.load(Y, row_at(r, h), un, norm && r < R.q + R.k && h < heads);
+    };
+    B next_g, next_x;
+    load(next_g, next_x, first);
     float co[V], si[V];
     angles<V>(positions[m], inv_freq, s, lane, u, un.turns, lds[wave], co, si);
-    const int h1 = min(heads, (part + 1) * s.per * heads_per);
-    for (int h = part * s.per * heads_per + sub; h < h1; h += heads_per) {
-      const bool is_q = h < s.nq, is_v = h >= s.nq + s.nk;
-      const void *src = is_q ? dQ : is_v ? dV : dK;
-      const int64_t from = is_q ? (m * s.nq + h) * s.d : (m * s.nk + (h - s.nq - (is_v ? s.nk : 0))) * s.d;
-      const int64_t at = m * s.row + static_cast<int64_t>(h) * s.d;
-      float g[2 * V];
+    // one round of q or k heads; the gradients of w are summed in dw
+    auto round = [&](B &g, const B &x, const B &weight, float *dw) __attribute__((always_inline)) {
+      float v[2 * V];
+      g.values(v);
+      turn<V, INTER>(v, co, si, -1.0f);
+      if (norm) {
+        float xv[2 * V], w[2 * V], sq = 0.0f, gx = 0.0f;
+        x.values(xv);
+        weight.values(w);
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) g[e] = 0.0f;
-      if (un.has0) load_values<T16, V>(src, from + un.o0, g);
-      if (un.has1) load_values<T16, V>(src, from + un.o1, g + V);
-      if (!is_v) {
-        turn<V, INTER>(g, co, si, -1.0f);
-        if (norm) {
-          float x[2 * V];
+        for (int e = 0; e < 2 * V; ++e) {
+          sq = __builtin_fmaf(xv[e], xv[e], sq);
+          gx = __builtin_fmaf(v[e] * w[e], xv[e], gx);
+        }
+        sq = lanes_sum(sq, s.lanes);
+        gx = lanes_sum(gx, s.lanes);
+        const float r = inverse_rms(sq, s), back = r * r * (gx * s.inv_d);
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) x[e] = 0.0f;
-          if (un.has0) load_values<T16, V>(Y, at + un.o0, x);
-          if (un.has1) load_values<T16, V>(Y, at + un.o1, x + V);
-          float sq = 0.0f, gx = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            sq = __builtin_fmaf(x[e], x[e], sq);
-            gx = __builtin_fmaf(g[e] * (is_q ? wq[e] : wk[e]), x[e], gx);
-          }
-          sq = lanes_sum(sq, s.lanes);
-          gx = lanes_sum(gx, s.lanes);
-          const float r = 1.0f / sqrtf(sq * s.inv_d + s.eps);
-          const float back = r * (gx * s.inv_d);
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            const float xh = x[e] * r, d = g[e] * xh;
-            dwq[e] += is_q ? d : 0.0f;
-            dwk[e] += is_q ? 0.0f : d;
-            g[e] = r * (g[e] * (is_q ? wq[e] : wk[e]) - xh * back);
-          }
+        for (int e = 0; e < 2 * V; ++e) {
+          dw[e] = __builtin_fmaf(v[e] * r, xv[e], dw[e]);
+          v[e] = r * (v[e] * w[e] - xv[e] * back);
         }
       }
-      if (un.has0) store_values<T16, V>(dY, at + un.o0, g);
-      if (un.has1) store_values<T16, V>(dY, at + un.o1, g + V);
+      g.set(v);
+    };
+    for (int r = first; r < last; ++r) {
+      B g = next_g, x = next_x;
+      if (r + 1 < last) load(next_g, next_x, r + 1);
+      if (r < R.q)
+        round(g, x, wq, dwq);
+      else if (r < R.q + R.k)
+        round(g, x, wk, dwk);
+      const int h = head(r);
+      if (h < pick(r < R.q, s.nq, s.nk)) g.store(dY, row_at(r, h), un);
     }
   }
   if (!norm) return;
 
   // the wave's sums over its heads, then the workgroup's over its waves, in a fixed order
-  __shared__ float dw[kWaves][2][kQkMaxDim];
+  __shared__ __attribute__((aligned(16))) float dw[kBwdWaves][2][kQkMaxDim];
 #pragma unroll
   for (int e = 0; e < 2 * V; ++e) {
-    for (int m = s.lanes; m < 64; m <<= 1) {
-      dwq[e] += __shfl_xor(dwq[e], m, 64);
-      dwk[e] += __shfl_xor(dwk[e], m, 64);
-    }
+    dwq[e] = heads_sum(dwq[e], s.lanes);
+    dwk[e] = heads_sum(dwk[e], s.lanes);
     const int o = e < V ? un.o0 + e : un.o1 + e - V;
     if (lane < s.lanes && (e < V ? un.has0 : un.has1)) dw[wave][0][o] = dwq[e], dw[wave][1][o] = dwk[e];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * s.d; i += kThreads) {
-    const int which = i >= s.d, o = which ? i - s.d : i;
-    float v = dw[0][which][o];
-#pragma unroll
-    for (int k = 1; k < kWaves; ++k) v += dw[k][which][o];
-    part_dw[static_cast<int64_t>(blockIdx.x) * 2 * s.d + i] = v;
+  // The workgroup's sums, four columns a thread; agent-coherent (SC1: the L2 of one XCD is not
+  // coherent with the others).
+  const int cols = 2 * s.d, quads = cols / 4;
+  const __amdgpu_buffer_rsrc_t P = make_rsrc(part, gridDim.x * cols * 4u);
+  if (threadIdx.x < quads) {
+    const int i = 4 * threadIdx.x, which = i >= s.d, o = which ? i - s.d : i;
+    f32x4_t v = *reinterpret_cast<const f32x4_t *>(&dw[0][which][o]);
+    for (int k = 1; k < kBwdWaves; ++k) v += *reinterpret_cast<const f32x4_t *>(&dw[k][which][o]);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (blockIdx.x * cols + i) * 4u, 0, kSC1);
   }
-}
-
-// The workgroups' partial sums [parts][2 d] added in a fixed order: 32 columns and 32 slices
-// of the parts to a workgroup, the slices' sums added in slice order.
-template <bool T16>
-__global__ __launch_bounds__(1024) void qk_dw_kernel(const float *__restrict__ P, int parts, int d,
-                                                     void *__restrict__ dqw, void *__restrict__ dkw) {
-  __shared__ float sums[32][33];
-  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5, i = blockIdx.x * 32 + col;
-  float v = 0.0f;
-  if (i < 2 * d)
-    for (int k = slice; k < parts; k += 32) v += P[static_cast<int64_t>(k) * 2 * d + i];
-  sums[slice][col] = v;
+  // The last workgroup to leave its sums adds them all.  They have completed before the ticket is
+  // taken, so whoever sees the last ticket sees them.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (slice != 0 || i >= 2 * d) return;
-  for (int k = 1; k < 32; ++k) v += sums[k][col];
-  void *out = i < d ? dqw : dkw;
-  const int o = i < d ? i : i - d;
+  __shared__ uint32_t taken;
+  if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (taken != gridDim.x - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // a thread takes four columns of every slices-th workgroup, the slices are added in their order
+  float *sums = &dw[0][0][0];
+  const int slices = kBwdThreads / quads, slice = threadIdx.x / quads, col = 4 * (threadIdx.x - slice * quads);
+  const int parts = static_cast<int>(gridDim.x);
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (slice < slices) {
+    for (int k = slice; k < parts; k += kInFlight * slices) {
+      u32x4_t t[kInFlight];
+#pragma unroll
+      for (int e = 0; e < kInFlight; ++e) {
+        const int row = k + e * slices;  // past the last: zeros
+        t[e] = __builtin_amdgcn_raw_buffer_load_b128(P, row < parts ? (row * cols + col) * 4u : kOOB, 0, kSC1);
+      }
+#pragma unroll
+      for (int e = 0; e < kInFlight; ++e) v += __builtin_bit_cast(f32x4_t, t[e]);
+    }
+    *reinterpret_cast<f32x4_t *>(sums + slice * cols + col) = v;
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= cols) return;
+  float w = sums[c];
+  for (int k = 1; k < slices; ++k) w += sums[k * cols + c];
+  void *out = pick(c < s.d, dqw, dkw);
+  const int o = c < s.d ? c : c - s.d;
   if constexpr (T16)
-    static_cast<uint16_t *>(out)[o] = to_bf16(v);
+    static_cast<uint16_t *>(out)[o] = to_bf16(w);
   else
-    static_cast<float *>(out)[o] = v;
+    static_cast<float *>(out)[o] = w;
 }
 
-// Elements of a lane's chunk: the widest access (16 bytes) that divides the head and half the
-// rotated part.
-int chunk_of(const QkShape &s, bool t16) {
-  int v = t16 ? 8 : 4;
+// Elements of a lane's chunk: the widest access that divides the head and half the rotated part, of
+// up to 16 bytes.  The backward stops at 8 bytes (4 of bf16): with 16 a lane holds twice the values and
+// half as many waves fit (2048 tokens of 64 + 64 + 64 heads of 128: 50.5 us with 8 bytes, 59.4 with
+// 16; forward 28.0 and 24.5).
+int chunk_of(const QkShape &s, bool t16, int most) {
+  int v = t16 ? most : 4;
   while (v > 2 && (s.d % v != 0 || s.rot % (2 * v) != 0)) v /= 2;
   return v;
 }
 
-// Lanes of a head, and how a token's heads are split over waves: all of them to one wave (one
-// computation of the angles) unless the tokens are too few for the card.
-constexpr int64_t kWantedWaves = 256 * 16;
-void plan(QkShape *s, int v, int heads) {
+// Lanes of a head, and how a token's rounds are split over waves: enough of them to fill the card
+// (eight a SIMD forward, four backward, where a wave holds more), and no more, since each
+// computes the token's angles.
+constexpr int64_t kFwdWaves = 1024 * 8, kBwdAllWaves = 1024 * 4;
+void plan(QkShape *s, int v, bool with_v) {
   const int units = (s->d + 2 * v - 1) / (2 * v);
   s->lanes = 1;
   while (s->lanes < units) s->lanes *= 2;
-  const int heads_per = 64 / s->lanes, rounds = (heads + heads_per - 1) / heads_per;
-  int64_t split = (kWantedWaves + s->M - 1) / s->M;
+  const int heads_per = 64 / s->lanes;
+  const int rounds = (s->nq + heads_per - 1) / heads_per + (with_v ? 2 : 1) * ((s->nk + heads_per - 1) / heads_per);
+  int64_t split = ((with_v ? kBwdAllWaves : kFwdWaves) + s->M - 1) / s->M;
   if (split > rounds) split = rounds;
   s->per = static_cast<int>((rounds + split - 1) / split);
   s->split = (rounds + s->per - 1) / s->per;
   s->row = static_cast<int64_t>(s->nq + 2 * s->nk) * s->d;
   s->inv_d = 1.0f / static_cast<float>(s->d);
 }
-int64_t workgroups(const QkShape &s, int64_t most) {
-  const int64_t wgs = (s.M * s.split + kWaves - 1) / kWaves;
+int64_t workgroups(const QkShape &s, int waves, int64_t most) {
+  const int64_t wgs = (s.M * s.split + waves - 1) / waves;
   return wgs < most ? wgs : most;
 }
-constexpr int64_t kFwdWorkgroups = 256 * 8, kBwdWorkgroups = 256 * 4;
+// The backward's workgroups each leave partial sums, so no more than are on the card at once.
+constexpr int64_t kFwdWorkgroups = 256 * 16, kBwdWorkgroups = 256;
 
 }  // namespace
 
 size_t qk_bwd_workspace(QkShape s, bool t16, bool norm) {
   if (!norm) return 0;
-  plan(&s, chunk_of(s, t16), s.nq + 2 * s.nk);
-  return static_cast<size_t>(workgroups(s, kBwdWorkgroups)) * 2 * s.d * sizeof(float);
+  plan(&s, chunk_of(s, t16, 4), true);
+  return static_cast<size_t>(workgroups(s, kBwdWaves, kBwdWorkgroups)) * 2 * s.d * sizeof(float);
 }
 
 hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
                          const float *inv_freq, const void *qw, const void *kw, void *Q, void *K,
                          hipStream_t stream) {
-  const int v = chunk_of(s, t16);
-  plan(&s, v, s.nq + s.nk);
-  const dim3 grid(static_cast<unsigned>(workgroups(s, kFwdWorkgroups))), block(kThreads);
+  const int v = chunk_of(s, t16, 8);
+  plan(&s, v, false);
+  const dim3 grid(static_cast<unsigned>(workgroups(s, kWaves, kFwdWorkgroups))), block(kThreads);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, Y, s, positions, inv_freq, qw, kw, Q, K);
     return hipGetLastError();
@@ -368,35 +489,26 @@ hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, c
 
 hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const void *Y, QkShape s, bool t16,
                          bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
-                         const void *kw, void *dY, void *dqw, void *dkw, float *part, hipStream_t stream) {
-  const int v = chunk_of(s, t16);
-  plan(&s, v, s.nq + 2 * s.nk);
-  const int64_t wgs = workgroups(s, kBwdWorkgroups);
-  const dim3 grid(static_cast<unsigned>(wgs)), block(kThreads);
+                         const void *kw, void *dY, void *dqw, void *dkw, float *part, uint32_t *ticket,
+                         hipStream_t stream) {
+  const int v = chunk_of(s, t16, 4);
+  plan(&s, v, true);
+  const dim3 grid(static_cast<unsigned>(workgroups(s, kBwdWaves, kBwdWorkgroups))), block(kBwdThreads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, dQ, dK, dV, Y, s, positions, inv_freq, qw, kw, dY, part);
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, dQ, dK, dV, Y, s, positions, inv_freq, qw, kw, dY, dqw, dkw,
+                       part, ticket);
     return hipGetLastError();
   };
-  hipError_t e;
   switch ((t16 ? 100 : 0) + 10 * v + (interleaved ? 1 : 0)) {
-    case 180: e = go(qk_bwd_kernel<true, 8, false>); break;
-    case 181: e = go(qk_bwd_kernel<true, 8, true>); break;
-    case 140: e = go(qk_bwd_kernel<true, 4, false>); break;
-    case 141: e = go(qk_bwd_kernel<true, 4, true>); break;
-    case 120: e = go(qk_bwd_kernel<true, 2, false>); break;
-    case 121: e = go(qk_bwd_kernel<true, 2, true>); break;
-    case 40: e = go(qk_bwd_kernel<false, 4, false>); break;
-    case 41: e = go(qk_bwd_kernel<false, 4, true>); break;
-    case 20: e = go(qk_bwd_kernel<false, 2, false>); break;
-    default: e = go(qk_bwd_kernel<false, 2, true>); break;
+    case 140: return go(qk_bwd_kernel<true, 4, false>);
+    case 141: return go(qk_bwd_kernel<true, 4, true>);
+    case 120: return go(qk_bwd_kernel<true, 2, false>);
+    case 121: return go(qk_bwd_kernel<true, 2, true>);
+    case 40: return go(qk_bwd_kernel<false, 4, false>);
+    case 41: return go(qk_bwd_kernel<false, 4, true>);
+    case 20: return go(qk_bwd_kernel<false, 2, false>);
+    default: return go(qk_bwd_kernel<false, 2, true>);
   }
-  if (e != hipSuccess || !qw) return e;
-  const dim3 dgrid(static_cast<unsigned>((2 * s.d + 31) / 32));
-  if (t16)
-    hipLaunchKernelGGL(qk_dw_kernel<true>, dgrid, dim3(1024), 0, stream, part, static_cast<int>(wgs), s.d, dqw, dkw);
-  else
-    hipLaunchKernelGGL(qk_dw_kernel<false>, dgrid, dim3(1024), 0, stream, part, static_cast<int>(wgs), s.d, dqw, dkw);
-  return hipGetLastError();
 }
 
 }  // namespace qlora

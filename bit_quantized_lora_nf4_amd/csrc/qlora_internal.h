@@ -312,10 +312,12 @@ struct QkShape {
 // t16: bf16 tensors, else fp32; qw, kw NULL: no norm (Y is not read then by the backward).
 hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
                          const float *inv_freq, const void *qw, const void *kw, void *Q, void *K, hipStream_t stream);
-// `part`: qk_bwd_workspace bytes of partial sums of dqw and dkw (norm only).
+// Norm only: `part`, qk_bwd_workspace bytes of partial sums of dqw and dkw, and `ticket`, a word that
+// is zero when the call starts and when it has run.
 size_t qk_bwd_workspace(QkShape s, bool t16, bool norm);
 hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const void *Y, QkShape s, bool t16,
                          bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
-                         const void *kw, void *dY, void *dqw, void *dkw, float *part, hipStream_t stream);
+                         const void *kw, void *dY, void *dqw, void *dkw, float *part, uint32_t *ticket,
+                         hipStream_t stream);
 
 }  // namespace qlora

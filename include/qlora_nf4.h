@@ -24,7 +24,7 @@
  *     fixed scratch array of the library instead).
  *   - Workspaces: the first QLORA_WORKSPACE_HEADER_BYTES bytes of every
  *     workspace hold counters and flags that the small-M forward's workgroups
- *     use to hand U_s to each other.  They must be zero when a workspace is
+ *     use to hand U_s to each other, and the ticket of qlora_qk_bwd.  They must be zero when a workspace is
  *     first used (clear it once after allocating); every call leaves them
  *     zero, and no other call writes them, so one workspace can serve calls of
  *     any shape.  Calls that share a workspace must not overlap.  Launches of
