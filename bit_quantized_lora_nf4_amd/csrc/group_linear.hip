@@ -65,6 +65,13 @@ __device__ __forceinline__ uint32_t from_lane_group(uint32_t v, int q) {
   return o[q & 1];
 }
 
+// Waits until at most N of the wave's loads are on their way (they complete in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the counter has six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // What a wave holds.  XR: tokens kept in LDS (a power of two; MT tiles of 16 of them).  FS:
 // columns between two uses of a scale, the largest of 32, 64 and 128 that divides the group.
 // VS: a block's scales of a row are one aligned load.
@@ -90,7 +97,7 @@ struct Product {
   __amdgpu_buffer_rsrc_t codes, scales, zeros, X;
   bool zp;  // zeros are given (else 8 everywhere)
   uint32_t lane, row_bytes, row_groups, x_bytes, per, magic, n_steps;
-  char *xs;  // the wave's LDS: [4][XR][256] bytes (few tokens) or [XR][128]
+  char *xs;  // the wave's LDS, [4][XR][256] bytes (few tokens)
   f32x4_t y[MT][NT];
 
   __device__ __forceinline__ void init(const GroupView &w, int64_t n0, const uint16_t *x, uint32_t tokens,
@@ -161,32 +168,26 @@ struct Product {
 #pragma unroll
     for (int m = 0; m < kXLoads; ++m) b.x[m] = buf_load16(X, o < x_bytes ? m * x_bytes + o : kOOB);
   }
-  __device__ __forceinline__ void load_half(Xs &b, uint32_t half) const {
-    const uint32_t o = half * 128 + 16 * (lane % 8);
+  __device__ __forceinline__ void load_half(char *to, uint32_t half) const {
+    const uint32_t o = half * 128 + 16 * ((lane % 8) ^ (lane / 8));
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      b.x[i] = buf_load16(X, o < x_bytes ? (8 * i + lane / 8) * x_bytes + o : kOOB);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(X, (__attribute__((address_space(3))) void *)(to + 1024 * i), 16,
+                                               o < x_bytes ? (8 * i + lane / 8) * x_bytes + o : kOOB, 0, 0, 0);
   }
   __device__ __forceinline__ void stage_round(const Xs &b) const {
 #pragma unroll
     for (int m = 0; m < kXLoads; ++m)
       *reinterpret_cast<u32x4_t *>(xs + ((lane / 16) * XR + m) * 256 + 16 * ((lane % 16) ^ m)) = code_order(b.x[m]);
   }
-  __device__ __forceinline__ void stage_half(const Xs &b) const {
-#pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const uint32_t m = 8 * i + lane / 8;
-      *reinterpret_cast<u32x4_t *>(xs + m * 128 + 16 * ((lane % 8) ^ (m % 8))) = code_order(b.x[i]);
-    }
-  }
   // Fragments of a round's block q (few tokens) and of the half block in LDS.
   __device__ __forceinline__ u32x4_t frag_round(int q, int j) const {
     const uint32_t m = (lane % 16) % XR;
     return *reinterpret_cast<const u32x4_t *>(xs + (q * XR + m) * 256 + 16 * ((4 * j + lane / 16) ^ m));
   }
-  __device__ __forceinline__ u32x4_t frag_half(int m, int j) const {
+  __device__ __forceinline__ u32x4_t frag_half(const char *from, int m, int j) const {
     const uint32_t r = lane % 16;
-    return *reinterpret_cast<const u32x4_t *>(xs + (16 * m + r) * 128 + 16 * ((4 * (j & 1) + lane / 16) ^ (r % 8)));
+    return *reinterpret_cast<const u32x4_t *>(from + (16 * m + r) * 128 + 16 * ((4 * (j & 1) + lane / 16) ^ (r % 8)));
   }
 
   // Scales and zeros of a block as every lane knows them.
@@ -220,6 +221,11 @@ struct Product {
   template <bool EXACT, int J0, int J1, typename FRAG>
   __device__ __forceinline__ void multiply(Sums &a, const Codes &c, const Known &v, uint32_t block, FRAG frag) {
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    u32x4_t x[J1 - J0][MT];
+#pragma unroll
+    for (int j = J0; j < J1; ++j)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) x[j - J0][m] = frag(m, j);
 #pragma unroll
     for (int j = J0; j < J1; ++j) {
       if (4 * block + j >= n_steps) break;
@@ -240,10 +246,10 @@ struct Product {
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const u32x4_t x = frag(m, j);
-        if constexpr (!EXACT) a.sum[m] = mfma16x16x32(x, ones, a.sum[m]);
+        const u32x4_t f = XR < 16 ? x[j - J0][m] : code_order(x[j - J0][m]);  // (few: stored in this order)
+        if constexpr (!EXACT) a.sum[m] = mfma16x16x32(f, ones, a.sum[m]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) a.acc[m][t] = mfma16x16x32(x, w[t], a.acc[m][t]);
+        for (int t = 0; t < NT; ++t) a.acc[m][t] = mfma16x16x32(f, w[t], a.acc[m][t]);
       }
       if ((j + 1) % (kFlush / 32) == 0) {
 #pragma unroll
@@ -282,10 +288,13 @@ struct Product {
     return v == 0.0f;
   }
 
-  // The waves' sums added in wave order through `part`, [wave][m tile][t][token][row], and stored.
-  __device__ __forceinline__ void finish(float *part, uint32_t wave, uint32_t waves, uint32_t tokens, uint32_t rows,
-                                         uint16_t *Y, int64_t ldy) const {
+  // The waves' sums added in wave order through LDS, [wave][m tile][t][token][row] (the waves
+  // from `half` on in `part1`), and stored.
+  __device__ __forceinline__ void finish(float *part0, float *part1, uint32_t half, uint32_t wave, uint32_t waves,
+                                         uint32_t tokens, uint32_t rows, uint16_t *Y, int64_t ldy) const {
     constexpr uint32_t kTok = XR < 16 ? XR : 16, kPart = MT * NT * kTok * 16;
+    auto part = [&](uint32_t k) { return k < half ? part0 + k * kPart : part1 + (k - half) * kPart; };
+    float *mine = part(wave);
     __syncthreads();  // the waves' X pieces are read
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -294,14 +303,14 @@ struct Product {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t tok = 4 * (lane / 16) + i;
-          if (tok < kTok) part[wave * kPart + ((m * NT + t) * kTok + tok) * 16 + lane % 16] = y[m][t][i];
+          if (tok < kTok) mine[((m * NT + t) * kTok + tok) * 16 + lane % 16] = y[m][t][i];
         }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < kPart; e += blockDim.x) {
       const uint32_t mt = e / (16 * kTok), m = 16 * (mt / NT) + (e / 16) % kTok, n = 16 * (mt % NT) + e % 16;
       if (m >= tokens || n >= rows) continue;
-      float v = part[e];
-      for (uint32_t k = 1; k < waves; ++k) v += part[k * kPart + e];
+      float v = part0[e];
+      for (uint32_t k = 1; k < waves; ++k) v += part(k)[e];
       Y[m * ldy + n] = to_bf16(v);
     }
   }
@@ -346,54 +355,65 @@ __global__ __launch_bounds__(64 * W) void group_few_kernel(GroupView w, const ui
     T.clear();
     rounds(std::true_type());
   }
-  T.finish(reinterpret_cast<float *>(lds), wave, waves, M, static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT))),
-           Y + n0, w.n_rows);
+  float *part = reinterpret_cast<float *>(lds);
+  T.finish(part, part, 64, wave, waves, M, static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT))), Y + n0,
+           w.n_rows);
 }
 
-// More tokens, XR of them a workgroup: half a block of X and a block of codes in flight while the
-// one before is multiplied.
+// More tokens, XR of them a workgroup.  X goes straight from memory to LDS, half a block to each of
+// two stages of the wave's own, and a stage is asked for again as soon as it is multiplied; the
+// next block of codes is in flight while one is multiplied.  The stages are separate objects, so that
+// the waits the compiler puts before one's reads leave the other's loads in flight.  (Four
+// stages: 32 us instead of 28.5 at 16 x 8192 -> 22016, fewer workgroups fit.)
 template <int XR, int NT, int W, int FS, bool S16, bool VS>
 __global__ __launch_bounds__(64 * W) void group_many_kernel(GroupView w, const uint16_t *__restrict__ X, int64_t M,
                                                             uint32_t magic, uint16_t *__restrict__ Y) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using P = Product<XR, NT, FS, S16, VS>;
+  static_assert(P::MT * NT * 1024 * ((W + 1) / 2) <= W * XR * 128, "partial sums of half the waves fit a stage");
+  __shared__ __attribute__((aligned(16))) char x0[W * XR * 128];
+  __shared__ __attribute__((aligned(16))) char x1[W * XR * 128];
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT), m0 = static_cast<int64_t>(blockIdx.y) * XR;
   const uint32_t tokens = static_cast<uint32_t>(min(M - m0, int64_t(XR)));
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  using P = Product<XR, NT, FS, S16, VS>;
   P T;
   T.init(w, n0, X + m0 * w.n_cols, tokens, magic);
-  T.xs = lds + wave * (XR * 128);
   T.clear();
   auto rounds = [&](auto exact) {
-    typename P::Xs x;
     typename P::Scales s, s2;
     typename P::Codes c, c2;
     typename P::Sums a;
-    auto frag = [&](int m, int j) { return T.frag_half(m, j); };
+    char *const stage[2] = {x0 + wave * (XR * 128), x1 + wave * (XR * 128)};
     T.load_scales(s, wave);
-    T.load_half(x, 8 * wave);
     T.load_codes(c, 4 * wave);
+    T.load_half(stage[0], 8 * wave);
+    T.load_half(stage[1], 8 * wave + 1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma nounroll
     for (uint32_t k = wave; 16 * k < T.n_steps; k += waves) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t block = 4 * k + q, next = q < 3 ? block + 1 : 4 * (k + waves);
-        T.stage_half(x);
-        __builtin_amdgcn_sched_barrier(0);
-        T.load_half(x, 2 * block + 1);
         T.load_codes(c2, next);
         if (q == 3) T.load_scales(s2, k + waves);
         __builtin_amdgcn_sched_barrier(0);
         const typename P::Known v = T.known(s, q);
         T.transpose(c);
-        T.template multiply<decltype(exact)::value, 0, 2>(a, c, v, block, frag);
-        __builtin_amdgcn_sched_barrier(0);
-        T.stage_half(x);
-        __builtin_amdgcn_sched_barrier(0);
-        T.load_half(x, 2 * next);
-        __builtin_amdgcn_sched_barrier(0);
-        T.template multiply<decltype(exact)::value, 2, 4>(a, c, v, block, frag);
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          auto frag = [&](int m, int j) { return T.frag_half(stage[h], m, j); };
+          // The stage's loads have landed when only what was asked for after them is on its way: the
+          // other stage's and the next block's codes.  (The waits that the compiler derives are not
+          // enough: it takes a direct load for a store of one lane's 16 bytes.)
+          wait_loads<P::kXLoads + NT>();
+          if (h == 0)
+            T.template multiply<decltype(exact)::value, 0, 2>(a, c, v, block, frag);
+          else
+            T.template multiply<decltype(exact)::value, 2, 4>(a, c, v, block, frag);
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is read
+          T.load_half(stage[h], 2 * next + h);
+          __builtin_amdgcn_sched_barrier(0);
+        }
         c = c2;
       }
       s = s2;
@@ -404,10 +424,13 @@ __global__ __launch_bounds__(64 * W) void group_many_kernel(GroupView w, const u
     T.clear();
     rounds(std::true_type());
   }
-  T.finish(reinterpret_cast<float *>(lds), wave, waves, tokens,
+  // the loads asked for past the last round write zeros to the stages, which become the sums' place
+  wait_loads<0>();
+  T.finish(reinterpret_cast<float *>(x0), reinterpret_cast<float *>(x1), W / 2, wave, waves, tokens,
            static_cast<uint32_t>(min(w.n_rows - n0, int64_t(16 * NT))), Y + m0 * w.n_rows + n0, w.n_rows);
 }
 
+// FEW: group_few_kernel, else group_many_kernel.
 template <bool FEW, int XR, int NT, int W>
 hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   const int64_t gx = (w.n_rows + 16 * NT - 1) / (16 * NT), gy = (M + XR - 1) / XR;
@@ -416,8 +439,7 @@ hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hip
   const int64_t rounds = (w.n_cols + 511) / 512, each = (rounds + W - 1) / W;
   const int waves = static_cast<int>((rounds + each - 1) / each);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * waves);
-  const size_t xs = FEW ? XR * 1024 : XR * 128, part = ((XR + 15) / 16) * NT * (XR < 16 ? XR : 16) * 64;
-  const size_t lds = static_cast<size_t>(waves) * (xs > part ? xs : part);
+  const size_t lds = FEW ? static_cast<size_t>(waves) * XR * 1024 : 0;  // (at least the partial sums)
   const uint32_t magic = group_magic(static_cast<uint32_t>(w.group / 32));
   auto launch = [&](auto kernel) {
     if (lds > 64 * 1024) {
@@ -457,9 +479,12 @@ hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hip
 
 }  // namespace
 
-// Up to 8 tokens the whole of a wave's round is in flight (1024-column rows: 1 token 7.8 us, 4
-// tokens of 12288 rows 9.0 us); more are multiplied by tiles of 16, 32 or 64 tokens.  The height of
-// a workgroup's tile is the one that leaves the fewest rows to the busiest CU.
+// Up to 8 tokens a wave has the whole of its round in flight; more are multiplied in tiles of 16, 32 or
+// 64 tokens.  There the height of a workgroup's tile is the least that leaves a CU one workgroup, so
+// that all run at once, up to 48 rows (registers): X is read once for each workgroup.  In us, a launch in
+// a graph: 16 x 8192 -> 22016 36.1, 32.2, 28.5 with 16, 32, 48 rows (43.0, 35.7, 32.8 with twice the
+// waves); 16 x 8192 -> 8192 14.3, 12.8, 15.1; 8 x 8192 -> 1024 7.7, 10.8, 14.7 (few tokens: 7.1);
+// 32 x 4096 -> 11008 23.4 and 13.2 with 32 and 48; 64 tokens 26.2 and 19.3.
 hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   if (M == 1) return go<true, 1, 1, 16>(w, X, M, Y, stream);
   if (M <= 4) return go<true, 4, 1, 16>(w, X, M, Y, stream);
@@ -467,7 +492,7 @@ hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M,
   const int64_t tiles = (w.n_rows + 15) / 16;
   if (M <= 16) {
     if (tiles <= 256) return go<false, 16, 1, 16>(w, X, M, Y, stream);
-    if (tiles <= 512) return go<false, 16, 2, 16>(w, X, M, Y, stream);
+    if (tiles <= 512) return go<false, 16, 2, 8>(w, X, M, Y, stream);
     return go<false, 16, 3, 8>(w, X, M, Y, stream);
   }
   if (M <= 32) {
