@@ -788,15 +788,16 @@ def group_quantize(W, group=128, zeros=False, scale_dtype=None):
     st = _type_of(torch.bfloat16 if scale_dtype is None else scale_dtype, "scale_dtype")
     if W.dim() != 2:
         raise ValueError(f"W must be 2-D, got shape {tuple(W.shape)}")
-    _meta(W, W.dtype, "W")
     N, K = W.shape
     _check_groups(N, K, group)
-    _on(W, "W")
-    dev = W.device
-    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=dev)
-    scales = torch.empty((N, K // group), dtype=torch.bfloat16 if st == QLORA_BF16 else torch.float32, device=dev)
-    z = torch.empty((N, K // group), dtype=torch.uint8, device=dev) if zeros else None
-    _run("qlora_group_quantize", qlora_group_quantize, W.get_device(), W.data_ptr(), wt, N, K, group, st,
+    i = W.get_device()
+    if i < 0 or not W.is_contiguous():
+        _need(W, W.dtype, "W")
+    new, u8, shape = W.new_empty, torch.uint8, (N, K // group)
+    codes = new((N * K // 2,), dtype=u8)
+    scales = new(shape, dtype=torch.bfloat16 if st == QLORA_BF16 else torch.float32)
+    z = new(shape, dtype=u8) if zeros else None
+    _run("qlora_group_quantize", qlora_group_quantize, i, W.data_ptr(), wt, N, K, group, st,
          codes.data_ptr(), scales.data_ptr(), _ptr(z))
     return GroupWeight(codes, scales, z, N, K, group)
 
@@ -806,14 +807,15 @@ def group_dequantize(gw, dtype=None, out=None):
     torch = _torch()
     dtype = dtype or torch.bfloat16
     ot = _type_of(dtype, "dtype")
-    chk = gw.checked()
-    if out is not None:
-        chk.need(out, dtype, "out", gw.shape)
-    chk.devices()
-    dev = chk.device
+    i = gw.codes.get_device() if isinstance(gw.codes, torch.Tensor) else -1
+    if not (gw.fits(i) and (out is None or _fits(out, dtype, gw.shape, i))):
+        chk = gw.checked()
+        if out is not None:
+            chk.need(out, dtype, "out", gw.shape)
+        chk.devices()
     if out is None:
-        out = torch.empty(gw.shape, dtype=dtype, device=dev)
-    _run("qlora_group_dequantize", qlora_group_dequantize, out.get_device(), gw.descriptor(), out.data_ptr(), ot)
+        out = gw.codes.new_empty(gw.shape, dtype=dtype)
+    _run("qlora_group_dequantize", qlora_group_dequantize, i, gw.descriptor(), out.data_ptr(), ot)
     return out
 
 
@@ -962,7 +964,7 @@ def qk_norm_rope_bwd(dQ, dK, dV, positions, inv_freq, Y=None, q_weight=None, k_w
         nbytes = qlora_workspace_bytes_qk(shape, 1)
         if ws is None:
             ws = _scratch(nbytes, dev)
-        else:
+        elif not (isinstance(ws, torch.Tensor) and ws.numel() >= nbytes and _fits(ws, torch.uint8, ws.shape, i)):
             chk = _Args(dev)
             chk.workspace(ws, nbytes)
             chk.devices()

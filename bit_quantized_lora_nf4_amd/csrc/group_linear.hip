@@ -477,30 +477,54 @@ hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hip
   }
 }
 
+// Tiles of XR tokens and 16 NT rows for more than 8 tokens.  Below 256 workgroups, one to a CU, a
+// launch takes what its tile takes (in us at K = 8192, beside 3.5 of the launch itself: small
+// tiles are sooner done, each reads X for itself), above it as many times that as it has rounds
+// of 256.  58 tokens x 8064 -> 560: 8.4 us with the smallest tile, 26.4 with the largest; 64 x
+// 8192 -> 8192: 56.3 with the smallest, 23.2 with 64 x 32; 64 x 4096 -> 11008: 19.3 with the largest.
+struct TileCost {
+  int tokens, rows16;
+  double us;
+};
+constexpr TileCost kTiles[] = {{16, 1, 4.9}, {16, 2, 7.5}, {16, 3, 10.8}, {32, 2, 10.6},
+                               {32, 3, 14.9}, {64, 2, 17.2}, {64, 3, 22.9}};
+int best_tile(int64_t M, int64_t rows) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 7; ++i) {
+    const TileCost &t = kTiles[i];
+    const int64_t wgs = (rows + 16 * t.rows16 - 1) / (16 * t.rows16) * ((M + t.tokens - 1) / t.tokens);
+    const double us = t.us * static_cast<double>((wgs + 255) / 256);
+    if (i == 0 || us < least) best = i, least = us;
+  }
+  return best;
+}
+
+template <int XR>
+hipError_t few(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
+  if (w.n_rows >= 16 * 1024) return go<true, XR, 2, 8>(w, X, M, Y, stream);
+  return go<true, XR, 1, 16>(w, X, M, Y, stream);
+}
+
 }  // namespace
 
-// Up to 8 tokens a wave has the whole of its round in flight; more are multiplied in tiles of 16, 32 or
-// 64 tokens.  There the height of a workgroup's tile is the least that leaves a CU one workgroup, so
-// that all run at once, up to 48 rows (registers): X is read once for each workgroup.  In us, a launch in
-// a graph: 16 x 8192 -> 22016 36.1, 32.2, 28.5 with 16, 32, 48 rows (43.0, 35.7, 32.8 with twice the
-// waves); 16 x 8192 -> 8192 14.3, 12.8, 15.1; 8 x 8192 -> 1024 7.7, 10.8, 14.7 (few tokens: 7.1);
-// 32 x 4096 -> 11008 23.4 and 13.2 with 32 and 48; 64 tokens 26.2 and 19.3.
+// Up to 8 tokens a wave has the whole of its round in flight, with 16 rows a workgroup, or 32 where
+// they are so many that the card's CUs have several workgroups each all the same: 1, 4 and 8 tokens
+// x 8192 -> 22016 24.3, 26.2, 28.2 us with 32 rows, 27.4, 36.7, 42.9 with 16; 1 x 4096 -> 11008 8.7 and 7.8,
+// 8 x 11008 -> 4096 15.5 and 10.5.
 hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
-  if (M == 1) return go<true, 1, 1, 16>(w, X, M, Y, stream);
-  if (M <= 4) return go<true, 4, 1, 16>(w, X, M, Y, stream);
-  if (M <= 8) return go<true, 8, 1, 16>(w, X, M, Y, stream);
-  const int64_t tiles = (w.n_rows + 15) / 16;
-  if (M <= 16) {
-    if (tiles <= 256) return go<false, 16, 1, 16>(w, X, M, Y, stream);
-    if (tiles <= 512) return go<false, 16, 2, 8>(w, X, M, Y, stream);
-    return go<false, 16, 3, 8>(w, X, M, Y, stream);
+  if (M == 1) return few<1>(w, X, M, Y, stream);
+  if (M <= 4) return few<4>(w, X, M, Y, stream);
+  if (M <= 8) return few<8>(w, X, M, Y, stream);
+  switch (best_tile(M, w.n_rows)) {
+    case 0: return go<false, 16, 1, 16>(w, X, M, Y, stream);
+    case 1: return go<false, 16, 2, 8>(w, X, M, Y, stream);
+    case 2: return go<false, 16, 3, 8>(w, X, M, Y, stream);
+    case 3: return go<false, 32, 2, 8>(w, X, M, Y, stream);
+    case 4: return go<false, 32, 3, 8>(w, X, M, Y, stream);
+    case 5: return go<false, 64, 2, 8>(w, X, M, Y, stream);
+    default: return go<false, 64, 3, 8>(w, X, M, Y, stream);
   }
-  if (M <= 32) {
-    if (tiles <= 512) return go<false, 32, 2, 8>(w, X, M, Y, stream);
-    return go<false, 32, 3, 8>(w, X, M, Y, stream);
-  }
-  if (tiles <= 512) return go<false, 64, 2, 8>(w, X, M, Y, stream);
-  return go<false, 64, 3, 8>(w, X, M, Y, stream);
 }
 
 }  // namespace qlora

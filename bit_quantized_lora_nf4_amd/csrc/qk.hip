@@ -294,29 +294,31 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict
   }
 }
 
-template <bool T16, int V, bool INTER>
-__global__ __launch_bounds__(kBwdThreads) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
+// With a norm the waves of large workgroups sum the weights' gradients (few partial sums); without
+// one nothing is summed, and the kernel is the forward's with the other sign and the v heads.
+template <bool T16, int V, bool INTER, bool NORM>
+__global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
                                                           const void *__restrict__ dV, const void *__restrict__ Y,
                                                           QkShape s, const int64_t *__restrict__ positions,
                                                           const float *__restrict__ inv_freq,
                                                           const void *__restrict__ qw, const void *__restrict__ kw,
                                                           void *__restrict__ dY, void *__restrict__ dqw, void *__restrict__ dkw,
                                                           float *__restrict__ part, uint32_t *__restrict__ ticket) {
-  __shared__ float lds[kBwdWaves][2 * kMaxPairs];
+  constexpr int kW = NORM ? kBwdWaves : kWaves;
+  __shared__ float lds[kW][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int u = lane & (s.lanes - 1), sub = lane / s.lanes;
   const Unit un = unit_of<V, INTER>(u, s);
   const Rounds R(s, true);
-  const bool norm = qw != nullptr;
   using B = Both<T16, V>;
   B wq, wk;
-  wq.load(qw, 0, un, norm);
-  wk.load(kw, 0, un, norm);
+  wq.load(qw, 0, un, NORM);
+  wk.load(kw, 0, un, NORM);
   float dwq[2 * V], dwk[2 * V];
 #pragma unroll
   for (int e = 0; e < 2 * V; ++e) dwq[e] = dwk[e] = 0.0f;
-  const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kBwdWaves;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kBwdWaves + __builtin_amdgcn_readfirstlane(wave); task < tasks;
+  const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kW;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kW + __builtin_amdgcn_readfirstlane(wave); task < tasks;
        task += step) {
     const int64_t m = task / s.split;
     const int first = static_cast<int>(task - m * s.split) * s.per, last = min(first + s.per, R.total);
@@ -327,7 +329,7 @@ __global__ __launch_bounds__(kBwdThreads) void qk_bwd_kernel(const void *__restr
     auto load = [&](B &g, B &x, int r) __attribute__((always_inline)) {
       const int h = head(r), heads = pick(r < R.q, s.nq, s.nk);
       g.load(pick(r < R.q, dQ, pick(r < R.q + R.k, dK, dV)), (m * heads + h) * s.d, un, h < heads);
-      x.load(Y, row_at(r, h), un, norm && r < R.q + R.k && h < heads);
+      x.load(Y, row_at(r, h), un, NORM && r < R.q + R.k && h < heads);
     };
     B next_g, next_x;
     load(next_g, next_x, first);
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(kBwdThreads) void qk_bwd_kernel(const void *__restr
       float v[2 * V];
       g.values(v);
       turn<V, INTER>(v, co, si, -1.0f);
-      if (norm) {
+      if constexpr (NORM) {
         float xv[2 * V], w[2 * V], sq = 0.0f, gx = 0.0f;
         x.values(xv);
         weight.values(w);
@@ -369,89 +371,90 @@ __global__ __launch_bounds__(kBwdThreads) void qk_bwd_kernel(const void *__restr
       if (h < pick(r < R.q, s.nq, s.nk)) g.template store<false>(dY, row_at(r, h), un);
     }
   }
-  if (!norm) return;
+  if constexpr (NORM) {
 
-  // the wave's sums over its heads, then the workgroup's over its waves, in a fixed order
-  __shared__ __attribute__((aligned(16))) float dw[kBwdWaves][2][kQkMaxDim];
+    // the wave's sums over its heads, then the workgroup's over its waves, in a fixed order
+    __shared__ __attribute__((aligned(16))) float dw[kBwdWaves][2][kQkMaxDim];
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) {
-    dwq[e] = heads_sum(dwq[e], s.lanes);
-    dwk[e] = heads_sum(dwk[e], s.lanes);
-    const int o = e < V ? un.o0 + e : un.o1 + e - V;
-    if (lane < s.lanes && (e < V ? un.has0 : un.has1)) dw[wave][0][o] = dwq[e], dw[wave][1][o] = dwk[e];
-  }
-  __syncthreads();
-  // The workgroup's sums, four columns a thread; agent-coherent (SC1: the L2 of one XCD is not
-  // coherent with the others).
-  const int cols = 2 * s.d, quads = cols / 4;
-  const __amdgpu_buffer_rsrc_t P = make_rsrc(part, gridDim.x * cols * 4u);
-  if (threadIdx.x < quads) {
-    const int i = 4 * threadIdx.x, which = i >= s.d, o = which ? i - s.d : i;
-    f32x4_t v = *reinterpret_cast<const f32x4_t *>(&dw[0][which][o]);
-    for (int k = 1; k < kBwdWaves; ++k) v += *reinterpret_cast<const f32x4_t *>(&dw[k][which][o]);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (blockIdx.x * cols + i) * 4u, 0, kSC1);
-  }
-  // The last workgroup to leave its sums adds them all.  They have completed before the ticket is
-  // taken, so whoever sees the last ticket sees them.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  __shared__ uint32_t taken;
-  if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (taken != gridDim.x - 1) return;
-  if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  // a thread takes four columns of every slices-th workgroup, the slices are added in their order
-  float *sums = &dw[0][0][0];
-  const int slices = kBwdThreads / quads, slice = threadIdx.x / quads, col = 4 * (threadIdx.x - slice * quads);
-  const int parts = static_cast<int>(gridDim.x);
-  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (slice < slices) {
-    for (int k = slice; k < parts; k += kInFlight * slices) {
-      u32x4_t t[kInFlight];
-#pragma unroll
-      for (int e = 0; e < kInFlight; ++e) {
-        const int row = k + e * slices;  // past the last: zeros
-        t[e] = __builtin_amdgcn_raw_buffer_load_b128(P, row < parts ? (row * cols + col) * 4u : kOOB, 0, kSC1);
-      }
-#pragma unroll
-      for (int e = 0; e < kInFlight; ++e) v += __builtin_bit_cast(f32x4_t, t[e]);
+    for (int e = 0; e < 2 * V; ++e) {
+      dwq[e] = heads_sum(dwq[e], s.lanes);
+      dwk[e] = heads_sum(dwk[e], s.lanes);
+      const int o = e < V ? un.o0 + e : un.o1 + e - V;
+      if (lane < s.lanes && (e < V ? un.has0 : un.has1)) dw[wave][0][o] = dwq[e], dw[wave][1][o] = dwk[e];
     }
-    *reinterpret_cast<f32x4_t *>(sums + slice * cols + col) = v;
+    __syncthreads();
+    // The workgroup's sums, four columns a thread; agent-coherent (SC1: the L2 of one XCD is not
+    // coherent with the others).
+    const int cols = 2 * s.d, quads = cols / 4;
+    const __amdgpu_buffer_rsrc_t P = make_rsrc(part, gridDim.x * cols * 4u);
+    if (threadIdx.x < quads) {
+      const int i = 4 * threadIdx.x, which = i >= s.d, o = which ? i - s.d : i;
+      f32x4_t v = *reinterpret_cast<const f32x4_t *>(&dw[0][which][o]);
+      for (int k = 1; k < kBwdWaves; ++k) v += *reinterpret_cast<const f32x4_t *>(&dw[k][which][o]);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (blockIdx.x * cols + i) * 4u, 0, kSC1);
+    }
+    // The last workgroup to leave its sums adds them all.  They have completed before the ticket is
+    // taken, so whoever sees the last ticket sees them.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __shared__ uint32_t taken;
+    if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (taken != gridDim.x - 1) return;
+    if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // a thread takes four columns of every slices-th workgroup, the slices are added in their order
+    float *sums = &dw[0][0][0];
+    const int slices = kBwdThreads / quads, slice = threadIdx.x / quads, col = 4 * (threadIdx.x - slice * quads);
+    const int parts = static_cast<int>(gridDim.x);
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (slice < slices) {
+      for (int k = slice; k < parts; k += kInFlight * slices) {
+        u32x4_t t[kInFlight];
+#pragma unroll
+        for (int e = 0; e < kInFlight; ++e) {
+          const int row = k + e * slices;  // past the last: zeros
+          t[e] = __builtin_amdgcn_raw_buffer_load_b128(P, row < parts ? (row * cols + col) * 4u : kOOB, 0, kSC1);
+        }
+#pragma unroll
+        for (int e = 0; e < kInFlight; ++e) v += __builtin_bit_cast(f32x4_t, t[e]);
+      }
+      *reinterpret_cast<f32x4_t *>(sums + slice * cols + col) = v;
+    }
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= cols) return;
+    float w = sums[c];
+    for (int k = 1; k < slices; ++k) w += sums[k * cols + c];
+    void *out = pick(c < s.d, dqw, dkw);
+    const int o = c < s.d ? c : c - s.d;
+    if constexpr (T16)
+      static_cast<uint16_t *>(out)[o] = to_bf16(w);
+    else
+      static_cast<float *>(out)[o] = w;
   }
-  __syncthreads();
-  const int c = threadIdx.x;
-  if (c >= cols) return;
-  float w = sums[c];
-  for (int k = 1; k < slices; ++k) w += sums[k * cols + c];
-  void *out = pick(c < s.d, dqw, dkw);
-  const int o = c < s.d ? c : c - s.d;
-  if constexpr (T16)
-    static_cast<uint16_t *>(out)[o] = to_bf16(w);
-  else
-    static_cast<float *>(out)[o] = w;
 }
 
 // Elements of a lane's chunk: the widest access that divides the head and half the rotated part, of
-// up to 16 bytes.  The backward stops at 8 bytes (4 of bf16): with 16 a lane holds twice the values and
-// half as many waves fit (2048 tokens of 64 + 64 + 64 heads of 128: 50.5 us with 8 bytes, 59.4 with
+// up to 16 bytes.  The backward with a norm (sums) stops at 8 bytes (4 of bf16): with 16 a lane holds
+// twice the values and half as many waves fit (2048 tokens of 64 + 64 + 64 heads of 128: 50.5 us with 8 bytes, 59.4 with
 // 16; forward 28.0 and 24.5).
-int chunk_of(const QkShape &s, bool t16, int most) {
-  int v = t16 ? most : 4;
+int chunk_of(const QkShape &s, bool t16, bool sums) {
+  int v = t16 && !sums ? 8 : 4;
   while (v > 2 && (s.d % v != 0 || s.rot % (2 * v) != 0)) v /= 2;
   return v;
 }
 
 // Lanes of a head, and how a token's rounds are split over waves: enough of them to fill the card
-// (eight a SIMD forward, four backward, where a wave holds more), and no more, since each
+// (eight a SIMD, four of the backward with a norm, where a wave holds more), and no more, since each
 // computes the token's angles.
 constexpr int64_t kFwdWaves = 1024 * 8, kBwdAllWaves = 1024 * 4;
-void plan(QkShape *s, int v, bool with_v) {
+void plan(QkShape *s, int v, bool with_v, bool sums) {
   const int units = (s->d + 2 * v - 1) / (2 * v);
   s->lanes = 1;
   while (s->lanes < units) s->lanes *= 2;
   const int heads_per = 64 / s->lanes;
   const int rounds = (s->nq + heads_per - 1) / heads_per + (with_v ? 2 : 1) * ((s->nk + heads_per - 1) / heads_per);
-  int64_t split = ((with_v ? kBwdAllWaves : kFwdWaves) + s->M - 1) / s->M;
+  int64_t split = ((sums ? kBwdAllWaves : kFwdWaves) + s->M - 1) / s->M;
   if (split > rounds) split = rounds;
   s->per = static_cast<int>((rounds + split - 1) / split);
   s->split = (rounds + s->per - 1) / s->per;
@@ -469,15 +472,15 @@ constexpr int64_t kFwdWorkgroups = 256 * 16, kBwdWorkgroups = 256;
 
 size_t qk_bwd_workspace(QkShape s, bool t16, bool norm) {
   if (!norm) return 0;
-  plan(&s, chunk_of(s, t16, 4), true);
+  plan(&s, chunk_of(s, t16, true), true, true);
   return static_cast<size_t>(workgroups(s, kBwdWaves, kBwdWorkgroups)) * 2 * s.d * sizeof(float);
 }
 
 hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
                          const float *inv_freq, const void *qw, const void *kw, void *Q, void *K,
                          hipStream_t stream) {
-  const int v = chunk_of(s, t16, 8);
-  plan(&s, v, false);
+  const int v = chunk_of(s, t16, false);
+  plan(&s, v, false, false);
   const dim3 grid(static_cast<unsigned>(workgroups(s, kWaves, kFwdWorkgroups))), block(kThreads);
   const bool stream_out = s.M * (s.nq + s.nk) * s.d * (t16 ? 2 : 4) > (int64_t(32) << 20);
   auto launch = [&](auto kernel) {
@@ -505,24 +508,31 @@ hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const v
                          bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
                          const void *kw, void *dY, void *dqw, void *dkw, float *part, uint32_t *ticket,
                          hipStream_t stream) {
-  const int v = chunk_of(s, t16, 4);
-  plan(&s, v, true);
-  const dim3 grid(static_cast<unsigned>(workgroups(s, kBwdWaves, kBwdWorkgroups))), block(kBwdThreads);
-  auto go = [&](auto kernel) {
+  const bool norm = qw != nullptr;
+  const int v = chunk_of(s, t16, norm);
+  plan(&s, v, true, norm);
+  const int64_t wgs = norm ? workgroups(s, kBwdWaves, kBwdWorkgroups) : workgroups(s, kWaves, kFwdWorkgroups);
+  const dim3 grid(static_cast<unsigned>(wgs)), block(norm ? kBwdThreads : kThreads);
+  auto launch = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, dQ, dK, dV, Y, s, positions, inv_freq, qw, kw, dY, dqw, dkw,
                        part, ticket);
     return hipGetLastError();
   };
+#define QLORA_BWD(t16, v, inter) \
+  return norm ? launch(qk_bwd_kernel<t16, v, inter, true>) : launch(qk_bwd_kernel<t16, v, inter, false>);
   switch ((t16 ? 100 : 0) + 10 * v + (interleaved ? 1 : 0)) {
-    case 140: return go(qk_bwd_kernel<true, 4, false>);
-    case 141: return go(qk_bwd_kernel<true, 4, true>);
-    case 120: return go(qk_bwd_kernel<true, 2, false>);
-    case 121: return go(qk_bwd_kernel<true, 2, true>);
-    case 40: return go(qk_bwd_kernel<false, 4, false>);
-    case 41: return go(qk_bwd_kernel<false, 4, true>);
-    case 20: return go(qk_bwd_kernel<false, 2, false>);
-    default: return go(qk_bwd_kernel<false, 2, true>);
+    case 180: return launch(qk_bwd_kernel<true, 8, false, false>);
+    case 181: return launch(qk_bwd_kernel<true, 8, true, false>);
+    case 140: QLORA_BWD(true, 4, false)
+    case 141: QLORA_BWD(true, 4, true)
+    case 120: QLORA_BWD(true, 2, false)
+    case 121: QLORA_BWD(true, 2, true)
+    case 40: QLORA_BWD(false, 4, false)
+    case 41: QLORA_BWD(false, 4, true)
+    case 20: QLORA_BWD(false, 2, false)
+    default: QLORA_BWD(false, 2, true)
   }
+#undef QLORA_BWD
 }
 
 }  // namespace qlora
