@@ -439,14 +439,10 @@ hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hip
   const int64_t rounds = (w.n_cols + 511) / 512, each = (rounds + W - 1) / W;
   const int waves = static_cast<int>((rounds + each - 1) / each);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * waves);
-  const size_t lds = FEW ? static_cast<size_t>(waves) * XR * 1024 : 0;  // (at least the partial sums)
+  static_assert(!FEW || W * XR <= 64, "64 KB of dynamic LDS");
+  const size_t lds = FEW ? static_cast<size_t>(waves) * XR * 1024 : 0;  // (holds the partial sums too)
   const uint32_t magic = group_magic(static_cast<uint32_t>(w.group / 32));
   auto launch = [&](auto kernel) {
-    if (lds > 64 * 1024) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-      if (e != hipSuccess) return e;
-    }
     hipLaunchKernelGGL(kernel, grid, block, lds, stream, w, X, M, magic, Y);
     return hipGetLastError();
   };
@@ -503,15 +499,15 @@ int best_tile(int64_t M, int64_t rows) {
 template <int XR>
 hipError_t few(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   if (w.n_rows >= 16 * 1024) return go<true, XR, 2, 8>(w, X, M, Y, stream);
-  return go<true, XR, 1, 16>(w, X, M, Y, stream);
+  return go<true, XR, 1, XR < 8 ? 16 : 8>(w, X, M, Y, stream);
 }
 
 }  // namespace
 
 // Up to 8 tokens a wave has the whole of its round in flight, with 16 rows a workgroup, or 32 where
 // they are so many that the card's CUs have several workgroups each all the same: 1, 4 and 8 tokens
-// x 8192 -> 22016 24.3, 26.2, 28.2 us with 32 rows, 27.4, 36.7, 42.9 with 16; 1 x 4096 -> 11008 8.7 and 7.8,
-// 8 x 11008 -> 4096 15.5 and 10.5.
+// x 8192 -> 22016 24.3, 26.2, 28.2 us with 32 rows, 27.4, 36.7, 31.6 with 16; 1 x 4096 -> 11008 8.7 and 7.8,
+// 8 x 11008 -> 4096 15.5 and 11.2.
 hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   if (M == 1) return few<1>(w, X, M, Y, stream);
   if (M <= 4) return few<4>(w, X, M, Y, stream);

@@ -147,6 +147,16 @@ def test_layers(q, M, N, K, group):
     _check(q, M, N, K, group, True, group != 32)
 
 
+# one shape for each height and width of tile that the launcher chooses (by M and N alone), and two
+# lengths of rows: of whole blocks, and with a part of one
+@pytest.mark.parametrize("M,N", [(1, 16400), (3, 16400), (7, 16400), (8, 500), (12, 6000), (16, 12288), (64, 4096),
+                                 (32, 11008), (64, 8192), (64, 11008), (130, 4100), (1000, 250)])
+@pytest.mark.parametrize("K,group,zeros,bf16", [(640, 128, True, True), (640, 64, False, False), (1280, 32, True, False),
+                                                (1120, 32, True, True)])
+def test_every_tile(q, M, N, K, group, zeros, bf16):
+    _check(q, M, N, K, group, zeros, bf16)
+
+
 def test_longest_rows(q):
     _check(q, 2, 17, 262144, 128, True, True)
     _check(q, 1, 3, 262144, 32, False, True)
@@ -167,11 +177,11 @@ def test_a_token_does_not_depend_on_its_batch(q):
         assert torch.equal(q.group_linear_fwd(gw, X[m:m + 1])[0], Y[m])
 
 
-@pytest.mark.parametrize("M", [3, 40])
-def test_infinite_and_nan_inputs(q, M):
+@pytest.mark.parametrize("M,N", [(3, 70), (3, 16400), (12, 6000), (40, 70), (64, 4096), (64, 8200)])
+def test_infinite_and_nan_inputs(q, M, N):
     """As the definition: only the token concerned, infinite or NaN where its products are."""
     import torch
-    N, K, group = 70, 512, 64
+    K, group = 512, 64
     codes, s, z, gw = _weight(q, N, K, group, True, True, seed=3)
     codes[5, 100] = z[5, 100 // group]          # a weight of zero meets the infinity
     gw.codes = torch.from_numpy(og.pack(codes)).cuda()
