@@ -21,6 +21,13 @@
 // whole contiguous pieces and passed through LDS of the wave's own (no barrier), in the order of
 // the codes, the 16-byte chunk c of a token's block at slot c ^ token, so that the sixteen
 // token lanes of a fragment read fall in distinct banks.
+//
+// Times here are of a product in a graph; an empty node takes 1.8 us of each.  One token x 4096 ->
+// 11008 takes 7.8 us (23.2 MB, 3.9 TB/s past the node's 1.8): most of it is the start, the first
+// loads' way and the sums' way out.  16 x 8192 -> 22016 takes 28.6 us (93 MB, 3.5 TB/s; one token of the
+// same weight 23.6): memory, with the codes in flight that the registers have room for.  64 x 4096 ->
+// 11008 takes 22.1 us in groups of 32 and 17.7 in groups of 128: the scales are applied by vector
+// instructions, two for each sum of a group.
 
 #include <type_traits>
 
@@ -40,10 +47,18 @@ __device__ __forceinline__ u32x4_t transpose_lane_groups(u32x4_t d) {
 }
 
 // Eight codes -> four bf16 pairs in the order (0, 4), (1, 5), (2, 6), (3, 7): 16 + q, or q - z.
-__device__ __forceinline__ u32x4_t offset_codes(uint32_t c) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
-  return u32x4_t{((c << 3) & kMask) | kBase, ((c >> 1) & kMask) | kBase, ((c >> 5) & kMask) | kBase,
-                 ((c >> 9) & kMask) | kBase};
+// The two constants stand in registers that the compiler cannot see through (as literals they would
+// take an instruction each: an and-or has no room for them).
+struct CodeBits {
+  uint32_t mask, base;
+  __device__ __forceinline__ void init() {
+    asm("s_mov_b32 %0, 0x780078" : "=s"(mask));
+    asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
+  }
+};
+__device__ __forceinline__ u32x4_t offset_codes(uint32_t c, const CodeBits &k) {
+  return u32x4_t{((c << 3) & k.mask) | k.base, ((c >> 1) & k.mask) | k.base, ((c >> 5) & k.mask) | k.base,
+                 ((c >> 9) & k.mask) | k.base};
 }
 __device__ __forceinline__ u32x4_t plain_codes(uint32_t c, float z) {
   u32x4_t r;
@@ -57,12 +72,20 @@ __device__ __forceinline__ u32x4_t code_order(u32x4_t x) {
   return u32x4_t{pack_lo(x[0], x[2]), pack_hi(x[0], x[2]), pack_lo(x[1], x[3]), pack_hi(x[1], x[3])};
 }
 
-// The value of lane group q (of four) made known to all lanes.
-__device__ __forceinline__ uint32_t from_lane_group(uint32_t v, int q) {
-  const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // lane groups (0 1 0 1), (2 3 2 3)
-  const uint32_t u = h[q >> 1];
-  const auto o = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return o[q & 1];
+// The value of lane group q (of four) made known to all lanes: by lane moves, or through the LDS
+// crossbar, which leaves the vector pipe alone.  Measured (us a product in a graph, moves / crossbar):
+// 1 x 11008 -> 4096 in groups of 64 8.7 / 8.2, 64 x 4096 -> 11008 in groups of 32 22.9 / 22.0, but
+// 16 x 8192 -> 22016 28.6 / 30.2: there LDS serves X at the rate at which the weight arrives.
+template <bool CROSSBAR>
+__device__ __forceinline__ uint32_t from_lane_group(uint32_t v, int q, uint32_t lane) {
+  if constexpr (CROSSBAR) {
+    return __builtin_amdgcn_ds_bpermute(4 * (lane % 16) + 64 * q, v);
+  } else {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // lane groups (0 1 0 1), (2 3 2 3)
+    const uint32_t u = h[q >> 1];
+    const auto o = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return o[q & 1];
+  }
 }
 
 // Waits until at most N of the wave's loads are on their way (they complete in order).
@@ -73,8 +96,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // What a wave holds.  XR: tokens kept in LDS (a power of two; MT tiles of 16 of them).  FS:
-// columns between two uses of a scale, the largest of 32, 64 and 128 that divides the group.
-// VS: a block's scales of a row are one aligned load.
+// columns between two uses of a scale: 128 where that divides the group, 64 for groups of 64
+// in whole blocks, else 32.  VS: a block's scales of a row are one aligned load.
 template <int XR, int NT, int FS, bool S16, bool VS>
 struct Product {
   static constexpr int MT = (XR + 15) / 16;
@@ -95,6 +118,7 @@ struct Product {
   };
 
   __amdgpu_buffer_rsrc_t codes, scales, zeros, X;
+  CodeBits bits;
   bool zp;  // zeros are given (else 8 everywhere)
   uint32_t lane, row_bytes, row_groups, x_bytes, per, magic, n_steps;
   char *xs;  // the wave's LDS, [4][XR][256] bytes (few tokens)
@@ -114,6 +138,7 @@ struct Product {
     const uint32_t n_groups = rows * row_groups;
     constexpr uint32_t kBytes = S16 ? 2 : 4;
     const int64_t g0 = n0 * row_groups;
+    bits.init();
     codes = make_rsrc(w.codes + n0 * row_bytes, rows * row_bytes);
     scales = make_rsrc(static_cast<const char *>(w.scales) + g0 * kBytes, n_groups * kBytes);
     zp = w.zeros != nullptr;
@@ -206,9 +231,9 @@ struct Product {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int k = 0; k < kSRegs; ++k) v.s[t][k] = from_lane_group(b.s[t][k], q);
+      for (int k = 0; k < kSRegs; ++k) v.s[t][k] = from_lane_group<XR != 16>(b.s[t][k], q, lane);
 #pragma unroll
-      for (int k = 0; k < kZRegs; ++k) v.z[t][k] = from_lane_group(b.z[t][k], q);
+      for (int k = 0; k < kZRegs; ++k) v.z[t][k] = zp ? from_lane_group<XR != 16>(b.z[t][k], q, lane) : b.z[t][k];
     }
     return v;
   }
@@ -242,7 +267,7 @@ struct Product {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t cj = c.c[t][j];
-        w[t] = EXACT ? plain_codes(cj, v.zero(t, k)) : offset_codes(cj);
+        w[t] = EXACT ? plain_codes(cj, v.zero(t, k)) : offset_codes(cj, bits);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -476,8 +501,8 @@ hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hip
 // Tiles of XR tokens and 16 NT rows for more than 8 tokens.  Below 256 workgroups, one to a CU, a
 // launch takes what its tile takes (in us at K = 8192, beside 3.5 of the launch itself: small
 // tiles are sooner done, each reads X for itself), above it as many times that as it has rounds
-// of 256.  58 tokens x 8064 -> 560: 8.4 us with the smallest tile, 26.4 with the largest; 64 x
-// 8192 -> 8192: 56.3 with the smallest, 23.2 with 64 x 32; 64 x 4096 -> 11008: 19.3 with the largest.
+// of 256.  58 tokens x 8064 -> 560: 8.4 us with the smallest tile, 26.1 with the largest; 64 x
+// 8192 -> 8192: 55.8 and 28.1, 23.6 with 64 x 32; 64 x 4096 -> 11008: 34.0 and 17.7, 26.4 with 64 x 32.
 struct TileCost {
   int tokens, rows16;
   double us;
@@ -506,8 +531,8 @@ hipError_t few(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hi
 
 // Up to 8 tokens a wave has the whole of its round in flight, with 16 rows a workgroup, or 32 where
 // they are so many that the card's CUs have several workgroups each all the same: 1, 4 and 8 tokens
-// x 8192 -> 22016 24.3, 26.2, 28.2 us with 32 rows, 27.4, 36.7, 31.6 with 16; 1 x 4096 -> 11008 8.7 and 7.8,
-// 8 x 11008 -> 4096 15.5 and 11.2.
+// x 8192 -> 22016 23.6, 25.0, 28.1 us with 32 rows, 26.4, 35.9, 32.5 with 16; 1 x 4096 -> 11008 8.8 and 7.8,
+// 8 x 11008 -> 4096 13.2 and 10.2.
 hipError_t launch_group_linear(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   if (M == 1) return few<1>(w, X, M, Y, stream);
   if (M <= 4) return few<4>(w, X, M, Y, stream);

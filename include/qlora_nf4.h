@@ -24,14 +24,14 @@
  *     fixed scratch array of the library instead).
  *   - Workspaces: the first QLORA_WORKSPACE_HEADER_BYTES bytes of every
  *     workspace hold counters and flags that the small-M forward's workgroups
- *     use to hand U_s to each other, and the ticket of qlora_qk_bwd.  They must be zero when a workspace is
- *     first used (clear it once after allocating); every call leaves them
- *     zero, and no other call writes them, so one workspace can serve calls of
- *     any shape.  Calls that share a workspace must not overlap.  Launches of
- *     the small-M forward must not overlap each other on one GPU at all (on
- *     several streams, even with a workspace each): their first workgroups
- *     have to be on the card together, and each could keep the other's from
- *     starting.  They may overlap other kernels.
+ *     use to hand U_s to each other, and the ticket of qlora_qk_bwd.  They must
+ *     be zero when a workspace is first used (clear it once after allocating);
+ *     every call leaves them zero, and no other call writes them, so one
+ *     workspace can serve calls of any shape.  Calls that share a workspace
+ *     must not overlap.  Launches of the small-M forward must not overlap each
+ *     other on one GPU at all (on several streams, even with a workspace
+ *     each): their first workgroups have to be on the card together, and each
+ *     could keep the other's from starting.  They may overlap other kernels.
  *   - `stream` is a hipStream_t (NULL = the null stream).  Each call checks
  *     its arguments on the host, then enqueues its kernels asynchronously on
  *     `stream` and returns.  Kernel faults surface at the caller's next
