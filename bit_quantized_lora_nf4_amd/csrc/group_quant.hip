@@ -7,7 +7,8 @@
 //   code = clamp(rint(RN(w RN(1 / s))) + z, 0, 15),   w' = RN((code - z) s)
 //
 // RN rounds to fp32, ST to the scales' type (bf16 or fp32); s below 2^-126 counts as 0 and
-// 1 / s as 0 then, so that a group of zeros (or of subnormal numbers) stands for zeros.  The
+// 1 / s as 0 then, so that a group of zeros (or of subnormal numbers) stands for zeros; s that is not
+// finite (an infinity or a NaN in the group) becomes NaN, and 1 / s counts as 0.  The
 // reciprocal is taken once a group, the weights are multiplied by it.  Both kernels are bound
 // by memory: 2 or 4 bytes a weight on one side, 0.5 and the scales on the other.
 
@@ -35,6 +36,7 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi) {
   float s = ZP ? (hi - lo) * kPer15 : hi * kPer7;
   if constexpr (S16) s = bf16_to_f32(to_bf16(s));
   if (s < 0x1p-126f) return {0.0f, 0.0f, ZP ? 0.0f : 8.0f};
+  if (!(s < __builtin_inff())) return {__builtin_nanf(""), 0.0f, ZP ? 0.0f : 8.0f};
   const float inv = 1.0f / s;
   const float z = ZP ? fminf(fmaxf(__builtin_rintf(-lo * inv), 0.0f), 15.0f) : 8.0f;
   return {s, inv, z};
@@ -74,12 +76,15 @@ __device__ __forceinline__ Chunk<W16> load_chunk(const void *W, int64_t c) {
   }
   return x;
 }
+// NaN if either is.
+__device__ __forceinline__ float lesser(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float greater(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 template <bool W16, bool ZP>
 __device__ __forceinline__ void extremes(const Chunk<W16> &x, float &lo, float &hi) {
 #pragma unroll
   for (int i = 0; i < Chunk<W16>::V; ++i) {
-    if constexpr (ZP) lo = fminf(lo, x.v[i]);
-    hi = fmaxf(hi, ZP ? x.v[i] : fabsf(x.v[i]));
+    if constexpr (ZP) lo = lesser(lo, x.v[i]);
+    hi = greater(hi, ZP ? x.v[i] : fabsf(x.v[i]));
   }
 }
 template <bool W16>
@@ -119,8 +124,8 @@ __global__ __launch_bounds__(kThreads) void group_quantize_kernel(const void *__
     float lo = 0.0f, hi = 0.0f;
     extremes<W16, ZP>(x[u], lo, hi);
     for (int m = 1; m < lanes; m <<= 1) {
-      hi = fmaxf(hi, __shfl_xor(hi, m, 64));
-      if constexpr (ZP) lo = fminf(lo, __shfl_xor(lo, m, 64));
+      hi = greater(hi, __shfl_xor(hi, m, 64));
+      if constexpr (ZP) lo = lesser(lo, __shfl_xor(lo, m, 64));
     }
     const GroupStep g = group_step<S16, ZP>(lo, hi);
     store_codes<W16>(x[u], g, c, codes);
@@ -141,8 +146,10 @@ __global__ __launch_bounds__(kThreads) void group_quantize_any_kernel(const void
     const int64_t base = i * per_group;
     float lo = 0.0f, hi = 0.0f;
     for (int64_t c = lane; c < per_group; c += 64) extremes<W16, ZP>(load_chunk<W16, false>(W, base + c), lo, hi);
-    hi = wave_max(hi);
-    if constexpr (ZP) lo = wave_min(lo);
+    for (int m = 1; m < 64; m <<= 1) {
+      hi = greater(hi, __shfl_xor(hi, m, 64));
+      if constexpr (ZP) lo = lesser(lo, __shfl_xor(lo, m, 64));
+    }
     const GroupStep g = group_step<S16, ZP>(lo, hi);
     for (int64_t c = lane; c < per_group; c += 64) store_codes<W16>(load_chunk<W16, false>(W, base + c), g, base + c, codes);
     if (lane == 0) store_step<S16, ZP>(g, i, scales, zeros);

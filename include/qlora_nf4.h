@@ -421,7 +421,9 @@ typedef struct {
  *   else         lo = min(w, 0), hi = max(w, 0), s = ST(RN(RN(hi - lo) RN(1 / 15))),
  *                z = clamp(rint(RN(-lo RN(1 / s))), 0, 15)
  *   code = clamp(rint(RN(w RN(1 / s))) + z, 0, 15)   (rint: ties to even)
- * s below 2^-126 is stored as 0 and 1 / s counts as 0 then: such a group stands for zeros. */
+ * s below 2^-126 is stored as 0 and 1 / s counts as 0 then: such a group stands for zeros.  A
+ * group with an infinity or a NaN, or whose range is beyond fp32, gets the scale NaN: all of it
+ * stands for NaN. */
 int qlora_group_quantize(const void *W, int w_dtype, int64_t n_rows, int64_t n_cols, int64_t group, int scale_type,
                          uint8_t *codes, void *scales, uint8_t *zeros, void *stream);
 

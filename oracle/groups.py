@@ -14,7 +14,8 @@ TINY = np.float32(2.0 ** -126)
 
 
 def quantize(W, group, zeros, scale_bf16):
-    """codes [N, K] (0..15), scales [N, G] fp32 values, zeros [N, G] of W (float32 values)."""
+    """codes [N, K] (0..15), scales [N, G] fp32 values, zeros [N, G] of W (float32 values).  A group
+    whose scale is not finite gets the scale NaN (its codes mean nothing)."""
     W = np.asarray(W, np.float32)
     N, K = W.shape
     w = W.reshape(N, K // group, group)
@@ -25,9 +26,10 @@ def quantize(W, group, zeros, scale_bf16):
         s = np.abs(w).max(2) * (np.float32(1) / np.float32(7))
     if scale_bf16:
         s = fp.bf16_to_f32(fp.bf16_bits(s)).reshape(s.shape)
-    none = s < TINY
-    s = np.where(none, np.float32(0), s).astype(np.float32)
+    s = np.where(s < TINY, np.float32(0), np.where(np.isfinite(s), s, np.float32(np.nan))).astype(np.float32)
+    none = ~(s > 0)
     inv = np.where(none, np.float32(0), np.float32(1) / np.where(none, np.float32(1), s)).astype(np.float32)
+    w, lo = (np.where(np.isfinite(v), v, np.float32(0)) for v in (w, lo if zeros else s))
     z = np.clip(np.rint(-lo * inv), 0, 15) if zeros else np.full(s.shape, 8, np.float32)
     codes = np.clip(np.rint(w * inv[:, :, None]) + z[:, :, None], 0, 15)
     return codes.reshape(N, K).astype(np.uint8), s, z.astype(np.uint8)

@@ -108,6 +108,38 @@ def test_quantize_bits(q, N, K, group, zeros, w16, s16):
                           synth.bf16_bits_to_f32(synth.to_bf16_bits(w32)).reshape(N, K).astype(np.float64))
 
 
+@pytest.mark.parametrize("group", [32, 128, 512, 96, 1536])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("w16", [True, False])
+def test_quantize_not_finite(q, group, zeros, w16):
+    """An infinity or a NaN anywhere in a group makes that group NaN, and no other; so does a range
+    that fp32 does not hold."""
+    import torch
+    N, K = 12, 1536
+    W = np.random.default_rng(group).standard_normal((N, K)).astype(np.float32)
+    for k, bad in enumerate((np.inf, -np.inf, np.nan, -np.nan)):
+        W[2 * k + 1, (0, K // 2 + 5, K - 1, K // 3)[k]] = bad
+    if zeros:
+        W[9, 0], W[9, 1] = 3e38, -3e38
+    if w16:
+        bits = synth.to_bf16_bits(W)
+        W, dev = synth.bf16_bits_to_f32(bits).reshape(N, K), gc.dev_bf16(bits)
+    else:
+        dev = gc.dev_f32(W)
+    with np.errstate(over="ignore", invalid="ignore"):
+        codes, s, z = og.quantize(W, group, zeros, True)
+    bad = np.isnan(s)
+    assert bad.sum() == 4 + zeros
+    gw = q.group_quantize(dev, group, zeros=zeros)
+    assert np.array_equal(np.isnan(gw.scales.float().cpu().numpy()), bad)
+    got = q.group_dequantize(gw, torch.float32).cpu().numpy().reshape(N, K // group, group)
+    assert np.all(np.isnan(got[bad]))
+    want = og.values(codes, s, z, group).reshape(got.shape)
+    assert np.array_equal(got[~bad], want[~bad].astype(np.float32))
+    Y = q.group_linear_fwd(gw, torch.ones((3, K), dtype=torch.bfloat16, device="cuda")).float().cpu().numpy()
+    assert np.array_equal(np.isnan(Y), np.repeat(bad.any(1)[None], 3, 0))
+
+
 def test_dequantize_any_zero_byte_and_out(q):
     import torch
     z = np.random.default_rng(0).integers(0, 256, (9, 5)).astype(np.uint8)

@@ -165,3 +165,14 @@ def test_abi_refusals():
     assert g(FAKE + 4, 1, N, K, G, 0, FAKE, FAKE, None, None) == _lib.QLORA_ERR_ALIGN
     assert g(FAKE, 1, N, K, G, 0, FAKE + 4, FAKE, None, None) == _lib.QLORA_ERR_ALIGN
     assert g(FAKE, 1, N, K, G, 0, FAKE, FAKE + 2, None, None) == _lib.QLORA_ERR_ALIGN
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_a_group_with_a_bad_value_is_nan(zeros):
+    W = np.ones((3, 64), np.float32)
+    W[0, 3], W[1, 40], W[2, 7] = np.inf, np.nan, -np.inf
+    with np.errstate(over="ignore", invalid="ignore"):
+        codes, s, z = og.quantize(W, 32, zeros, False)
+    assert np.isnan(s).tolist() == [[True, False], [False, True], [True, False]]
+    v = og.values(codes, s, z, 32).reshape(3, 2, 32)
+    assert np.all(np.isnan(v[np.isnan(s)])) and np.allclose(v[~np.isnan(s)], 1.0, atol=1e-6)
