@@ -20,13 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Chunks of a thread of the quantizer, and of the inverse.
-constexpr int chunks_each(bool bf16) { return bf16 ? 2 : 4; }
-constexpr int kUnroll = 4;
+constexpr int kEach = 2, kUnroll = 4;  // chunks of a thread of the quantizer, and of the inverse
 constexpr int64_t kMemorySideCache = int64_t(256) << 20;
+
+// 1.5 x 2^23: added to a number below 2^22 it leaves the number rounded to an integer, ties to even,
+// in the sum's last bits.
+constexpr float kRound = 12582912.0f;
 
 struct GroupStep {
   float s, inv, z;
+  float least, most;  // kRound - z, kRound + 15 - z: where a rounded weight may be
 };
 // Scale, its reciprocal and the zero of a group from its extremes (lo <= 0 <= hi with zeros,
 // else hi = max |w|).
@@ -35,14 +38,12 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi) {
   constexpr float kPer7 = 1.0f / 7.0f, kPer15 = 1.0f / 15.0f;
   float s = ZP ? (hi - lo) * kPer15 : hi * kPer7;
   if constexpr (S16) s = bf16_to_f32(to_bf16(s));
-  if (s < 0x1p-126f) return {0.0f, 0.0f, ZP ? 0.0f : 8.0f};
-  if (!(s < __builtin_inff())) return {__builtin_nanf(""), 0.0f, ZP ? 0.0f : 8.0f};
-  const float inv = 1.0f / s;
-  const float z = ZP ? fminf(fmaxf(__builtin_rintf(-lo * inv), 0.0f), 15.0f) : 8.0f;
-  return {s, inv, z};
-}
-__device__ __forceinline__ uint32_t group_code(float w, const GroupStep &g) {
-  return static_cast<uint32_t>(fminf(fmaxf(__builtin_rintf(w * g.inv) + g.z, 0.0f), 15.0f));
+  const bool any = s >= 0x1p-126f && s < __builtin_inff();
+  const float inv = any ? 1.0f / s : 0.0f;
+  s = any ? s : s < 0x1p-126f ? 0.0f : __builtin_nanf("");
+  float z = 8.0f;
+  if constexpr (ZP) z = any ? __builtin_amdgcn_fmed3f(__builtin_rintf(-lo * inv), 0.0f, 15.0f) : 0.0f;
+  return {s, inv, z, kRound - z, kRound + (15.0f - z)};
 }
 template <bool S16, bool ZP>
 __device__ __forceinline__ void store_step(const GroupStep &g, int64_t i, void *scales, uint8_t *zeros) {
@@ -79,6 +80,27 @@ __device__ __forceinline__ Chunk<W16> load_chunk(const void *W, int64_t c) {
 // NaN if either is.
 __device__ __forceinline__ float lesser(float a, float b) { return __builtin_elementwise_minimum(a, b); }
 __device__ __forceinline__ float greater(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+// The extreme over `lanes` neighbouring lanes (a power of two), known to all of them; by moves
+// within rows of 16 lanes, then between rows.
+template <int MOVE>
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), MOVE, 0xF, 0xF, true));
+}
+template <typename F>
+__device__ __forceinline__ float lanes_extreme(float v, int lanes, F of) {
+  if (lanes > 1) v = of(v, moved<0xB1>(v));   // lanes 1 0 3 2
+  if (lanes > 2) v = of(v, moved<0x4E>(v));   // lanes 2 3 0 1
+  if (lanes > 4) v = of(v, moved<0x141>(v));  // mirrored within 8
+  if (lanes > 8) v = of(v, moved<0x140>(v));  // mirrored within 16
+  if (lanes > 16) v = of(v, __shfl_xor(v, 16, 64));
+  if (lanes > 32) v = of(v, __shfl_xor(v, 32, 64));
+  return v;
+}
+template <bool ZP>
+__device__ __forceinline__ void lanes_extremes(float &lo, float &hi, int lanes) {
+  hi = lanes_extreme(hi, lanes, greater);
+  if constexpr (ZP) lo = lanes_extreme(lo, lanes, lesser);
+}
 template <bool W16, bool ZP>
 __device__ __forceinline__ void extremes(const Chunk<W16> &x, float &lo, float &hi) {
 #pragma unroll
@@ -89,9 +111,13 @@ __device__ __forceinline__ void extremes(const Chunk<W16> &x, float &lo, float &
 }
 template <bool W16>
 __device__ __forceinline__ void store_codes(const Chunk<W16> &x, const GroupStep &g, int64_t c, void *codes) {
+  // Each code is the rounded weight's last bits less those of kRound - z, which come off all of them at
+  // once (modulo 2^32).
   uint32_t p = 0;
 #pragma unroll
-  for (int i = 0; i < Chunk<W16>::V; ++i) p |= group_code(x.v[i], g) << (4 * i);
+  for (int i = Chunk<W16>::V - 1; i >= 0; --i)
+    p = (p << 4) + __float_as_uint(__builtin_amdgcn_fmed3f(x.v[i] * g.inv + kRound, g.least, g.most));
+  p -= __float_as_uint(g.least) * (W16 ? 0x11111111u : 0x1111u);
   if constexpr (W16)
     static_cast<uint32_t *>(codes)[c] = p;
   else
@@ -99,34 +125,31 @@ __device__ __forceinline__ void store_codes(const Chunk<W16> &x, const GroupStep
 }
 
 // Groups of a power of two of chunks, at most a wave's 64: `lanes` neighbouring lanes hold a
-// group, a thread takes a few chunks, all loaded before the first is used (11008 x 4096 bf16: 23.9 us
-// with two, 27.7 with four; 22016 x 8192 fp32, streamed: 136 with two, 128 with four).  Whole groups
-// fall out together at the end, so no lane misses a partner.
+// group, a thread takes two chunks, both loaded before the first is used (11008 x 4096 bf16 with zeros:
+// 21.7 us, 23.9 with four; 22016 x 8192 fp32, streamed: 128.5 and 128.3).  Whole groups fall out together
+// at the end, so no lane misses a partner.  Vector instructions are what bounds it beside memory: about
+// six a weight with the minima, maxima and codes, 23.8 us for the first of these weights with ten.
 // STREAM: W is larger than the memory-side cache and is read past it (22016 x 8192 fp32, 721 MB: 128
-// us, 181 through the caches; 90 MB of bf16 are read faster through them, 23.9 us and 26.0).
+// us, 146 through the caches; 90 MB of bf16 are read faster through them, 21.7 us and 26.4).
 template <bool W16, bool S16, bool ZP, bool STREAM>
 __global__ __launch_bounds__(kThreads) void group_quantize_kernel(const void *__restrict__ W, int64_t chunks,
                                                                   int lanes, int shift, void *__restrict__ codes,
                                                                   void *__restrict__ scales,
                                                                   uint8_t *__restrict__ zeros) {
-  constexpr int kUnroll = chunks_each(W16);
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kUnroll) * kThreads + threadIdx.x;
-  Chunk<W16> x[kUnroll];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kEach) * kThreads + threadIdx.x;
+  Chunk<W16> x[kEach];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kEach; ++u) {
     const int64_t c = first + u * kThreads;
     if (c < chunks) x[u] = load_chunk<W16, STREAM>(W, c);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kEach; ++u) {
     const int64_t c = first + u * kThreads;
     if (c >= chunks) return;
     float lo = 0.0f, hi = 0.0f;
     extremes<W16, ZP>(x[u], lo, hi);
-    for (int m = 1; m < lanes; m <<= 1) {
-      hi = greater(hi, __shfl_xor(hi, m, 64));
-      if constexpr (ZP) lo = lesser(lo, __shfl_xor(lo, m, 64));
-    }
+    lanes_extremes<ZP>(lo, hi, lanes);
     const GroupStep g = group_step<S16, ZP>(lo, hi);
     store_codes<W16>(x[u], g, c, codes);
     if ((threadIdx.x & (lanes - 1)) == 0) store_step<S16, ZP>(g, c >> shift, scales, zeros);
@@ -146,10 +169,7 @@ __global__ __launch_bounds__(kThreads) void group_quantize_any_kernel(const void
     const int64_t base = i * per_group;
     float lo = 0.0f, hi = 0.0f;
     for (int64_t c = lane; c < per_group; c += 64) extremes<W16, ZP>(load_chunk<W16, false>(W, base + c), lo, hi);
-    for (int m = 1; m < 64; m <<= 1) {
-      hi = greater(hi, __shfl_xor(hi, m, 64));
-      if constexpr (ZP) lo = lesser(lo, __shfl_xor(lo, m, 64));
-    }
+    lanes_extremes<ZP>(lo, hi, 64);
     const GroupStep g = group_step<S16, ZP>(lo, hi);
     for (int64_t c = lane; c < per_group; c += 64) store_codes<W16>(load_chunk<W16, false>(W, base + c), g, base + c, codes);
     if (lane == 0) store_step<S16, ZP>(g, i, scales, zeros);
@@ -214,8 +234,7 @@ hipError_t quantize_go(const void *W, int64_t n, int64_t group, void *codes, voi
   constexpr int V = Chunk<W16>::V;
   const int64_t chunks = n / V, per_group = group / V;
   if (per_group <= 64 && (per_group & (per_group - 1)) == 0) {
-    constexpr int kEach = kThreads * chunks_each(W16);
-    const int64_t blocks = (chunks + kEach - 1) / kEach;
+    const int64_t blocks = (chunks + kThreads * kEach - 1) / (kThreads * kEach);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     int shift = 0;
     while ((int64_t(1) << shift) < per_group) ++shift;
