@@ -335,8 +335,9 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
     load(next_g, next_x, first);
     float co[V], si[V];
     angles<V>(positions[m], inv_freq, s, lane, u, un.turns, lds[wave], co, si);
-    // one round of q or k heads; the gradients of w are summed in dw
-    auto round = [&](B &g, const B &x, const B &weight, float *dw) __attribute__((always_inline)) {
+    // one round of q or k heads; the gradients of w are summed in dw.  on: this lane has a head (with a
+    // zero eps the root of another's zeros is infinite, and its product with them NaN)
+    auto round = [&](B &g, const B &x, const B &weight, float *dw, bool on) __attribute__((always_inline)) {
       float v[2 * V];
       g.values(v);
       turn<V, INTER>(v, co, si, -1.0f);
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
         }
         sq = lanes_sum(sq, s.lanes);
         gx = lanes_sum(gx, s.lanes);
-        const float r = inverse_rms(sq, s), back = r * r * (gx * s.inv_d);
+        const float r = on ? inverse_rms(sq, s) : 0.0f, back = r * r * (gx * s.inv_d);
 #pragma unroll
         for (int e = 0; e < 2 * V; ++e) {
           dw[e] = __builtin_fmaf(v[e] * r, xv[e], dw[e]);
@@ -363,12 +364,13 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
     for (int r = first; r < last; ++r) {
       B g = next_g, x = next_x;
       if (r + 1 < last) load(next_g, next_x, r + 1);
-      if (r < R.q)
-        round(g, x, wq, dwq);
-      else if (r < R.q + R.k)
-        round(g, x, wk, dwk);
       const int h = head(r);
-      if (h < pick(r < R.q, s.nq, s.nk)) g.template store<false>(dY, row_at(r, h), un);
+      const bool on = h < pick(r < R.q, s.nq, s.nk);
+      if (r < R.q)
+        round(g, x, wq, dwq, on);
+      else if (r < R.q + R.k)
+        round(g, x, wk, dwk, on);
+      if (on) g.template store<false>(dY, row_at(r, h), un);
     }
   }
   if constexpr (NORM) {
