@@ -147,14 +147,16 @@ __device__ __forceinline__ void angles(int64_t position, const float *inv_freq, 
     lds[kMaxPairs + i] = sn;
   }
   __builtin_amdgcn_wave_barrier();
+  const int at = turns ? u * V : 0;  // (a lane that does not turn uses neither)
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    co[e] = turns ? lds[u * V + e] : 1.0f;
-    si[e] = turns ? lds[kMaxPairs + u * V + e] : 0.0f;
+    co[e] = lds[at + e];
+    si[e] = lds[kMaxPairs + at + e];
   }
 }
 
-// (x0, x1) of one lane turned by its V angles.
+// (x0, x1) of one lane turned by its V angles.  A lane whose elements only pass must not get here: times
+// 1 and 0 an infinity or a NaN of one would reach the other, and a negative zero would lose its sign.
 template <int V, bool INTER>
 __device__ __forceinline__ void turn(float *x, const float *co, const float *si, float sign) {
 #pragma unroll
@@ -287,8 +289,8 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict
 #pragma unroll
         for (int e = 0; e < 2 * V; ++e) v[e] = v[e] * rms * w[e];
       }
-      turn<V, INTER>(v, co, si, 1.0f);
-      x.set(v);
+      if (un.turns) turn<V, INTER>(v, co, si, 1.0f);
+      if (norm || un.turns) x.set(v);  // (else the bits as loaded: a conversion would quiet a NaN)
       if (h < heads) x.template store<STREAM>(pick(is_q, Q, K), (m * heads + h) * s.d, un);
     }
   }
@@ -338,9 +340,10 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
     // one round of q or k heads; the gradients of w are summed in dw.  on: this lane has a head (with a
     // zero eps the root of another's zeros is infinite, and its product with them NaN)
     auto round = [&](B &g, const B &x, const B &weight, float *dw, bool on) __attribute__((always_inline)) {
+      if (!NORM && !un.turns) return;  // (the bits as loaded: a conversion would quiet a NaN)
       float v[2 * V];
       g.values(v);
-      turn<V, INTER>(v, co, si, -1.0f);
+      if (un.turns) turn<V, INTER>(v, co, si, -1.0f);
       if constexpr (NORM) {
         float xv[2 * V], w[2 * V], sq = 0.0f, gx = 0.0f;
         x.values(xv);

@@ -1,6 +1,8 @@
 """Norms of query / key heads with the rotation on the GPU, where single values decide: a zero eps with
-head counts that leave a wave's round partly filled."""
+head counts that leave a wave's round partly filled; elements past the rotated ones beside
+infinities, NaN and signed zeros."""
 
+import numpy as np
 import pytest
 
 from tests import test_gpu_qk as tq
@@ -25,3 +27,97 @@ def test_zero_eps(q, monkeypatch, nq, nk, d, rot, bf16):  # noqa: F811
     got = c.bwd(q)
     torch.cuda.synchronize()
     c.check_bwd(got)
+
+
+# ---- elements that pass ----------------------------------------------------------------
+
+PASS = [(80, 32), (64, 16), (128, 64), (96, 48), (12, 4), (100, 36), (128, 0), (252, 64), (256, 128)]
+
+
+def _bits(t):
+    import torch
+    return t.contiguous().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+def _bad_values(bf16):
+    """Infinities, quiet and signalling NaN of both signs and a negative zero, as bits."""
+    if bf16:
+        return np.array([0x7F80, 0xFF80, 0x7FC0, 0xFFC0, 0x7F81, 0xFF93, 0x8000], np.uint16).view(np.int16)
+    return np.array([0x7F800000, 0xFF800000, 0x7FC00000, 0xFFC12345, 0x7F800001, 0xFF800101, 0x80000000],
+                    np.uint32).view(np.int32)
+
+
+def _spread(t, rot, bf16, seed):
+    """t [M, heads, d] with one bad value in each head, at an element past rot."""
+    import torch
+    t = t.clone()
+    M, H, d = t.shape
+    bad = torch.from_numpy(_bad_values(bf16)).cuda()
+    rng = np.random.default_rng([seed, d, rot])
+    at = torch.from_numpy(rng.integers(rot, d, (M, H))).cuda()[..., None]
+    which = torch.arange(M * H, device="cuda").view(M, H, 1) % len(bad)
+    _bits(t).scatter_(2, at, bad[which])
+    return t
+
+
+@pytest.mark.parametrize("d,rot", PASS)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_elements_past_rot_pass_bit_for_bit(q, d, rot, inter, bf16):  # noqa: F811
+    """Without a norm: what stands past rot comes out with its bits, and leaves the others alone."""
+    import torch
+    M, nq, nk = 5, 5, 3
+    c = Case(M, nq, nk, d, rot, False, inter, bf16)
+    Q0, K0 = c.fwd(q)
+    dY0 = c.bwd(q)[0].view(M, -1, d)
+    rows = c.dY.view(M, nq + 2 * nk, d)
+    rows = torch.cat([_spread(rows[:, :nq + nk], rot, bf16, 1), rows[:, nq + nk:]], 1)
+    c.dY = rows.reshape(M, -1)
+    Q, K = c.fwd(q)
+    for got, clean, given in ((Q, Q0, rows[:, :nq]), (K, K0, rows[:, nq:nq + nk])):
+        assert torch.equal(_bits(got[..., :rot]), _bits(clean[..., :rot]))
+        assert torch.equal(_bits(got[..., rot:]), _bits(given[..., rot:]))
+    c.g = [(a, _spread(t, rot, bf16, 2 + i)) for i, (a, t) in enumerate(c.g)]
+    dY = c.bwd(q)[0].view(M, -1, d)
+    up = torch.cat([t for _, t in c.g], 1)
+    assert torch.equal(_bits(dY[..., :rot]), _bits(torch.cat([dY0[:, :nq + nk, :rot], up[:, nq + nk:, :rot]], 1)))
+    assert torch.equal(_bits(dY[..., rot:]), _bits(up[..., rot:]))
+
+
+@pytest.mark.parametrize("d,rot", PASS)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_normed_elements_past_rot(q, d, rot, inter, bf16):  # noqa: F811
+    """With a norm a head with an infinity is x * 0: NaN at the infinity, zeros elsewhere, and a
+    passed negative zero stays one.  In the backward an infinite gradient of a passed element
+    reaches that element of the weight's gradient alone."""
+    import torch
+    M, nq, nk = 4, 3, 2
+    c = Case(M, nq, nk, d, rot, True, inter, bf16)
+    rows = c.dY.view(M, -1, d)
+    rng = np.random.default_rng(d)
+    at = rng.integers(rot, d, (M, nq))
+    zero = (at - rot + 1) % (d - rot) + rot        # another element that passes
+    for m in range(M):
+        for h in range(nq):
+            rows[m, h, at[m, h]] = float("inf") if h % 2 else -0.0
+            rows[m, h, zero[m, h]] = -0.0
+    Q = c.fwd(q)[0]
+    for m in range(M):
+        for h in range(nq):
+            if h % 2:
+                hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+                hit[at[m, h]] = True
+                assert torch.equal(Q[m, h].isnan(), hit) and not bool(Q[m, h][~hit].any())
+            else:
+                assert bool(Q[m, h].isfinite().all())
+            for e in {int(zero[m, h])} - {int(at[m, h])}:
+                assert float(Q[m, h, e]) == 0 and bool(torch.signbit(Q[m, h, e]))
+    c = Case(M, nq, nk, d, rot, True, inter, bf16)
+    want = c.bwd(q)[1:]
+    e = [int(v) for v in rng.integers(rot, d, 2)]
+    c.g[0][1][1, 2, e[0]] = float("inf")
+    c.g[1][1][3, 0, e[1]] = float("-inf")
+    for got, clean, j in zip(c.bwd(q)[1:], want, e):
+        rest = torch.arange(d, device="cuda") != j
+        assert bool(got[j].isinf()) and torch.equal(got[rest], clean[rest])
