@@ -12,7 +12,7 @@
 // and backward, with dn the rotation by -t of the output's gradient:
 //   dw = sum dn x r,   dx = r (g - x r (r mean(g x))),  g = dn w
 //
-// The angle in turns, p f / (2 pi), is formed and reduced to [-1/2, 1/2] in 64 bits (at
+// The angle in turns, p f / (2 pi), its reduction, sine and cosine are formed in 64 bits (at
 // position 131071 a product in fp32 would be off by up to 2^-8 radians); one sine and cosine
 // a pair and token, shared by the token's heads through LDS.  Both directions are bound by
 // memory; every row is read once and every result written once.
@@ -129,7 +129,51 @@ struct Both {
     c[0] = from_values<T16, V>(v);
     c[1] = from_values<T16, V>(v + V);
   }
+  // The other's where `changed`; else the bits as loaded, which a conversion would not keep of a NaN.
+  __device__ __forceinline__ void take(const Both &o, bool changed) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < Raw<T16, V>::kWords; ++e) c[k].w[e] = changed ? o.c[k].w[e] : c[k].w[e];
+  }
 };
+
+// 1 / OVER in a scalar register that is set where it is used: the compiler would keep every constant of
+// a series in vector registers over the whole kernel, 16 more of them, and fewer waves would fit.
+template <int64_t OVER>
+__device__ __forceinline__ double one_over() {
+  constexpr uint64_t bits = __builtin_bit_cast(uint64_t, 1.0 / OVER);
+  uint32_t lo, hi;
+  asm volatile("s_mov_b32 %0, %1" : "=s"(lo) : "n"(static_cast<uint32_t>(bits)));
+  asm volatile("s_mov_b32 %0, %1" : "=s"(hi) : "n"(static_cast<uint32_t>(bits >> 32)));
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sine and cosine of an angle given in turns, all in 64 bits and each rounded once: within half a step of
+// fp32, also at far positions.  The angle is reduced to an eighth of a turn on either side of a quarter's
+// multiple (1.5 x 2^52 added leaves the multiple in the sum's last bits), where the power series to
+// x^11 and x^12 are off by less than 2^-36.  (An angle
+// rounded to fp32 before its sine is taken leaves a cosine off by up to 1.1e-7, its rounding alone by 3.0e-8.)
+__device__ __forceinline__ void sine_cosine(double turn, float &sn, float &cs) {
+  const double t = turn - __builtin_rint(turn);
+  const double k = __builtin_fma(4.0, t, 0x1.8p52);
+  const uint32_t quarter = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, k));
+  const double x = __builtin_fma(-0.25, k - 0x1.8p52, t) * 6.283185307179586;
+  const double x2 = x * x;
+  double s = one_over<-39916800>(), c = one_over<479001600>();
+  s = __builtin_fma(s, x2, one_over<362880>());
+  s = __builtin_fma(s, x2, one_over<-5040>());
+  s = __builtin_fma(s, x2, one_over<120>());
+  s = __builtin_fma(s, x2, one_over<-6>());
+  c = __builtin_fma(c, x2, one_over<-3628800>());
+  c = __builtin_fma(c, x2, one_over<40320>());
+  c = __builtin_fma(c, x2, one_over<-720>());
+  c = __builtin_fma(c, x2, one_over<24>());
+  c = __builtin_fma(c, x2, -0.5);
+  const float fs = static_cast<float>(__builtin_fma(x * x2, s, x)), fc = static_cast<float>(__builtin_fma(c, x2, 1.0));
+  const bool odd = quarter & 1;
+  sn = __uint_as_float(__float_as_uint(odd ? fc : fs) ^ ((quarter & 2) << 30));
+  cs = __uint_as_float(__float_as_uint(odd ? fs : fc) ^ (((quarter + 1) & 2) << 30));
+}
 
 // Sines and cosines of a token's pairs into the wave's own LDS, then the V pairs of this
 // lane's unit.  LDS accesses of one wave stay in order, so no barrier is needed.
@@ -139,15 +183,13 @@ __device__ __forceinline__ void angles(int64_t position, const float *inv_freq, 
   const double p = static_cast<double>(position);
   __builtin_amdgcn_wave_barrier();
   for (int i = lane; i < s.rot / 2; i += 64) {
-    const double turn = p * (static_cast<double>(inv_freq[i]) * 0.15915494309189535);
-    const float half_turns = static_cast<float>(2.0 * (turn - __builtin_rint(turn)));
     float sn, cs;
-    sincospif(half_turns, &sn, &cs);
+    sine_cosine(p * (static_cast<double>(inv_freq[i]) * 0.15915494309189535), sn, cs);
     lds[i] = cs;
     lds[kMaxPairs + i] = sn;
   }
   __builtin_amdgcn_wave_barrier();
-  const int at = turns ? u * V : 0;  // (a lane that does not turn uses neither)
+  const int at = turns ? u * V : 0;  // (the result of a lane that does not turn is not used)
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     co[e] = lds[at + e];
@@ -155,8 +197,8 @@ __device__ __forceinline__ void angles(int64_t position, const float *inv_freq, 
   }
 }
 
-// (x0, x1) of one lane turned by its V angles.  A lane whose elements only pass must not get here: times
-// 1 and 0 an infinity or a NaN of one would reach the other, and a negative zero would lose its sign.
+// (x0, x1) of one lane turned by its V angles.  Of a lane whose elements only pass the result is not
+// used: times 1 and 0 an infinity or a NaN of one would reach the other, and a negative zero lose its sign.
 template <int V, bool INTER>
 __device__ __forceinline__ void turn(float *x, const float *co, const float *si, float sign) {
 #pragma unroll
@@ -297,9 +339,11 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict
 }
 
 // With a norm the waves of large workgroups sum the weights' gradients (few partial sums); without
-// one nothing is summed, and the kernel is the forward's with the other sign and the v heads.
+// one nothing is summed, and the kernel is the forward's with the other sign and the v heads, on eight
+// waves a SIMD (62 registers; with 65, and seven, 2048 tokens of 64 + 64 + 64 heads of 128 take 35.3 us
+// instead of 34.3).
 template <bool T16, int V, bool INTER, bool NORM>
-__global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
+__global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void qk_bwd_kernel(const void *__restrict__ dQ, const void *__restrict__ dK,
                                                           const void *__restrict__ dV, const void *__restrict__ Y,
                                                           QkShape s, const int64_t *__restrict__ positions,
                                                           const float *__restrict__ inv_freq,
@@ -340,10 +384,9 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
     // one round of q or k heads; the gradients of w are summed in dw.  on: this lane has a head (with a
     // zero eps the root of another's zeros is infinite, and its product with them NaN)
     auto round = [&](B &g, const B &x, const B &weight, float *dw, bool on) __attribute__((always_inline)) {
-      if (!NORM && !un.turns) return;  // (the bits as loaded: a conversion would quiet a NaN)
       float v[2 * V];
       g.values(v);
-      if (un.turns) turn<V, INTER>(v, co, si, -1.0f);
+      if (!NORM || un.turns) turn<V, INTER>(v, co, si, -1.0f);
       if constexpr (NORM) {
         float xv[2 * V], w[2 * V], sq = 0.0f, gx = 0.0f;
         x.values(xv);
@@ -362,7 +405,13 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads) void qk_bwd_kernel(c
           v[e] = r * (v[e] * w[e] - xv[e] * back);
         }
       }
-      g.set(v);
+      if constexpr (NORM) {
+        g.set(v);
+      } else {  // (by a choice of words: with a branch around it 40.1 us instead of 39.0, interleaved)
+        B turned;
+        turned.set(v);
+        g.take(turned, un.turns);
+      }
     };
     for (int r = first; r < last; ++r) {
       B g = next_g, x = next_x;

@@ -1,10 +1,12 @@
 """Norms of query / key heads with the rotation on the GPU, where single values decide: a zero eps with
 head counts that leave a wave's round partly filled; elements past the rotated ones beside
-infinities, NaN and signed zeros."""
+infinities, NaN and signed zeros; sines and cosines to half a step."""
 
 import numpy as np
 import pytest
 
+from oracle import rotation as orot
+from tests import gpu_cases as gc
 from tests import test_gpu_qk as tq
 from tests.test_gpu_qk import Case, q  # noqa: F401  (q: the module's fixture)
 
@@ -121,3 +123,34 @@ def test_normed_elements_past_rot(q, d, rot, inter, bf16):  # noqa: F811
     for got, clean, j in zip(c.bwd(q)[1:], want, e):
         rest = torch.arange(d, device="cuda") != j
         assert bool(got[j].isinf()) and torch.equal(got[rest], clean[rest])
+
+
+# ---- angles ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("far,base", [(4096, 10000.0), (131072, 500000.0), (1 << 24, 10000.0)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_sines_and_cosines(q, far, base, inter):  # noqa: F811
+    """Pairs (1, 0) come out as (cos t, sin t), and backward as (cos t, -sin t): within half a step
+    of fp32, 2^-24 of the value, and the error of 64 bits (three roundings of t; 2^-36 for
+    sine and cosine on the reduced angle)."""
+    import torch
+    M, d = 777, 128
+    rng = np.random.default_rng(far)
+    pos = rng.integers(-far, far, M)
+    f = (base ** -(np.arange(d // 2) / (d // 2))).astype(np.float32)
+    i, j = orot.pairs(d, inter)
+    x = np.zeros((M, 3, d), np.float32)
+    x[..., i] = 1.0
+    Y, dpos, df = gc.dev_f32(x.reshape(M, -1)), torch.from_numpy(pos).cuda(), gc.dev_f32(f)
+    Y = Y.view(M, -1)
+    t = pos.astype(np.longdouble)[:, None] * f.astype(np.longdouble)[None]
+    co, si = np.cos(t).astype(np.float64), np.sin(t).astype(np.float64)
+    slack = 2.0 ** -36 + 4 * 2.0 ** -53 * np.abs(t).astype(np.float64)
+    Q, K = q.qk_norm_rope_fwd(Y, dpos, df, 1, 1, interleaved=inter)
+    R = Y.view(M, 3, d)
+    dY = q.qk_norm_rope_bwd(*(R[:, k:k + 1].contiguous() for k in range(3)), dpos, df, interleaved=inter)[0].view(M, 3, d)
+    for z, sign in ((Q[:, 0], 1), (K[:, 0], 1), (dY[:, 0], -1), (dY[:, 1], -1)):
+        z = z.cpu().numpy().astype(np.float64)
+        for got, want in ((z[:, i], co), (z[:, j], sign * si)):
+            tol = 2.0 ** -24 * np.abs(want) + slack
+            assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
