@@ -1269,14 +1269,14 @@ int qlora_qk_bwd(const qlora_qk_shape *shape, const void *dQ, const void *dK, co
   if (!aligned16(dQ) || !aligned16(dK) || !aligned16(dV) || !aligned16(dY) ||
       (norm && (!aligned16(Y) || !aligned16(dqw) || !aligned16(dkw))))
     return fail(QLORA_ERR_ALIGN, "qk_bwd: tensors must be 16-byte aligned");
-  float *part = nullptr;
+  double *part = nullptr;
   if (norm) {
     const size_t need = qlora_workspace_bytes_qk(shape, 1);
     if (!workspace || workspace_bytes < need)
       return fail(QLORA_ERR_WORKSPACE, "qk_bwd: workspace has %zu bytes, %zu needed", workspace ? workspace_bytes : 0,
                   need);
     if (!aligned16(workspace)) return fail(QLORA_ERR_ALIGN, "qk_bwd: workspace must be 16-byte aligned");
-    part = reinterpret_cast<float *>(static_cast<char *>(workspace) + qlora::kGemvSyncBytes);
+    part = reinterpret_cast<double *>(static_cast<char *>(workspace) + qlora::kGemvSyncBytes);
   }
   e = check_device();
   if (e != QLORA_OK) return e;

@@ -31,6 +31,9 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;           // forward
 constexpr int kBwdThreads = 1024, kBwdWaves = kBwdThreads / 64;  // backward: few partial sums
 constexpr int kMaxPairs = kQkMaxDim / 2;
 
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef double f64x2_t __attribute__((ext_vector_type(2)));
+
 // V values of a tensor (T16: bf16, else fp32) as loaded: one access of 16, 8 or 4 bytes.
 template <bool T16, int V>
 struct Raw {
@@ -210,7 +213,8 @@ __device__ __forceinline__ void turn(float *x, const float *co, const float *si,
   }
 }
 
-constexpr int kInFlight = 16;  // partial sums a thread asks for before it adds them
+constexpr int kJoin = 16;  // rows of partial sums that one workgroup adds
+constexpr int kJoinLoads = kJoin * kQkMaxDim / kBwdThreads;  // of a thread, for the longest rows
 constexpr int kSC1 = 16;       // buffer cache policy: agent-coherent access
 
 // Sum over the `lanes` lanes of a head (a power of two, the same for the whole launch), known
@@ -242,14 +246,38 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   if (lanes > 32) v = rows_sum<32>(v);
   return v;
 }
-// Sum over the lanes of a wave that are a multiple of `lanes` apart, known to the first `lanes`.
-__device__ __forceinline__ float heads_sum(float v, int lanes) {
-  if (lanes <= 1) v += moved<0x121>(v);  // a row of 16 turned by 1, 2, 4, 8
+// The same in 64 bits, for the weights' gradients: two values at a time.  Lanes 0 to 31 (STEP 16: the even
+// rows of 16) get a's sum over the partner lanes, the others b's.
+template <int STEP>
+__device__ __forceinline__ double two_sums(double a, double b) {
+  const uint64_t ua = __builtin_bit_cast(uint64_t, a), ub = __builtin_bit_cast(uint64_t, b);
+  uint64_t x = 0, y = 0;
+#pragma unroll
+  for (int k = 0; k < 64; k += 32) {
+    const uint32_t wa = static_cast<uint32_t>(ua >> k), wb = static_cast<uint32_t>(ub >> k);
+    if constexpr (STEP == 16) {
+      const auto r = __builtin_amdgcn_permlane16_swap(wa, wb, false, false);
+      x |= static_cast<uint64_t>(r[0]) << k, y |= static_cast<uint64_t>(r[1]) << k;
+    } else {
+      const auto r = __builtin_amdgcn_permlane32_swap(wa, wb, false, false);
+      x |= static_cast<uint64_t>(r[0]) << k, y |= static_cast<uint64_t>(r[1]) << k;
+    }
+  }
+  return __builtin_bit_cast(double, x) + __builtin_bit_cast(double, y);
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(u), CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(u >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sum over the lanes of a row of 16 that are a multiple of `lanes` apart.
+__device__ __forceinline__ double row_sum(double v, int lanes) {
+  if (lanes <= 1) v += moved<0x121>(v);  // the row turned by 1, 2, 4, 8
   if (lanes <= 2) v += moved<0x122>(v);
   if (lanes <= 4) v += moved<0x124>(v);
   if (lanes <= 8) v += moved<0x128>(v);
-  if (lanes <= 16) v = rows_sum<16>(v);
-  if (lanes <= 32) v = rows_sum<32>(v);
   return v;
 }
 // 1 / sqrt(mean + eps): the hardware's reciprocal root is within a unit in the last place; its
@@ -338,7 +366,12 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(const void *__restrict
   }
 }
 
-// With a norm the waves of large workgroups sum the weights' gradients (few partial sums); without
+// With a norm the waves of large workgroups sum the weights' gradients (few partial sums), in 64 bits: a
+// sum over all tokens and heads in fp32 loses what its terms still hold.  The partial sums of 16
+// workgroups are added by the last of them to finish, the groups' by the last group: a single workgroup
+// would read all of them (512 KB for heads of 128) at one CU's rate (2048 tokens of 64 + 64 heads 57.3 us,
+// 60.7 with one level; 1024 tokens of 32 + 8 heads of 256 22.4 and 30.0).  Two values a lane move
+// (two_sums) instead of one took 333 tokens of 15 + 5 heads of 80 in fp32 from 13.6 to 12.2 us.  Without
 // one nothing is summed, and the kernel is the forward's with the other sign and the v heads, on eight
 // waves a SIMD (62 registers; with 65, and seven, 2048 tokens of 64 + 64 + 64 heads of 128 take 35.3 us
 // instead of 34.3).
@@ -349,7 +382,7 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
                                                           const float *__restrict__ inv_freq,
                                                           const void *__restrict__ qw, const void *__restrict__ kw,
                                                           void *__restrict__ dY, void *__restrict__ dqw, void *__restrict__ dkw,
-                                                          float *__restrict__ part, uint32_t *__restrict__ ticket) {
+                                                          double *__restrict__ part, uint32_t *__restrict__ ticket) {
   constexpr int kW = NORM ? kBwdWaves : kWaves;
   __shared__ float lds[kW][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -360,9 +393,9 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
   B wq, wk;
   wq.load(qw, 0, un, NORM);
   wk.load(kw, 0, un, NORM);
-  float dwq[2 * V], dwk[2 * V];
+  double dwq[2 * V], dwk[2 * V];
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) dwq[e] = dwk[e] = 0.0f;
+  for (int e = 0; e < 2 * V; ++e) dwq[e] = dwk[e] = 0.0;
   const int64_t tasks = s.M * s.split, step = static_cast<int64_t>(gridDim.x) * kW;
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * kW + __builtin_amdgcn_readfirstlane(wave); task < tasks;
        task += step) {
@@ -383,7 +416,7 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
     angles<V>(positions[m], inv_freq, s, lane, u, un.turns, lds[wave], co, si);
     // one round of q or k heads; the gradients of w are summed in dw.  on: this lane has a head (with a
     // zero eps the root of another's zeros is infinite, and its product with them NaN)
-    auto round = [&](B &g, const B &x, const B &weight, float *dw, bool on) __attribute__((always_inline)) {
+    auto round = [&](B &g, const B &x, const B &weight, double *dw, bool on) __attribute__((always_inline)) {
       float v[2 * V];
       g.values(v);
       if (!NORM || un.turns) turn<V, INTER>(v, co, si, -1.0f);
@@ -401,7 +434,7 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
         const float r = on ? inverse_rms(sq, s) : 0.0f, back = r * r * (gx * s.inv_d);
 #pragma unroll
         for (int e = 0; e < 2 * V; ++e) {
-          dw[e] = __builtin_fmaf(v[e] * r, xv[e], dw[e]);
+          dw[e] += static_cast<double>(v[e] * r * xv[e]);
           v[e] = r * (v[e] * w[e] - xv[e] * back);
         }
       }
@@ -428,63 +461,92 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
   if constexpr (NORM) {
 
     // the wave's sums over its heads, then the workgroup's over its waves, in a fixed order
-    __shared__ __attribute__((aligned(16))) float dw[kBwdWaves][2][kQkMaxDim];
+    __shared__ __attribute__((aligned(16))) double dw[kBwdWaves][2][kQkMaxDim];
+    auto put = [&](const double *v, int weight, bool second) {
+      if (second ? un.has1 : un.has0)
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) {
-      dwq[e] = heads_sum(dwq[e], s.lanes);
-      dwk[e] = heads_sum(dwk[e], s.lanes);
-      const int o = e < V ? un.o0 + e : un.o1 + e - V;
-      if (lane < s.lanes && (e < V ? un.has0 : un.has1)) dw[wave][0][o] = dwq[e], dw[wave][1][o] = dwk[e];
-    }
-    __syncthreads();
-    // The workgroup's sums, four columns a thread; agent-coherent (SC1: the L2 of one XCD is not
-    // coherent with the others).
-    const int cols = 2 * s.d, quads = cols / 4;
-    const __amdgpu_buffer_rsrc_t P = make_rsrc(part, gridDim.x * cols * 4u);
-    if (threadIdx.x < quads) {
-      const int i = 4 * threadIdx.x, which = i >= s.d, o = which ? i - s.d : i;
-      f32x4_t v = *reinterpret_cast<const f32x4_t *>(&dw[0][which][o]);
-      for (int k = 1; k < kBwdWaves; ++k) v += *reinterpret_cast<const f32x4_t *>(&dw[k][which][o]);
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (blockIdx.x * cols + i) * 4u, 0, kSC1);
-    }
-    // The last workgroup to leave its sums adds them all.  They have completed before the ticket is
-    // taken, so whoever sees the last ticket sees them.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    __shared__ uint32_t taken;
-    if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (taken != gridDim.x - 1) return;
-    if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // a thread takes four columns of every slices-th workgroup, the slices are added in their order
-    float *sums = &dw[0][0][0];
-    const int slices = kBwdThreads / quads, slice = threadIdx.x / quads, col = 4 * (threadIdx.x - slice * quads);
-    const int parts = static_cast<int>(gridDim.x);
-    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (slice < slices) {
-      for (int k = slice; k < parts; k += kInFlight * slices) {
-        u32x4_t t[kInFlight];
+        for (int e = 0; e < V; ++e) dw[wave][weight][(second ? un.o1 : un.o0) + e] = v[e];
+    };
+    if (s.lanes == 64) {
+      put(dwq, 0, false), put(dwq + V, 0, true), put(dwk, 1, false), put(dwk + V, 1, true);
+    } else {
+      double v[2 * V];  // (lanes 32 on: dkw)
 #pragma unroll
-        for (int e = 0; e < kInFlight; ++e) {
-          const int row = k + e * slices;  // past the last: zeros
-          t[e] = __builtin_amdgcn_raw_buffer_load_b128(P, row < parts ? (row * cols + col) * 4u : kOOB, 0, kSC1);
-        }
+      for (int e = 0; e < 2 * V; ++e) v[e] = two_sums<32>(dwq[e], dwk[e]);
+      if (s.lanes == 32) {
+        put(v, lane / 32, false), put(v + V, lane / 32, true);
+      } else {
 #pragma unroll
-        for (int e = 0; e < kInFlight; ++e) v += __builtin_bit_cast(f32x4_t, t[e]);
+        for (int e = 0; e < V; ++e) v[e] = row_sum(two_sums<16>(v[e], v[V + e]), s.lanes);  // (odd rows: the second chunk)
+        if (lane % 16 < s.lanes) put(v, lane / 32, lane / 16 % 2);
       }
-      *reinterpret_cast<f32x4_t *>(sums + slice * cols + col) = v;
     }
     __syncthreads();
-    const int c = threadIdx.x;
-    if (c >= cols) return;
-    float w = sums[c];
-    for (int k = 1; k < slices; ++k) w += sums[k * cols + c];
-    void *out = pick(c < s.d, dqw, dkw);
-    const int o = c < s.d ? c : c - s.d;
-    if constexpr (T16)
-      static_cast<uint16_t *>(out)[o] = to_bf16(w);
-    else
-      static_cast<float *>(out)[o] = w;
+    // Partial sums leave as rows of `cols`, two columns a thread: those of the workgroups, then those of
+    // groups of kJoin of them; agent-coherent (SC1: the L2 of one XCD is not coherent with the others).
+    const int cols = 2 * s.d, pairs = s.d, first_pair = 2 * static_cast<int>(threadIdx.x);
+    const uint32_t groups = (gridDim.x + kJoin - 1) / kJoin, group = blockIdx.x / kJoin;
+    const __amdgpu_buffer_rsrc_t P = make_rsrc(part, (gridDim.x + groups) * cols * 8u);
+    auto leave = [&](f64x2_t v, uint32_t row) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (row * cols + first_pair) * 8u, 0, kSC1);
+    };
+    // Whether this workgroup is the last of n to leave its sums, which have completed before the ticket
+    // is taken: so whoever takes the last ticket sees them all.
+    __shared__ uint32_t taken;
+    auto last_of = [&](uint32_t *t, uint32_t n) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(t, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      const bool last = taken == n - 1;
+      if (last && threadIdx.x == 0) __hip_atomic_store(t, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      return last;
+    };
+    // The sums of n <= kJoin rows, known to the first `pairs` threads: slices of the workgroup add every
+    // slices-th row each, the slices are added in their order.
+    auto join = [&](uint32_t first, uint32_t n) {
+      double *sums = &dw[0][0][0];
+      const uint32_t slices = kBwdThreads / pairs, slice = threadIdx.x / pairs, col = 2 * (threadIdx.x - slice * pairs);
+      u32x4_t t[kJoinLoads];
+#pragma unroll
+      for (int e = 0; e < kJoinLoads; ++e) {
+        const uint32_t row = slice + e * slices;  // past the last: zeros
+        t[e] = __builtin_amdgcn_raw_buffer_load_b128(
+            P, slice < slices && row < n ? ((first + row) * cols + col) * 8u : kOOB, 0, kSC1);
+      }
+      f64x2_t v = {0.0, 0.0};
+#pragma unroll
+      for (int e = 0; e < kJoinLoads; ++e) v += __builtin_bit_cast(f64x2_t, t[e]);
+      if (slice < slices) *reinterpret_cast<f64x2_t *>(sums + slice * cols + col) = v;
+      __syncthreads();
+      if (threadIdx.x < pairs) {
+        v = *reinterpret_cast<const f64x2_t *>(sums + first_pair);
+        for (uint32_t k = 1; k < min(slices, n); ++k) v += *reinterpret_cast<const f64x2_t *>(sums + k * cols + first_pair);
+      }
+      return v;
+    };
+    const int which = first_pair >= s.d, o = which ? first_pair - s.d : first_pair;
+    if (threadIdx.x < pairs) {
+      f64x2_t v = *reinterpret_cast<const f64x2_t *>(&dw[0][which][o]);
+      for (int k = 1; k < kBwdWaves; ++k) v += *reinterpret_cast<const f64x2_t *>(&dw[k][which][o]);
+      leave(v, blockIdx.x);
+    }
+    const uint32_t members = min(gridDim.x - group * kJoin, static_cast<uint32_t>(kJoin));
+    if (!last_of(ticket + 1 + group, members)) return;
+    f64x2_t v = join(group * kJoin, members);
+    if (groups > 1) {
+      if (threadIdx.x < pairs) leave(v, gridDim.x + group);
+      if (!last_of(ticket, groups)) return;
+      v = join(gridDim.x, groups);
+    }
+    if (threadIdx.x < pairs) {
+      const float a = static_cast<float>(v[0]), b = static_cast<float>(v[1]);
+      void *out = pick(which != 0, dkw, dqw);
+      if constexpr (T16)
+        static_cast<uint32_t *>(out)[o / 2] = pack_bf16x2(a, b);
+      else
+        static_cast<f32x2_t *>(out)[o / 2] = f32x2_t{a, b};
+    }
   }
 }
 
@@ -521,13 +583,15 @@ int64_t workgroups(const QkShape &s, int waves, int64_t most) {
 }
 // The backward's workgroups each leave partial sums, so no more than are on the card at once.
 constexpr int64_t kFwdWorkgroups = 256 * 16, kBwdWorkgroups = 256;
+static_assert(kBwdWorkgroups <= kJoin * kJoin, "two levels join them all");
 
 }  // namespace
 
 size_t qk_bwd_workspace(QkShape s, bool t16, bool norm) {
   if (!norm) return 0;
   plan(&s, chunk_of(s, t16, true), true, true);
-  return static_cast<size_t>(workgroups(s, kBwdWaves, kBwdWorkgroups)) * 2 * s.d * sizeof(float);
+  const int64_t wgs = workgroups(s, kBwdWaves, kBwdWorkgroups);
+  return static_cast<size_t>(wgs + (wgs + kJoin - 1) / kJoin) * 2 * s.d * sizeof(double);
 }
 
 hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
@@ -560,7 +624,7 @@ hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, c
 
 hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const void *Y, QkShape s, bool t16,
                          bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
-                         const void *kw, void *dY, void *dqw, void *dkw, float *part, uint32_t *ticket,
+                         const void *kw, void *dY, void *dqw, void *dkw, double *part, uint32_t *ticket,
                          hipStream_t stream) {
   const bool norm = qw != nullptr;
   const int v = chunk_of(s, t16, norm);

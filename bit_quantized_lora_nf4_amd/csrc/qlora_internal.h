@@ -312,12 +312,12 @@ struct QkShape {
 // t16: bf16 tensors, else fp32; qw, kw NULL: no norm (Y is not read then by the backward).
 hipError_t launch_qk_fwd(const void *Y, QkShape s, bool t16, bool interleaved, const int64_t *positions,
                          const float *inv_freq, const void *qw, const void *kw, void *Q, void *K, hipStream_t stream);
-// Norm only: `part`, qk_bwd_workspace bytes of partial sums of dqw and dkw, and `ticket`, a word that
-// is zero when the call starts and when it has run.
+// Norm only: `part`, qk_bwd_workspace bytes of partial sums of dqw and dkw, and `ticket`, 17 words that
+// are zero when the call starts and when it has run.
 size_t qk_bwd_workspace(QkShape s, bool t16, bool norm);
 hipError_t launch_qk_bwd(const void *dQ, const void *dK, const void *dV, const void *Y, QkShape s, bool t16,
                          bool interleaved, const int64_t *positions, const float *inv_freq, const void *qw,
-                         const void *kw, void *dY, void *dqw, void *dkw, float *part, uint32_t *ticket,
+                         const void *kw, void *dY, void *dqw, void *dkw, double *part, uint32_t *ticket,
                          hipStream_t stream);
 
 }  // namespace qlora

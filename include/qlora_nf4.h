@@ -24,7 +24,7 @@
  *     fixed scratch array of the library instead).
  *   - Workspaces: the first QLORA_WORKSPACE_HEADER_BYTES bytes of every
  *     workspace hold counters and flags that the small-M forward's workgroups
- *     use to hand U_s to each other, and the ticket of qlora_qk_bwd.  They must
+ *     use to hand U_s to each other, and the tickets of qlora_qk_bwd.  They must
  *     be zero when a workspace is first used (clear it once after allocating);
  *     every call leaves them zero, and no other call writes them, so one
  *     workspace can serve calls of any shape.  Calls that share a workspace
@@ -462,7 +462,7 @@ int qlora_qk_fwd(const qlora_qk_shape *shape, const void *Y, const int64_t *posi
 
 /* Backward of qlora_qk_fwd: dY [M, (nq + 2 nk) d] from dQ, dK, and dV [M, nk, d] (copied into
  * the value heads' place), so that dY is whole for the projections' backward.  With weights
- * also dqw, dkw [d], summed in fp32 in a fixed order, Y (the forward's rows) is required and
+ * also dqw, dkw [d], terms in fp32 summed in 64 bits in a fixed order, Y (the forward's rows) is required and
  * qlora_workspace_bytes_qk bytes of workspace (its header as for every workspace); without them
  * Y, dqw, dkw and the workspace are not used and may be NULL. */
 size_t qlora_workspace_bytes_qk(const qlora_qk_shape *shape, int norm);

@@ -1,6 +1,7 @@
 """Norms of query / key heads with the rotation on the GPU, where single values decide: a zero eps with
 head counts that leave a wave's round partly filled; elements past the rotated ones beside
-infinities, NaN and signed zeros; sines and cosines to half a step."""
+infinities, NaN and signed zeros; sines and cosines to half a step; the weights' gradients
+summed in 64 bits."""
 
 import numpy as np
 import pytest
@@ -154,3 +155,46 @@ def test_sines_and_cosines(q, far, base, inter):  # noqa: F811
         for got, want in ((z[:, i], co), (z[:, j], sign * si)):
             tol = 2.0 ** -24 * np.abs(want) + slack
             assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+
+
+# ---- sums of the weights' gradients ------------------------------------------------------
+
+@pytest.mark.parametrize("M,nq,nk,d", [(333, 15, 5, 64), (1000, 8, 2, 128), (20011, 2, 1, 32), (37, 3, 1, 256)])
+def test_weight_gradients_are_summed_in_64_bits(q, M, nq, nk, d):  # noqa: F811
+    """Rows of +-1 have the root mean square 1 exactly, so a term is dn x, exact, times 1 / rms (within
+    one step, 2^-23, the same for all).  The sum then is the definition's to that, half a step
+    of fp32, and one rounding of 64 bits a term."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    Y = torch.randint(0, 2, (M, (nq + 2 * nk) * d), device="cuda", generator=gen).float() * 2 - 1
+    g = [torch.randn((M, n, d), device="cuda", generator=gen) for n in (nq, nk, nk)]
+    w = torch.ones(d, device="cuda")
+    pos, f = torch.zeros(M, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    got = q.qk_norm_rope_bwd(*g, pos, f, Y, w, w, eps=0.0)[1:]
+    x = Y.double().cpu().numpy().reshape(M, -1, d)
+    for z, dz, first, n in ((got[0], g[0], 0, nq), (got[1], g[1], nq, nk)):
+        term = dz.double().cpu().numpy() * x[:, first:first + n]
+        want, mag = term.sum((0, 1)), np.abs(term).sum((0, 1))
+        err = np.abs(z.double().cpu().numpy() - want)
+        tol = (2.0 ** -24 + 2.0 ** -23) * np.abs(want) + (M * n + 64) * 2.0 ** -53 * mag
+        assert np.all(err <= tol), float(np.max(err / tol))
+
+
+@pytest.mark.parametrize("M,nq,nk,d", [(1, 1, 1, 4), (100, 4, 2, 128), (700, 4, 4, 96), (4097, 8, 2, 256)])
+def test_tickets_are_left_zero_and_the_sums_repeat(q, M, nq, nk, d):  # noqa: F811
+    """One workgroup, one group of them, a part of the groups and all: every call leaves the workspace's
+    header zero and gives the same bits, whatever the partial sums' place held."""
+    import torch
+    c = Case(M, nq, nk, d, d, True, False, False)
+    need = q.qlora_workspace_bytes_qk(q._lib.qlora_qk_shape(M, nq, nk, d, d, 0, 0, tq.EPS), 1)
+    want = None
+    for fill in (0, 255, 1):
+        ws = torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda")
+        ws[:q._lib.QLORA_WORKSPACE_HEADER_BYTES].zero_()
+        for _ in range(3):
+            got = c.bwd(q, ws=ws[:need])
+            want = want or got
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+        assert not bool(ws[:q._lib.QLORA_WORKSPACE_HEADER_BYTES].any()) and bool((ws[need:] == fill).all())
+    c.check_bwd(want)
