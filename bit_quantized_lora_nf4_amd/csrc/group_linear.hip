@@ -10,7 +10,8 @@
 // all rows of the tile.  That difference is of sums at most a few times larger than the
 // result's terms, so it costs two bits of the fp32 sums.  It does not hold when x is infinite
 // or so large that a sum overflows; a wave whose result is not finite computes its part again
-// from the integers q - z themselves (never taken on ordinary data).
+// from the integers 2^-16 (q - z) themselves, whose sums with finite x stay in range whatever x, and
+// s takes the 2^16 back (never taken on ordinary data).
 //
 // A workgroup owns 16 NT rows.  Its waves split K: each takes every W-th round of 512 columns
 // (four blocks of 128), and their fp32 sums are added in wave order through LDS.  A lane
@@ -60,11 +61,15 @@ __device__ __forceinline__ u32x4_t offset_codes(uint32_t c, const CodeBits &k) {
   return u32x4_t{((c << 3) & k.mask) | k.base, ((c >> 1) & k.mask) | k.base, ((c >> 5) & k.mask) | k.base,
                  ((c >> 9) & k.mask) | k.base};
 }
+// Times 2^-16, which is exact (|q - z| < 2^8): a group's sum of up to 128 products with the largest x stays
+// in range.
+constexpr float kPlain = 0x1p-16f;
 __device__ __forceinline__ u32x4_t plain_codes(uint32_t c, float z) {
   u32x4_t r;
 #pragma unroll
   for (int p = 0; p < 4; ++p)
-    r[p] = pack_bf16x2(static_cast<float>((c >> (4 * p)) & 15u) - z, static_cast<float>((c >> (4 * p + 16)) & 15u) - z);
+    r[p] = pack_bf16x2((static_cast<float>((c >> (4 * p)) & 15u) - z) * kPlain,
+                       (static_cast<float>((c >> (4 * p + 16)) & 15u) - z) * kPlain);
   return r;
 }
 // Eight consecutive values of X in the codes' order.
@@ -279,12 +284,15 @@ struct Product {
       if ((j + 1) % (kFlush / 32) == 0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float off = -16.0f - v.zero(t, k), s = v.scale(t, k);
+          const float off = -16.0f - v.zero(t, k);
+          float s = v.scale(t, k), back = 1.0f;
+          // plain_codes' 2^16 goes to the scale, or to the sum of a scale that it would take out of range
+          if constexpr (EXACT) (fabsf(s) < 0x1p100f ? s : back) *= 1.0f / kPlain;
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float u = EXACT ? a.acc[m][t][i] : __builtin_fmaf(off, a.sum[m][i], a.acc[m][t][i]);
+              const float u = EXACT ? a.acc[m][t][i] * back : __builtin_fmaf(off, a.sum[m][i], a.acc[m][t][i]);
               y[m][t][i] = __builtin_fmaf(s, u, y[m][t][i]);
             }
         }
