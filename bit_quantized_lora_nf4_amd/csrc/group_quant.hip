@@ -177,18 +177,17 @@ __global__ __launch_bounds__(kThreads) void group_quantize_any_kernel(const void
 }
 
 // A wave takes spans of kUnroll x 64 chunks of one row (V codes and 16 bytes of output a
-// lane), so the group of a chunk is a 32-bit division by the group's chunks, done by a
-// multiplication (exact for the row lengths that the caller allows).  The output is stored past the
+// lane), so the group of a chunk is a 32-bit division by the group's chunks (four at least), done
+// by a multiplication (exact for the row lengths that the caller allows).  The output is stored past the
 // caches, which hold the codes (11008 x 4096 bf16: 16.1 us, 19.9 through them; 22016 x 8192 fp32: 120
 // us, 6.7 TB/s, and 179).
 template <bool O16>
 __global__ __launch_bounds__(kThreads) void group_dequantize_kernel(GroupView w, uint32_t row_chunks, uint32_t spans,
-                                                                    uint32_t per_group, uint32_t magic,
+                                                                    uint32_t row_groups, uint32_t magic,
                                                                     void *__restrict__ out) {
   constexpr int V = O16 ? 8 : 4;
   const uint32_t lane = threadIdx.x & 63;
   const int64_t total = w.n_rows * spans, step = static_cast<int64_t>(gridDim.x) * (kThreads / 64);
-  const uint32_t row_groups = row_chunks / per_group;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6); i < total; i += step) {
     const int64_t row = i / spans;
     const uint32_t c0 = static_cast<uint32_t>(i - row * spans) * (kUnroll * 64) + lane;
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void group_dequantize_kernel(GroupView w,
         code[u] = reinterpret_cast<const uint32_t *>(w.codes)[chunk0 + c];
       else
         code[u] = reinterpret_cast<const uint16_t *>(w.codes)[chunk0 + c];
-      const int64_t g = group0 + (per_group == 1 ? c : __umulhi(c, magic));
+      const int64_t g = group0 + __umulhi(c, magic);
       s[u] = w.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t *>(w.scales)[g])
                           : static_cast<const float *>(w.scales)[g];
       z[u] = w.zeros ? static_cast<float>(w.zeros[g]) : 8.0f;
@@ -282,11 +281,11 @@ hipError_t launch_group_dequantize(const GroupView &w, void *out, bool out_bf16,
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   const uint32_t magic = group_magic(per_group);
   if (out_bf16)
-    hipLaunchKernelGGL(group_dequantize_kernel<true>, grid, block, 0, stream, w, row_chunks, spans, per_group, magic,
-                       out);
+    hipLaunchKernelGGL(group_dequantize_kernel<true>, grid, block, 0, stream, w, row_chunks, spans, row_chunks / per_group,
+                       magic, out);
   else
-    hipLaunchKernelGGL(group_dequantize_kernel<false>, grid, block, 0, stream, w, row_chunks, spans, per_group, magic,
-                       out);
+    hipLaunchKernelGGL(group_dequantize_kernel<false>, grid, block, 0, stream, w, row_chunks, spans, row_chunks / per_group,
+                       magic, out);
   return hipGetLastError();
 }
 
