@@ -467,10 +467,10 @@ __global__ __launch_bounds__(64 * W) void group_many_kernel(GroupView w, const u
 template <bool FEW, int XR, int NT, int W>
 hipError_t go(const GroupView &w, const uint16_t *X, int64_t M, uint16_t *Y, hipStream_t stream) {
   const int64_t gx = (w.n_rows + 16 * NT - 1) / (16 * NT), gy = (M + XR - 1) / XR;
-  if (gx > 0x7fffffff || gy > 0xffff) return hipErrorInvalidValue;
   // as many waves as share the rounds evenly
   const int64_t rounds = (w.n_cols + 511) / 512, each = (rounds + W - 1) / W;
   const int waves = static_cast<int>((rounds + each - 1) / each);
+  if (gx * 64 * waves > kMaxThreads || gy > 0xffff) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * waves);
   static_assert(!FEW || W * XR <= 64, "64 KB of dynamic LDS");
   const size_t lds = FEW ? static_cast<size_t>(waves) * XR * 1024 : 0;  // (holds the partial sums too)

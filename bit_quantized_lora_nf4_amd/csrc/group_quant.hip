@@ -234,7 +234,7 @@ hipError_t quantize_go(const void *W, int64_t n, int64_t group, void *codes, voi
   const int64_t chunks = n / V, per_group = group / V;
   if (per_group <= 64 && (per_group & (per_group - 1)) == 0) {
     const int64_t blocks = (chunks + kThreads * kEach - 1) / (kThreads * kEach);
-    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    if (blocks * kThreads > kMaxThreads) return hipErrorInvalidValue;
     int shift = 0;
     while ((int64_t(1) << shift) < per_group) ++shift;
     const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);

@@ -290,6 +290,8 @@ constexpr int64_t kGroupMaxCols = int64_t(1) << 18;
 inline uint32_t group_magic(uint32_t d) {
   return d < 2 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d);
 }
+// Threads of a launch along one axis: counted in 32 bits.
+constexpr int64_t kMaxThreads = 0xffffffff;
 hipError_t launch_group_quantize(const void *W, bool w_bf16, int64_t n_rows, int64_t n_cols, int64_t group,
                                  bool scale_bf16, uint8_t *codes, void *scales, uint8_t *zeros, hipStream_t stream);
 hipError_t launch_group_dequantize(const GroupView &w, void *out, bool out_bf16, hipStream_t stream);

@@ -64,3 +64,16 @@ def test_scales_beyond_the_range_of_a_scaled_one(q, M):  # noqa: F811
     Y = gc.host_f32_from_bf16(q.group_linear_fwd(gw, gc.dev_bf16(xb))).reshape(M, N)
     assert not np.isfinite(Y[0]).any()
     assert np.all(np.abs(Y - want)[1:] <= _bound(want, mag, K, group)[1:])
+
+
+def test_launches_of_too_many_threads_are_refused(q):  # noqa: F811
+    """Sizes whose launch would pass 2^32 threads along an axis stop on the host (the addresses are not
+    used), and the next call runs."""
+    import torch
+    fake = 0x10000
+    lib = q._lib
+    assert lib.qlora_group_quantize(fake, 1, 1 << 19, 1 << 18, 128, 1, fake, fake, None, None) == lib.QLORA_ERR_LAUNCH
+    w = lib.qlora_group_weight(fake, fake, None, 1 << 31, 32, 32, 1)
+    assert lib.qlora_group_linear_fwd(w, fake, 1, fake, None) == lib.QLORA_ERR_LAUNCH
+    _, _, _, gw = _weight(q, 8, 64, 32, False, True)
+    assert q.group_linear_fwd(gw, torch.ones((1, 64), dtype=torch.bfloat16, device="cuda")).isfinite().all()
