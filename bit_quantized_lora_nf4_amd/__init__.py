@@ -24,7 +24,8 @@ Gated feed-forward projections (``qw``: gate rows, then up rows; A [2 r, K], B [
     dX, dA, dB = gated_bwd(qw, dH, Y, X, A, B, alpha, U)
 
 Serving a merged weight in 4-bit integers with group scales, and what follows the query, key
-and value projections (also in training; the backward's dY goes to ``linear_bwd_fused``):
+and value projections (also in training; the backward's dY goes to ``linear_bwd_fused``, or to
+``linear_bwd`` where one linear holds the stacked rows, as grouped heads need):
 
     gw = group_quantize(lora_merge(qw, A, B, alpha), 128)
     Y = group_linear_fwd(gw, X)                        # few tokens: a decode step's batch
@@ -876,8 +877,9 @@ def _qk_fits(dtype, device, M, d, positions, inv_freq, q_weight, k_weight):
 
 def qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, Q=None, K=None):
-    """Queries and keys from the rows Y [M, (n_heads + 2 n_kv_heads) d] of a fused projection
-    (q heads, k heads, v heads): each head divided by its root mean square (eps inside the
+    """Queries and keys from the rows Y [M, (n_heads + 2 n_kv_heads) d] of one projection over the
+    stacked weights (q heads, k heads, v heads; ``linear_fwd`` or ``group_linear_fwd`` on the stacked
+    rows, and with n_heads = n_kv_heads ``linear_fwd_fused``): each head divided by its root mean square (eps inside the
     root) and multiplied by q_weight or k_weight [d] (both None: no norm), then its first
     2 len(inv_freq) elements turned by positions [M] (int64) times inv_freq (fp32): element i
     with i + len(inv_freq), or ``interleaved`` 2 i with 2 i + 1.  bf16 or fp32.  Returns Q [M,

@@ -439,16 +439,22 @@ int qlora_group_dequantize(const qlora_group_weight *w, void *out, int out_dtype
 int qlora_group_linear_fwd(const qlora_group_weight *w, const uint16_t *X, int64_t M, uint16_t *Y, void *stream);
 
 /* ---- norms of queries and keys with the position rotation --------------------------
- * Rows Y [M, (nq + 2 nk) d] as a fused projection writes them: nq query heads, nk key heads,
- * nk value heads of d elements.  For every query and key head x of the token at position p:
+ * Rows Y [M, (nq + 2 nk) d] as one projection over stacked weights writes them: nq query heads,
+ * nk key heads, nk value heads of d elements.  qlora_linear_fwd and qlora_group_linear_fwd on the
+ * stacked rows of the three weights do so for any nq and nk (in training with one adapter over all
+ * rows); qlora_linear_fwd_fused, whose parts have one height and an adapter each, for nq = nk alone.
+ * Outputs of three separate projections have to be copied side by side.
+ * For every query and key head x of the token at position p:
  *   n = x / sqrt(mean x^2 + eps) * w        (w = q_weight or k_weight [d]; both NULL: n = x)
  *   pair i < rot / 2 of its first rot elements, (a, b), turns by t = p * inv_freq[i]:
  *     (a cos t - b sin t, b cos t + a sin t)
  *   interleaved = 0: pair i is (i, i + rot / 2); 1: (2 i, 2 i + 1).  Elements past rot are n.
  * dtype QLORA_BF16 or QLORA_F32 is that of all tensors but positions (int64 [M], any sign) and
- * inv_freq (fp32 [rot / 2]).  The angle is formed and reduced in 64 bits, the rest in fp32 with
- * one rounding at the end.  1 <= nq, nk; d a multiple of 4, at most 256; rot a multiple of 4,
- * 0 <= rot <= d (0: the norm alone).
+ * inv_freq (fp32 [rot / 2]).  The angle, its sine and cosine are formed in 64 bits and rounded to
+ * fp32, the rest is in fp32 with one rounding at the end.  So is the sum of squares: elements past 2^60
+ * can make it infinite (n is 0 then), and where eps is next to nothing a head whose elements all are
+ * below 2^-63 loses bits of it.
+ * 1 <= nq, nk; d a multiple of 4, at most 256; rot a multiple of 4, 0 <= rot <= d (0: the norm alone).
  *   Q [M, nq, d], K [M, nk, d]; the value heads stay where they are. */
 typedef struct {
   int64_t M;
@@ -461,7 +467,7 @@ int qlora_qk_fwd(const qlora_qk_shape *shape, const void *Y, const int64_t *posi
                  const void *q_weight, const void *k_weight, void *Q, void *K, void *stream);
 
 /* Backward of qlora_qk_fwd: dY [M, (nq + 2 nk) d] from dQ, dK, and dV [M, nk, d] (copied into
- * the value heads' place), so that dY is whole for the projections' backward.  With weights
+ * the value heads' place), so that dY is whole for the backward of the projection that wrote Y.  With weights
  * also dqw, dkw [d], terms in fp32 summed in 64 bits in a fixed order, Y (the forward's rows) is required and
  * qlora_workspace_bytes_qk bytes of workspace (its header as for every workspace); without them
  * Y, dqw, dkw and the workspace are not used and may be NULL. */
