@@ -822,7 +822,8 @@ def group_dequantize(gw, dtype=None, out=None):
 
 def group_linear_fwd(gw, X, Y=None):
     """Y [M, n_rows] = bf16(X W^T) for X [M, n_cols] bf16 and a GroupWeight: made for few
-    tokens (the weight is read once for up to 64 of them, and again for every 64 more)."""
+    tokens (the weight is read once for up to 8 of them, then once for each tile of 16, 32 or 64,
+    whichever the row count makes cheapest)."""
     torch = _torch()
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError(f"X must be 2-D [M, {gw.n_cols}]")

@@ -7,8 +7,10 @@
 // a shift and an and-or, 16 + q (the bf16 of exponent 4 counts in eighths, so q is the
 // mantissa's upper four bits); the sum of (16 + q) x exceeds that of (q - z) x by
 // (16 + z) sum x, and sum x comes from one more matrix instruction against ones, shared by
-// all rows of the tile.  That difference is of sums at most a few times larger than the
-// result's terms, so it costs two bits of the fp32 sums.  It does not hold when x is infinite
+// all rows of the tile.  The terms of those sums are (16 + q) |x| and (16 + z) |x| where the
+// result's are |q - z| |x|: with zeros up to 15 at most 31 times as large each (codes spread over 0 to 15
+// about a zero of 8: six times on average), so the difference costs up to five bits of the fp32
+// sums of terms next to the zero; zeros above 15, up to 255, cost more.  It does not hold when x is infinite
 // or so large that a sum overflows; a wave whose result is not finite computes its part again
 // from the integers 2^-16 (q - z) themselves, whose sums with finite x stay in range whatever x, and
 // s takes the 2^16 back (never taken on ordinary data).

@@ -431,10 +431,11 @@ int qlora_group_quantize(const void *W, int w_dtype, int64_t n_rows, int64_t n_c
 int qlora_group_dequantize(const qlora_group_weight *w, void *out, int out_dtype, void *stream);
 
 /* Y[M, N] = bf16(X . W^T): X bf16 [M, K], fp32 sums, the weight's values never rounded.  Made
- * for few tokens (a decode step's batch): up to 64 tokens the weight is read once, more run in
- * tiles of 64 tokens that each read it again.  M <= 2^20.  The sums of a group are formed as
- * sum (16 + code) x - (16 + zero) sum x, so a value's error is that of fp32 sums of terms of up
- * to 31 |x| s.  Infinite and NaN inputs give what the definition gives.  No workspace; calls may
+ * for few tokens (a decode step's batch): up to 8 tokens the weight is read once, more run in tiles of
+ * 16, 32 or 64 tokens, whichever the row count makes cheapest, and each tile reads it.  M <= 2^20.  The
+ * sums of a group are formed as sum (16 + code) x - (16 + zero) sum x, so a value's error is that of
+ * fp32 sums of the terms (16 + code) |x| s and (16 + zero) |x| s: up to 31 |x| s each with zeros up to
+ * 15, up to 271 |x| s with larger ones, where the result's own terms are |code - zero| |x| s.  Infinite and NaN inputs give what the definition gives.  No workspace; calls may
  * overlap on any streams. */
 int qlora_group_linear_fwd(const qlora_group_weight *w, const uint16_t *X, int64_t M, uint16_t *Y, void *stream);
 
