@@ -553,7 +553,7 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
 // Elements of a lane's chunk: the widest access that divides the head and half the rotated part, of
 // up to 16 bytes.  The backward with a norm (sums) stops at 8 bytes (4 of bf16): with 16 a lane holds
 // twice the values and half as many waves fit (2048 tokens of 64 + 64 + 64 heads of 128: 50.5 us with
-// 8 bytes, 59.4 with 16; forward 28.0 and 24.5).
+// 8 bytes, 59.4 with 16, the sums in fp32 as they were then; forward 28.0 and 24.5).
 int chunk_of(const QkShape &s, bool t16, bool sums) {
   int v = t16 && !sums ? 8 : 4;
   while (v > 2 && (s.d % v != 0 || s.rot % (2 * v) != 0)) v /= 2;

@@ -435,8 +435,9 @@ int qlora_group_dequantize(const qlora_group_weight *w, void *out, int out_dtype
  * 16, 32 or 64 tokens, whichever the row count makes cheapest, and each tile reads it.  M <= 2^20.  The
  * sums of a group are formed as sum (16 + code) x - (16 + zero) sum x, so a value's error is that of
  * fp32 sums of the terms (16 + code) |x| s and (16 + zero) |x| s: up to 31 |x| s each with zeros up to
- * 15, up to 271 |x| s with larger ones, where the result's own terms are |code - zero| |x| s.  Infinite and NaN inputs give what the definition gives.  No workspace; calls may
- * overlap on any streams. */
+ * 15, up to 271 |x| s with larger ones, where the result's own terms are |code - zero| |x| s.
+ * Infinite and NaN inputs give what the definition gives.  No workspace; calls may overlap on any
+ * streams. */
 int qlora_group_linear_fwd(const qlora_group_weight *w, const uint16_t *X, int64_t M, uint16_t *Y, void *stream);
 
 /* ---- norms of queries and keys with the position rotation --------------------------
