@@ -880,8 +880,8 @@ def qk_norm_rope_fwd(Y, positions, inv_freq, n_heads, n_kv_heads, q_weight=None,
                      interleaved=False, Q=None, K=None):
     """Queries and keys from the rows Y [M, (n_heads + 2 n_kv_heads) d] of one projection over the
     stacked weights (q heads, k heads, v heads; ``linear_fwd`` or ``group_linear_fwd`` on the stacked
-    rows, and with n_heads = n_kv_heads ``linear_fwd_fused``): each head divided by its root mean square (eps inside the
-    root) and multiplied by q_weight or k_weight [d] (both None: no norm), then its first
+    rows, and with n_heads = n_kv_heads ``linear_fwd_fused``): each head divided by its root mean
+    square (eps inside the root) and multiplied by q_weight or k_weight [d] (both None: no norm), then its first
     2 len(inv_freq) elements turned by positions [M] (int64) times inv_freq (fp32): element i
     with i + len(inv_freq), or ``interleaved`` 2 i with 2 i + 1.  bf16 or fp32.  Returns Q [M,
     n_heads, d] and K [M, n_kv_heads, d]; the value heads are Y's last n_kv_heads * d columns."""

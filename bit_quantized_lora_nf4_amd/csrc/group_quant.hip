@@ -281,11 +281,11 @@ hipError_t launch_group_dequantize(const GroupView &w, void *out, bool out_bf16,
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   const uint32_t magic = group_magic(per_group);
   if (out_bf16)
-    hipLaunchKernelGGL(group_dequantize_kernel<true>, grid, block, 0, stream, w, row_chunks, spans, row_chunks / per_group,
-                       magic, out);
+    hipLaunchKernelGGL(group_dequantize_kernel<true>, grid, block, 0, stream, w, row_chunks, spans,
+                       row_chunks / per_group, magic, out);
   else
-    hipLaunchKernelGGL(group_dequantize_kernel<false>, grid, block, 0, stream, w, row_chunks, spans, row_chunks / per_group,
-                       magic, out);
+    hipLaunchKernelGGL(group_dequantize_kernel<false>, grid, block, 0, stream, w, row_chunks, spans,
+                       row_chunks / per_group, magic, out);
   return hipGetLastError();
 }
 

@@ -154,8 +154,8 @@ __device__ __forceinline__ double one_over() {
 // Sine and cosine of an angle given in turns, all in 64 bits and each rounded once: within half a step of
 // fp32, also at far positions.  The angle is reduced to an eighth of a turn on either side of a quarter's
 // multiple (1.5 x 2^52 added leaves the multiple in the sum's last bits), where the power series to
-// x^11 and x^12 are off by less than 2^-36.  (An angle
-// rounded to fp32 before its sine is taken leaves a cosine off by up to 1.1e-7, its rounding alone by 3.0e-8.)
+// x^11 and x^12 are off by less than 2^-36.  (An angle rounded to fp32 before its sine is taken leaves a
+// cosine off by up to 1.1e-7, the cosine's own rounding by 3.0e-8.)
 __device__ __forceinline__ void sine_cosine(double turn, float &sn, float &cs) {
   const double t = turn - __builtin_rint(turn);
   const double k = __builtin_fma(4.0, t, 0x1.8p52);
@@ -477,7 +477,8 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
         put(v, lane / 32, false), put(v + V, lane / 32, true);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = row_sum(two_sums<16>(v[e], v[V + e]), s.lanes);  // (odd rows: the second chunk)
+        for (int e = 0; e < V; ++e)  // (odd rows of 16 lanes: the second chunk)
+          v[e] = row_sum(two_sums<16>(v[e], v[V + e]), s.lanes);
         if (lane % 16 < s.lanes) put(v, lane / 32, lane / 16 % 2);
       }
     }
@@ -488,7 +489,8 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
     const uint32_t groups = (gridDim.x + kJoin - 1) / kJoin, group = blockIdx.x / kJoin;
     const __amdgpu_buffer_rsrc_t P = make_rsrc(part, (gridDim.x + groups) * cols * 8u);
     auto leave = [&](f64x2_t v, uint32_t row) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, (row * cols + first_pair) * 8u, 0, kSC1);
+      const uint32_t at = (row * cols + first_pair) * 8u;
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), P, at, 0, kSC1);
     };
     // Whether this workgroup is the last of n to leave its sums, which have completed before the ticket
     // is taken: so whoever takes the last ticket sees them all.
@@ -521,7 +523,8 @@ __global__ __launch_bounds__(NORM ? kBwdThreads : kThreads, NORM ? 4 : 8) void q
       __syncthreads();
       if (threadIdx.x < pairs) {
         v = *reinterpret_cast<const f64x2_t *>(sums + first_pair);
-        for (uint32_t k = 1; k < min(slices, n); ++k) v += *reinterpret_cast<const f64x2_t *>(sums + k * cols + first_pair);
+        for (uint32_t k = 1; k < min(slices, n); ++k)
+          v += *reinterpret_cast<const f64x2_t *>(sums + k * cols + first_pair);
       }
       return v;
     };

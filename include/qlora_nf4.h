@@ -469,10 +469,10 @@ int qlora_qk_fwd(const qlora_qk_shape *shape, const void *Y, const int64_t *posi
                  const void *q_weight, const void *k_weight, void *Q, void *K, void *stream);
 
 /* Backward of qlora_qk_fwd: dY [M, (nq + 2 nk) d] from dQ, dK, and dV [M, nk, d] (copied into
- * the value heads' place), so that dY is whole for the backward of the projection that wrote Y.  With weights
- * also dqw, dkw [d], terms in fp32 summed in 64 bits in a fixed order, Y (the forward's rows) is required and
- * qlora_workspace_bytes_qk bytes of workspace (its header as for every workspace); without them
- * Y, dqw, dkw and the workspace are not used and may be NULL. */
+ * the value heads' place), so that dY is whole for the backward of the projection that wrote Y.
+ * With weights also dqw, dkw [d], terms in fp32 summed in 64 bits in a fixed order; Y (the forward's
+ * rows) is required then, and qlora_workspace_bytes_qk bytes of workspace (its header as for every
+ * workspace).  Without weights Y, dqw, dkw and the workspace are not used and may be NULL. */
 size_t qlora_workspace_bytes_qk(const qlora_qk_shape *shape, int norm);
 int qlora_qk_bwd(const qlora_qk_shape *shape, const void *dQ, const void *dK, const void *dV, const void *Y,
                  const int64_t *positions, const float *inv_freq, const void *q_weight, const void *k_weight, void *dY,
